@@ -68,7 +68,7 @@ extern "C" {
 /* A CUDA stream (cudaStream_t); NULL means the legacy default stream. */
 typedef struct CUstream_st *sv_stream_t;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype; /* SV_F16: paged caches only */
 
 enum {
   SV_OK = 0,
@@ -90,13 +90,19 @@ enum {
   SV_STATUS_NONFINITE_ROW = 16u,  /* a row whose maximum is not finite (among the rows the
                                      call reads: see spec_verify_set_lazy) */
   SV_STATUS_INTERNAL = 32u,       /* an inverse-CDF draw found no token (never expected) */
-  SV_STATUS_TIMEOUT = 64u         /* a bounded wait for a request's decision ran out; the
+  SV_STATUS_TIMEOUT = 64u,        /* a bounded wait for a request's decision ran out; the
                                      request's outputs are incomplete and the workspace must
                                      be zero-filled again before reuse */
+  SV_STATUS_BAD_PROB = 128u,      /* a probability outside [0, 1] or NaN: counted as 0 (above 1:
+                                     as 1); or a row that sums to 0, or to 128 or more */
+  SV_STATUS_BAD_PAGE = 256u,      /* a page number outside the pool: not written, read as zeros */
+  SV_STATUS_BAD_LENGTH = 512u     /* kv_len negative, or a step past the request's page table:
+                                     that row or request is left out */
 };
 
 #define SV_MAX_GAMMA 31
 #define SV_MAX_VOCAB (1 << 24)
+#define SV_MAX_HEAD_DIM 128
 /* Size of the scratch array built into the library for spec_verify_sample_noalloc. */
 #define SV_NOALLOC_SCRATCH_BYTES (4u << 20)
 
@@ -194,6 +200,151 @@ int spec_verify_greedy_packed(const void *target_logits, sv_dtype dtype, int B, 
 int spec_verify_draw(const void *logits, sv_dtype dtype, int B, int V, const float *uniforms,
                      const float *temperature, int32_t *tokens, void *workspace,
                      size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * Verification against probabilities: the steps at the top of this file from step
+ * 2 on, where the caller holds p and q instead of logits.  A sampler that filters
+ * (top-k, top-p, penalties, a grammar) ends in probabilities, and drafts that
+ * were looked up rather than sampled have no q row at all.
+ *   target_probs  [B][G+1][V] (packed: [total_drafts + B][V]), float32 or bf16
+ *   draft_probs   [B][G][V] (packed: [total_drafts][V]), the same type; NULL:
+ *                 each draft was certain, q_i is 1 at x_i and 0 elsewhere (the
+ *                 test is u < p_i(x_i), the residual is p_k without x_k)
+ * Draft i is accepted iff q_i(x_i) = 0 or u q_i(x_i) < p_i(x_i); k and the final
+ * draw as in steps 2 and 3.  Rows need not sum to 1: a draw uses its weights'
+ * own total.  Of a request, the calls read p and q at the drafts, row k of
+ * target_probs and, after a rejection, row k of draft_probs.  The tests are
+ * exact; the draw's weights are p and q as whole multiples of 2^-56, summed
+ * exactly, and compared with u times the total exactly.  A residual whose
+ * weights are all 0 draws from p_k; a row of zeros draws V - 1 and sets
+ * SV_STATUS_BAD_PROB.  An entry that is no probability (negative, NaN, above 1)
+ * sets that bit where it is read and counts as 0 (above 1: as 1).
+ * The other arguments, the layouts, the workspace (status word only), errors and
+ * ownership: as spec_verify_sample and spec_verify_sample_packed.
+ */
+int spec_verify_sample_probs(const void *target_probs, const void *draft_probs, sv_dtype dtype,
+                             int B, int G, int V, const int32_t *draft_tokens,
+                             const int32_t *gamma, const float *uniforms, int32_t *out_tokens,
+                             int32_t *num_accepted, void *workspace, size_t ws_bytes,
+                             sv_stream_t stream);
+int spec_verify_sample_probs_packed(const void *target_probs, const void *draft_probs,
+                                    sv_dtype dtype, int B, int G, int V, const int32_t *cu_draft,
+                                    int total_drafts, const int32_t *draft_tokens,
+                                    const float *uniforms, int32_t *out_tokens,
+                                    int32_t *num_accepted, void *workspace, size_t ws_bytes,
+                                    sv_stream_t stream);
+
+/*
+ * The target's KV cache across verify steps.  The target scores a request's last
+ * token and its gamma_b drafts in one pass ("Speculative Decoding theory", Step
+ * 2): gamma_b + 1 rows, at the packed row offsets cu_draft[b] + b.  Their keys and
+ * values are appended behind the request's kv_len[b] tokens, the rows attend to
+ * the cache, and after the verification the cache is rolled back by its length
+ * alone (explainer, "Implementation points", KV rollback): the next step's
+ * kv_len[b] is kv_len[b] + num_accepted[b] + 1, and what lies behind is
+ * overwritten by the next append.
+ *
+ * A cache is a pool of pages of page_size tokens.  Element (page, token, head,
+ * value) of the keys lies at k_pages + page * k_strides[0] + token * k_strides[1]
+ * + head * k_strides[2] + value (elements), likewise for values, so pools stored
+ * [page][token][head][value] and [page][head][token][value] both fit.  Token t of
+ * request b lies in page page_table[b * max_pages + t / page_size], at t %
+ * page_size.  Pages that two requests share are only read; a page that is
+ * appended to belongs to one request.
+ *   dtype      SV_BF16 or SV_F16
+ *   page_size  a power of two from 16 to 4096
+ *   head_dim   a multiple of 8, at most SV_MAX_HEAD_DIM
+ *   strides    positive multiples of 8; pools 16-byte aligned
+ * The struct itself is HOST memory, read during the call; its pointers are device
+ * memory.
+ */
+typedef struct {
+  void *k_pages, *v_pages;
+  sv_dtype dtype;
+  int num_pages, page_size, kv_heads, head_dim;
+  int64_t k_strides[3], v_strides[3]; /* page, token, head */
+  const int32_t *page_table;          /* [batch][max_pages]; entries past a request's
+                                         tokens are not read */
+  int max_pages, batch;
+  const int32_t *kv_len;              /* [batch]: the request's own tokens before this step
+                                         (a shared prefix is not counted) */
+} sv_kv_cache;
+
+/*
+ * Appends a step's keys and values, and rotates its queries: row cu_draft[b] + b +
+ * i (i <= gamma_b) of request b goes to token kv_len[b] + i.
+ *   q            [total_drafts + batch][q_heads][head_dim], q_strides (HOST, row and
+ *                head, elements); q_out likewise (q_out may be q; otherwise the two
+ *                may not overlap).  q_heads 0: no queries, q and q_out may be NULL.
+ *   k, v         [total_drafts + batch][kv_heads][head_dim] with k_strides, v_strides
+ *   max_drafts   the largest gamma_b; any length (a prompt of n tokens is gamma_b =
+ *                n - 1)
+ *   freq         device int64 [rot_dim / 2]: pair j turns by freq[j] 2^-64 turns a
+ *                position (a far position loses nothing); NULL with rot_dim 0
+ *   rot_dim      even, at most head_dim: the first rot_dim values of a head turn, the
+ *                others are copied.  Pairs are (j, j + rot_dim / 2), with interleaved
+ *                (2j, 2j + 1): (a, c) -> rope_scale (a cos - c sin, c cos + a sin)
+ *   positions    optional device int32 [total_drafts + batch]: a row's position (the
+ *                depth of a tree draft's node); NULL: position_offset + kv_len[b] + i
+ *                (position_offset: the length of a shared prefix)
+ *   workspace    for the status word only: any of this library's, at least 4 bytes
+ * The rotation is computed in 32 bits and rounded once.  A request whose cu_draft
+ * entries are inconsistent (as in the packed calls, or a length above max_drafts)
+ * is skipped (SV_STATUS_BAD_GAMMA); a row past the page table
+ * (SV_STATUS_BAD_LENGTH) or on a page outside the pool (SV_STATUS_BAD_PAGE) is not
+ * stored, its query is still rotated.  No other element of the pools is written.
+ */
+int spec_verify_kv_append(const void *q, const int64_t *q_strides, int q_heads, const void *k,
+                          const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                          void *q_out, const int64_t *q_out_strides, const sv_kv_cache *cache,
+                          const int32_t *cu_draft, int total_drafts, int max_drafts,
+                          const int64_t *freq, int rot_dim, int interleaved, float rope_scale,
+                          const int32_t *positions, int position_offset, void *workspace,
+                          size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * Bytes of workspace that spec_verify_attention needs for total_rows =
+ * total_drafts + batch rows (more rows need more); 0 if the sizes are invalid.
+ */
+size_t spec_verify_attention_workspace_size(int total_rows, int q_heads, int head_dim);
+
+/*
+ * Attention of a step's rows over the cache, after their append.  Row i of request
+ * b sees the shared prefix and the request's own tokens 0 .. kv_len[b] + i:
+ *   o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j)
+ *   q, q_strides     as above (16-byte aligned, strides multiples of 8), the type of
+ *                    the cache; q_heads a multiple of kv_heads, at most 128 a key
+ *                    head; query head h reads key head h / (q_heads / kv_heads)
+ *   prefix_table     device int32, ceil(prefix_len / page_size) pages that every
+ *                    request reads before its own, with prefix_len (HOST) tokens;
+ *                    read once for the whole batch
+ *   draft_mask       optional device uint32 [total_drafts + batch], max_drafts <=
+ *                    SV_MAX_GAMMA: bit j of a row's word says whether it sees row j of
+ *                    its request's step (tree drafts), in place of j <= i; bits from
+ *                    gamma_b + 1 on are ignored.  Tokens before the step are always
+ *                    seen.
+ *   scale            positive
+ *   out              [total_drafts + batch][q_heads][head_dim], dense, 16-byte aligned
+ *   lse              optional float32 [total_drafts + batch][q_heads]: the natural log
+ *                    of the sum of weights
+ *   workspace        zero its first 4 bytes before the first use; the rest is
+ *                    scratch.  One call at a time, in order on one stream: two calls
+ *                    that may overlap, two captured graphs' among them, need two.
+ * A row that sees nothing (an empty mask word, no tokens before, no prefix), or
+ * whose scores are all -inf, gets zeros and lse -inf.  What the pool holds behind a
+ * request's last token is never used, whatever it is; a NaN or an infinity among
+ * the values of tokens that some row of a request sees reaches that request's
+ * other rows of the step too.  Requests with inconsistent cu_draft entries
+ * (SV_STATUS_BAD_GAMMA) or lengths (SV_STATUS_BAD_LENGTH: kv_len[b] + gamma_b + 1
+ * tokens past the page table) are skipped, their rows of out and lse left as they
+ * were.  Scores, sums and parts are 32 bits; weights are rounded to the cache's
+ * type for the product with the values.  Results repeat bit for bit.
+ */
+int spec_verify_attention(const void *q, const int64_t *q_strides, int q_heads,
+                          const sv_kv_cache *cache, const int32_t *prefix_table, int prefix_len,
+                          const int32_t *cu_draft, int total_drafts, int max_drafts, float scale,
+                          const uint32_t *draft_mask, void *out, float *lse, void *workspace,
+                          size_t ws_bytes, sv_stream_t stream);
 
 /*
  * spec_verify_sample_noalloc: spec_verify_sample with no caller workspace.

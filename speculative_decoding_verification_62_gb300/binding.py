@@ -15,22 +15,35 @@ import torch
 
 from . import build as _build
 
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_MAX_GAMMA = 31
+SV_MAX_HEAD_DIM = 128
 SV_MAX_VOCAB = 1 << 24
 STATUS_BITS = {1: "BAD_GAMMA", 2: "BAD_TOKEN", 4: "BAD_UNIFORM", 8: "BAD_TEMPERATURE",
-               16: "NONFINITE_ROW", 32: "INTERNAL", 64: "TIMEOUT"}
+               16: "NONFINITE_ROW", 32: "INTERNAL", 64: "TIMEOUT", 128: "BAD_PROB",
+               256: "BAD_PAGE", 512: "BAD_LENGTH"}
 SV_NOALLOC_SCRATCH_BYTES = 4 << 20
 EXPORTS = ("spec_verify_workspace_size", "spec_verify_sample", "spec_verify_greedy",
            "spec_verify_sample_packed", "spec_verify_greedy_packed", "spec_verify_draw",
            "spec_verify_sample_noalloc", "spec_verify_status", "spec_verify_strerror",
            "spec_verify_set_schedule", "spec_verify_route", "spec_verify_cluster_size",
-           "spec_verify_set_wait_limit", "spec_verify_set_lazy")
+           "spec_verify_set_wait_limit", "spec_verify_set_lazy", "spec_verify_sample_probs",
+           "spec_verify_sample_probs_packed", "spec_verify_kv_append", "spec_verify_attention",
+           "spec_verify_attention_workspace_size")
 SCHEDULE_AUTO, SCHEDULE_PERSISTENT, SCHEDULE_STREAM = 0, 1, 2
 ROUTE_PERSISTENT, ROUTE_CLUSTER, ROUTE_STREAM, ROUTE_CLAIMS, ROUTE_PIPELINE = 0, 1, 2, 3, 4
 
 _lock = threading.Lock()
 _lib = None
+
+
+class _KvCache(ctypes.Structure):
+    """sv_kv_cache of include/spec_verify.h."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("k_strides", ctypes.c_int64 * 3),
+                ("v_strides", ctypes.c_int64 * 3), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int), ("batch", ctypes.c_int), ("kv_len", ctypes.c_void_p)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -79,6 +92,22 @@ def load_library():
         lib.spec_verify_set_wait_limit.argtypes = [ctypes.c_ulonglong]
         lib.spec_verify_set_lazy.restype = ci
         lib.spec_verify_set_lazy.argtypes = [ci]
+        i64p, cf = ctypes.POINTER(ctypes.c_int64), ctypes.c_float
+        lib.spec_verify_sample_probs.restype = ci
+        lib.spec_verify_sample_probs.argtypes = [vp, vp, ci, ci, ci, ci, vp, vp, vp, vp, vp, vp,
+                                                 sz, vp]
+        lib.spec_verify_sample_probs_packed.restype = ci
+        lib.spec_verify_sample_probs_packed.argtypes = [vp, vp, ci, ci, ci, ci, vp, ci, vp, vp,
+                                                        vp, vp, vp, sz, vp]
+        cache = ctypes.POINTER(_KvCache)
+        lib.spec_verify_kv_append.restype = ci
+        lib.spec_verify_kv_append.argtypes = [vp, i64p, ci, vp, i64p, vp, i64p, vp, i64p, cache, vp,
+                                              ci, ci, vp, ci, ci, cf, vp, ci, vp, sz, vp]
+        lib.spec_verify_attention_workspace_size.restype = sz
+        lib.spec_verify_attention_workspace_size.argtypes = [ci, ci, ci]
+        lib.spec_verify_attention.restype = ci
+        lib.spec_verify_attention.argtypes = [vp, i64p, ci, cache, vp, ci, vp, ci, ci, cf, vp, vp,
+                                              vp, vp, sz, vp]
         _lib = lib
         return lib
 
@@ -302,6 +331,234 @@ def spec_verify_greedy(target_logits, draft_tokens, gamma, out_tokens, num_accep
         raise SpecVerifyError(rc)
 
 
+def _one_device(**tensors):
+    """The CUDA device that holds every given tensor (None: an argument left out)."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    return dev
+
+
+def _probs_draft(draft_probs, dtype, shape):
+    if draft_probs is None:
+        return None
+    return _dev(draft_probs, "draft_probs", dtype, shape)
+
+
+def spec_verify_sample_probs(target_probs, draft_probs, draft_tokens, gamma, uniforms, out_tokens,
+                             num_accepted, workspace, stream=None) -> None:
+    """Sampling verify step on probabilities instead of logits; draft_probs None: the
+    drafts were certain (looked up).  See include/spec_verify.h."""
+    dev = _one_device(target_probs=target_probs, draft_probs=draft_probs,
+                      draft_tokens=draft_tokens, gamma=gamma, uniforms=uniforms,
+                      out_tokens=out_tokens, num_accepted=num_accepted, workspace=workspace)
+    B, G1, V = target_probs.shape
+    G = G1 - 1
+    code = _dtype_code(target_probs)
+    with torch.cuda.device(dev):
+        rc = load_library().spec_verify_sample_probs(
+            _dev(target_probs, "target_probs"),
+            _probs_draft(draft_probs, target_probs.dtype, (B, G, V)), code, B, G, V,
+            _dev(draft_tokens, "draft_tokens", torch.int32, (B, G)),
+            _dev(gamma, "gamma", torch.int32, (B,)),
+            _dev(uniforms, "uniforms", torch.float32, (B, G + 1)),
+            _dev(out_tokens, "out_tokens", torch.int32, (B, G + 1)),
+            _dev(num_accepted, "num_accepted", torch.int32, (B,)),
+            _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise SpecVerifyError(rc)
+
+
+def spec_verify_sample_probs_packed(target_probs, draft_probs, cu_draft, draft_tokens, uniforms,
+                                    out_tokens, num_accepted, workspace, stream=None) -> None:
+    """spec_verify_sample_probs on the packed layout; see include/spec_verify.h."""
+    dev = _one_device(target_probs=target_probs, draft_probs=draft_probs, cu_draft=cu_draft,
+                      draft_tokens=draft_tokens, uniforms=uniforms, out_tokens=out_tokens,
+                      num_accepted=num_accepted, workspace=workspace)
+    B = cu_draft.numel() - 1
+    total = draft_tokens.numel()
+    V = target_probs.shape[1]
+    G = out_tokens.shape[1] - 1
+    if target_probs.shape[0] != total + B:
+        raise ValueError("target_probs must have total_drafts + B rows")
+    code = _dtype_code(target_probs)
+    with torch.cuda.device(dev):
+        rc = load_library().spec_verify_sample_probs_packed(
+            _dev(target_probs, "target_probs"),
+            _probs_draft(draft_probs, target_probs.dtype, (total, V)), code, B, G, V,
+            _dev(cu_draft, "cu_draft", torch.int32, (B + 1,)), total,
+            _dev(draft_tokens, "draft_tokens", torch.int32, (total,)),
+            _dev(uniforms, "uniforms", torch.float32, (total + B,)),
+            _dev(out_tokens, "out_tokens", torch.int32, (B, G + 1)),
+            _dev(num_accepted, "num_accepted", torch.int32, (B,)),
+            _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise SpecVerifyError(rc)
+
+
+class PagedCache:
+    """The target's KV cache of a batch: page pools, page table and lengths.
+
+    k_pages, v_pages [num_pages, page_size, kv_heads, head_dim] (bfloat16 or float16, the
+    last dimension contiguous, the others of any stride that is a multiple of 8: a pool
+    stored [page, head, token, value] is passed as its transpose(1, 2)), page_table
+    [batch, max_pages] int32 and kv_len [batch] int32.  The tensors stay the caller's: they
+    are used in place, and kv_len is advanced by commit() alone.  Pages or rows of the
+    pools may not overlap one another.
+    """
+
+    def __init__(self, k_pages, v_pages, page_table, kv_len):
+        self.device = _one_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+                                  kv_len=kv_len)
+        if k_pages.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"k_pages must be bfloat16 or float16, got {k_pages.dtype}")
+        if v_pages.dtype != k_pages.dtype:
+            raise TypeError(f"v_pages must be {k_pages.dtype}, got {v_pages.dtype}")
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must have one shape [num_pages, page_size, "
+                             "kv_heads, head_dim]")
+        n, page, heads, dim = k_pages.shape
+        if n < 1 or heads < 1:
+            raise ValueError("a pool needs a page and a head")
+        if page < 16 or page > 4096 or page & (page - 1):
+            raise ValueError(f"page_size must be a power of two from 16 to 4096, got {page}")
+        if dim < 8 or dim > SV_MAX_HEAD_DIM or dim % 8:
+            raise ValueError(f"head_dim must be a multiple of 8 up to {SV_MAX_HEAD_DIM}, got {dim}")
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.stride(3) != 1 or any(s <= 0 or s % 8 for s in t.stride()[:3]) or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be 16-byte aligned with contiguous heads and "
+                                 "strides that are multiples of 8")
+            order = sorted(range(4), key=lambda i: t.stride(i))
+            reach = 0
+            for i in order:
+                if t.shape[i] > 1:
+                    if t.stride(i) <= reach:
+                        raise ValueError(f"{name} overlaps itself")
+                    reach += (t.shape[i] - 1) * t.stride(i)
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous():
+            raise ValueError("page_table must be a contiguous int32 [batch, max_pages]")
+        B, width = page_table.shape
+        _dev(kv_len, "kv_len", torch.int32, (B,))
+        self.k_pages, self.v_pages, self.page_table, self.kv_len = k_pages, v_pages, page_table, kv_len
+        self.batch, self.kv_heads, self.head_dim, self.dtype = B, heads, dim, k_pages.dtype
+        self.page_size = page
+        ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
+        self.struct = _KvCache(
+            k_pages.data_ptr(), v_pages.data_ptr(),
+            SV_BF16 if k_pages.dtype == torch.bfloat16 else SV_F16, n, page, heads, dim,
+            (ctypes.c_int64 * 3)(*k_pages.stride()[:3]), (ctypes.c_int64 * 3)(*v_pages.stride()[:3]),
+            ptr(page_table), width, B, ptr(kv_len))
+
+    def commit(self, num_accepted) -> None:
+        """After a verification: every request keeps its last token and its accepted
+        drafts (kv_len += num_accepted + 1); the rejected drafts' entries lie behind the
+        new length and are overwritten by the next append.  On the current stream."""
+        self.kv_len.add_(num_accepted).add_(1)
+
+
+def make_attention_workspace(total_rows: int, q_heads: int, head_dim: int,
+                             device="cuda") -> torch.Tensor:
+    """Workspace of spec_verify_attention for steps of up to total_rows rows."""
+    n = int(load_library().spec_verify_attention_workspace_size(int(total_rows), int(q_heads),
+                                                                int(head_dim)))
+    if n == 0:
+        raise ValueError(f"invalid sizes rows={total_rows} q_heads={q_heads} head_dim={head_dim}")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _heads(t, name, cache, rows, heads):
+    """Pointer and (row, head) strides of a [rows, heads, head_dim] view."""
+    if t.dtype != cache.dtype:
+        raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
+    if tuple(t.shape) != (rows, heads, cache.head_dim):
+        raise ValueError(f"{name} must have shape {(rows, heads, cache.head_dim)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 2)(t.stride(0), t.stride(1))
+
+
+def _cu_rows(cu_draft, cache, rows):
+    if rows < cache.batch:
+        raise ValueError(f"a step of {cache.batch} requests has at least as many rows, got {rows}")
+    return _dev(cu_draft, "cu_draft", torch.int32, (cache.batch + 1,)), rows - cache.batch
+
+
+def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, workspace,
+                          interleaved=False, rope_scale=1.0, positions=None, position_offset=0,
+                          stream=None) -> None:
+    """Append a step's keys and values to the paged cache and rotate its queries and keys;
+    q and q_out may be None, freq (rope.fixed_point) None for no rotation.  See
+    include/spec_verify.h."""
+    dev = _one_device(k_pages=cache.k_pages, q=q, k=k, v=v, cu_draft=cu_draft, freq=freq,
+                      q_out=q_out, workspace=workspace, positions=positions)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    rows = k.shape[0]
+    cu, total = _cu_rows(cu_draft, cache, rows)
+    kp, ks = _heads(k, "k", cache, rows, cache.kv_heads)
+    vp, vs = _heads(v, "v", cache, rows, cache.kv_heads)
+    heads, qp, qs, op, os_ = 0, None, None, None, None
+    if q is not None:
+        heads = q.shape[1]
+        qp, qs = _heads(q, "q", cache, rows, heads)
+        op, os_ = _heads(q_out, "q_out", cache, rows, heads)
+        if (rows > 1 and q_out.stride(0) < cache.head_dim) or (heads > 1 and q_out.stride(1) < cache.head_dim):
+            raise ValueError("q_out overlaps itself")
+    rot = 0
+    if freq is not None:
+        rot = 2 * freq.numel()
+        _dev(freq, "freq", torch.int64, (rot // 2,))
+    with torch.cuda.device(dev):
+        rc = load_library().spec_verify_kv_append(
+            qp, qs, heads, kp, ks, vp, vs, op, os_, ctypes.byref(cache.struct), cu, total,
+            int(max_drafts), None if freq is None else _dev(freq, "freq"), rot, int(bool(interleaved)),
+            float(rope_scale), _dev(positions, "positions", torch.int32, (rows,)),
+            int(position_offset), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
+            _stream(stream))
+    if rc != 0:
+        raise SpecVerifyError(rc)
+
+
+def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix_table=None,
+                          prefix_len=0, scale=None, draft_mask=None, lse=None, stream=None) -> None:
+    """Attention of a step's rows over the paged cache (and a prefix that the batch shares);
+    scale None: head_dim ** -0.5.  See include/spec_verify.h."""
+    dev = _one_device(k_pages=cache.k_pages, q=q, cu_draft=cu_draft, out=out, workspace=workspace,
+                      prefix_table=prefix_table, draft_mask=draft_mask, lse=lse)
+    rows, heads = q.shape[0], q.shape[1]
+    cu, total = _cu_rows(cu_draft, cache, rows)
+    qp, qs = _heads(q, "q", cache, rows, heads)
+    prefix_len = int(prefix_len)
+    pages = -(-prefix_len // cache.page_size)
+    if prefix_len > 0:
+        if prefix_table is None or prefix_table.numel() < pages:
+            raise ValueError(f"prefix_table must hold {pages} pages")
+        pt = _dev(prefix_table, "prefix_table", torch.int32)
+    else:
+        pt = None
+    if draft_mask is not None and draft_mask.dtype not in (torch.int32, torch.uint32):
+        raise TypeError("draft_mask must be int32 or uint32 words")
+    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
+    with torch.cuda.device(dev):
+        rc = load_library().spec_verify_attention(
+            qp, qs, heads, ctypes.byref(cache.struct), pt, prefix_len, cu, total, int(max_drafts),
+            scale, _dev(draft_mask, "draft_mask", None, (rows,)),
+            _dev(out, "out", q.dtype, (rows, heads, cache.head_dim)),
+            _dev(lse, "lse", torch.float32, (rows, heads)),
+            _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise SpecVerifyError(rc)
+
+
 def spec_verify_status(workspace, stream=None) -> int:
     """Read and clear the workspace status word (synchronises the stream)."""
     out = ctypes.c_uint32(0)
@@ -347,4 +604,16 @@ class Verifier:
     def greedy_packed(self, target, cu_draft, draft_tokens, stream=None):
         spec_verify_greedy_packed(target, cu_draft, draft_tokens, self.out_tokens,
                                   self.num_accepted, self.workspace, stream)
+        return self.out_tokens, self.num_accepted
+
+    def sample_probs(self, target_probs, draft_probs, draft_tokens, gamma, uniforms, stream=None):
+        spec_verify_sample_probs(target_probs, draft_probs, draft_tokens, gamma, uniforms,
+                                 self.out_tokens, self.num_accepted, self.workspace, stream)
+        return self.out_tokens, self.num_accepted
+
+    def sample_probs_packed(self, target_probs, draft_probs, cu_draft, draft_tokens, uniforms,
+                            stream=None):
+        spec_verify_sample_probs_packed(target_probs, draft_probs, cu_draft, draft_tokens,
+                                        uniforms, self.out_tokens, self.num_accepted,
+                                        self.workspace, stream)
         return self.out_tokens, self.num_accepted

@@ -1,7 +1,8 @@
 """Compile the CUDA verify library (sm_103a) into the package directory.
 
-One translation unit, one -gencode: nvcc cross-compiles here without a GPU
-and builds natively on the GPU host in a few seconds.
+One -gencode; the translation units are compiled in parallel and linked into
+one library.  nvcc cross-compiles without a GPU and builds natively on the GPU
+host in well under a minute.
 """
 from __future__ import annotations
 
@@ -9,12 +10,14 @@ import glob
 import os
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspec_verify.so")
-SOURCES = [os.path.join(PKG, "csrc", "spec_verify.cu")]
+SOURCES = [os.path.join(PKG, "csrc", n + ".cu")
+           for n in ("spec_verify", "probs", "kv_append", "attention")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -26,7 +29,7 @@ def nvcc() -> str:
 
 
 def inputs() -> list[str]:
-    return SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.cuh")) + \
+    return SOURCES + glob.glob(os.path.join(PKG, "csrc", "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
@@ -42,11 +45,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not (force or stale()):
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), "-O3", *ARCH, "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", INCLUDE, "-o", tmp, *SOURCES]
+    base = [nvcc(), "-O3", *ARCH, "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+        base.insert(1, "-Xptxas=-v")
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(src) + ".o") for src in SOURCES]
+        runs = [subprocess.Popen([*base, "-c", "-o", obj, src]) for src, obj in zip(SOURCES, objs)]
+        codes = [r.wait() for r in runs]
+        if any(codes):
+            raise RuntimeError(f"nvcc failed on {[s for s, c in zip(SOURCES, codes) if c]}")
+        subprocess.run([*base, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,347 @@
+// A step's keys and values into a paged cache, with the rotary position
+// rotation applied on the way.
+//
+// Row i of request b sits at position p = position_offset + kv_len[b] + i (or
+// positions[row]) and goes to slot kv_len[b] + i of the request's pages.  Pair
+// j of a head (values j and j + rot/2, or 2j and 2j + 1) turns by the angle
+// p f_j: (a, c) -> s (a cos - c sin, c cos + a sin).  f_j is given in turns a
+// position, as a whole multiple of 2^-64, so p f_j modulo one turn is a 64-bit
+// product that wraps: far positions lose nothing (the rounding of f_j, 2^-65
+// turns, grows to 2^-34 turns at position 2^31).  The turn goes to 32-bit
+// floats as a fraction in [-1/2, 1/2), and cos and sin are taken of that.
+//
+// Bound: q, k and v are read once and written once.  Few rows: latency (the
+// page look-up depends on the request look-up).  A CTA handles kRows rows (one
+// where there are few): their angles are formed once, in shared memory, and
+// serve every head.
+#include "../../include/spec_verify.h"
+#include "internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 4;
+
+struct AppendParams {
+  const char* q;
+  const char* k;
+  const char* v;
+  char* q_out;
+  char* k_pages;
+  char* v_pages;
+  long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;  // elements
+  long long kp, kt, kh, vp, vt, vh;  // cache strides: page, token, head
+  int Hq, Hk, D, rot, B, T, G, num_pages, page_size, max_pages, rows;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* cu;
+  const long long* freq;
+  const int32_t* positions;
+  int offset;
+  float scale;
+  unsigned int* status;
+};
+
+struct RowInfo {
+  long long k_at, v_at;  // element offsets of the row's slot in the pools; -1: skipped
+};
+
+template <typename T>
+struct Conv;
+template <>
+struct Conv<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 up(unsigned int w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ unsigned int down(float a, float b) {
+    __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<unsigned int*>(&r);
+  }
+};
+template <>
+struct Conv<__half> {
+  static __device__ __forceinline__ float2 up(unsigned int w) {
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+  }
+  static __device__ __forceinline__ unsigned int down(float a, float b) {
+    __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<unsigned int*>(&r);
+  }
+};
+
+// VW 16-bit values as 32-bit words
+template <int VW>
+struct Vec {
+  unsigned int w[VW / 2];
+};
+template <int VW>
+__device__ __forceinline__ Vec<VW> load_vec(const char* p) {
+  Vec<VW> r;
+  if (VW == 8) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2 % (VW / 2)] = v.z, r.w[3 % (VW / 2)] = v.w;
+  } else {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+    r.w[0] = v.x, r.w[1] = v.y;
+  }
+  return r;
+}
+template <int VW>
+__device__ __forceinline__ void store_vec(char* p, const Vec<VW>& r) {
+  if (VW == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2 % (VW / 2)], r.w[3 % (VW / 2)]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+}
+
+// The request of row t: the largest b with cu[b] + b <= t, by one warp, 32
+// probes a round.
+__device__ __forceinline__ int request_of(const int32_t* cu, int B, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const bool le = at < hi && (long long)cu[at] + at <= t;
+    const int n = __popc(__ballot_sync(0xffffffffu, le));
+    if (n == 0) return lo;
+    lo += (n - 1) * step;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  return lo;
+}
+
+template <typename T, int VW, bool INTER>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
+  extern __shared__ float2 s_turn[];  // [rows][rot / 2] cos, sin
+  __shared__ RowInfo s_row[kMaxRows];
+  __shared__ int s_req[kMaxRows];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int half = P.rot / 2;
+  const int r0 = blockIdx.x * P.rows;
+  const int nrows = P.T - r0 < P.rows ? P.T - r0 : P.rows;
+  __shared__ long long s_pos[kMaxRows];
+  if (tid < 32) {
+    const int b0 = request_of(P.cu, P.B, r0);
+    unsigned int flags = 0;
+    if (lane < nrows) {
+      const int t = r0 + lane;
+      int b = b0;
+      while (b + 1 < P.B && (long long)P.cu[b + 1] + b + 1 <= t) ++b;
+      const int c0 = P.cu[b], c1 = P.cu[b + 1];
+      const int i = t - b - c0;
+      RowInfo info{-1, -1};
+      long long pos = 0;
+      if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 + P.B > P.T || i < 0 || i > c1 - c0) {
+        flags = SV_STATUS_BAD_GAMMA;
+      } else {
+        const int n = P.kv_len[b];
+        const long long slot = (long long)n + i;
+        if (n < 0 || slot >= (long long)P.max_pages * P.page_size) {
+          flags = SV_STATUS_BAD_LENGTH;
+        } else {
+          const int page = P.table[(size_t)b * P.max_pages + slot / P.page_size];
+          if (page < 0 || page >= P.num_pages) {
+            flags = SV_STATUS_BAD_PAGE;
+          } else {
+            const long long in = slot % P.page_size;
+            info.k_at = page * P.kp + in * P.kt;
+            info.v_at = page * P.vp + in * P.vt;
+          }
+          pos = P.positions ? (long long)P.positions[t] : (long long)P.offset + slot;
+        }
+      }
+      s_row[lane] = info;
+      s_pos[lane] = pos;
+      s_req[lane] = flags & SV_STATUS_BAD_GAMMA ? -1 : b;
+    }
+    const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
+    if (lane == 0 && any) atomicOr(P.status, any);
+  }
+  __syncthreads();
+  for (int e = tid; e < nrows * half; e += kThreads) {
+    const int r = e / half;
+    const long long turn = (long long)((unsigned long long)s_pos[r] * (unsigned long long)P.freq[e - r * half]);
+    float sn, cs;
+    sincospif(__ll2float_rn(turn) * 0x1p-63f, &sn, &cs);
+    s_turn[e] = make_float2(cs * P.scale, sn * P.scale);
+  }
+  __syncthreads();
+  const int per_head = VW == 1 ? (P.D + 1) / 2 : P.D / (2 * VW);
+  const int Hs = P.Hq + P.Hk;  // heads that turn
+  for (int r = 0; r < nrows; ++r) {
+    const int t = r0 + r;
+    if (s_req[r] < 0) continue;
+    const RowInfo info = s_row[r];
+    const float2* turn = s_turn + r * half;
+    const char* q = P.q + (size_t)t * P.q_row * 2;
+    const char* k = P.k + (size_t)t * P.k_row * 2;
+    const char* v = P.v + (size_t)t * P.v_row * 2;
+    char* o = P.q_out + (size_t)t * P.o_row * 2;
+    const int n = (Hs + P.Hk) * per_head;
+    for (int e = tid; e < n; e += kThreads) {
+      const int h = e / per_head, s = e - h * per_head;
+      const char* src;
+      char* dst;
+      if (h < P.Hq) {
+        src = q + (long long)h * P.q_head * 2;
+        dst = o + (long long)h * P.o_head * 2;
+      } else if (h < Hs) {
+        if (info.k_at < 0) continue;
+        src = k + (long long)(h - P.Hq) * P.k_head * 2;
+        dst = P.k_pages + (info.k_at + (long long)(h - P.Hq) * P.kh) * 2;
+      } else {
+        if (info.k_at < 0) continue;
+        src = v + (long long)(h - Hs) * P.v_head * 2;
+        dst = P.v_pages + (info.v_at + (long long)(h - Hs) * P.vh) * 2;
+      }
+      const bool turns = h < Hs && s < (VW == 1 ? half : P.rot / (2 * VW));
+      if constexpr (VW == 1) {
+        // one pair of values
+        const unsigned short* a = reinterpret_cast<const unsigned short*>(src);
+        unsigned short* d = reinterpret_cast<unsigned short*>(dst);
+        const int j = turns && !INTER ? s : 2 * s;
+        const int j2 = turns && !INTER ? s + half : 2 * s + 1;
+        if (!turns) {
+          d[j] = a[j];
+          if (j2 < P.D) d[j2] = a[j2];
+        } else {
+          const float2 x = Conv<T>::up((unsigned int)a[j] | ((unsigned int)a[j2] << 16));
+          const float2 c = turn[s];
+          const unsigned int y = Conv<T>::down(x.x * c.x - x.y * c.y, x.y * c.x + x.x * c.y);
+          d[j] = (unsigned short)y;
+          d[j2] = (unsigned short)(y >> 16);
+        }
+      } else if (!turns) {
+        const Vec<VW> x = load_vec<VW>(src + (size_t)s * VW * 4), y = load_vec<VW>(src + (size_t)s * VW * 4 + VW * 2);
+        store_vec<VW>(dst + (size_t)s * VW * 4, x);
+        store_vec<VW>(dst + (size_t)s * VW * 4 + VW * 2, y);
+      } else if (INTER) {
+        // two neighbouring vectors hold VW pairs
+        Vec<VW> x[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) x[m] = load_vec<VW>(src + (size_t)s * VW * 4 + m * VW * 2);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+          for (int w = 0; w < VW / 2; ++w) {
+            const float2 a = Conv<T>::up(x[m].w[w]);
+            const float2 c = turn[s * VW + m * (VW / 2) + w];
+            x[m].w[w] = Conv<T>::down(a.x * c.x - a.y * c.y, a.y * c.x + a.x * c.y);
+          }
+          store_vec<VW>(dst + (size_t)s * VW * 4 + m * VW * 2, x[m]);
+        }
+      } else {
+        Vec<VW> x = load_vec<VW>(src + (size_t)s * VW * 2), y = load_vec<VW>(src + ((size_t)half + s * VW) * 2);
+#pragma unroll
+        for (int w = 0; w < VW / 2; ++w) {
+          const float2 a = Conv<T>::up(x.w[w]), b = Conv<T>::up(y.w[w]);
+          const float2 c0 = turn[s * VW + 2 * w], c1 = turn[s * VW + 2 * w + 1];
+          x.w[w] = Conv<T>::down(a.x * c0.x - b.x * c0.y, a.y * c1.x - b.y * c1.y);
+          y.w[w] = Conv<T>::down(b.x * c0.x + a.x * c0.y, b.y * c1.x + a.y * c1.y);
+        }
+        store_vec<VW>(dst + (size_t)s * VW * 2, x);
+        store_vec<VW>(dst + ((size_t)half + s * VW) * 2, y);
+      }
+    }
+  }
+}
+
+template <typename T, int VW>
+int launch(const AppendParams& P, bool inter, cudaStream_t stream) {
+  const unsigned int grid = (unsigned int)((P.T + P.rows - 1) / P.rows);
+  const size_t smem = (size_t)P.rows * (P.rot / 2) * sizeof(float2);
+  if (inter)
+    append_kernel<T, VW, true><<<grid, kThreads, smem, stream>>>(P);
+  else
+    append_kernel<T, VW, false><<<grid, kThreads, smem, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <typename T>
+int launch_width(const AppendParams& P, int vw, bool inter, cudaStream_t stream) {
+  if (vw == 8) return launch<T, 8>(P, inter, stream);
+  if (vw == 4) return launch<T, 4>(P, inter, stream);
+  return launch<T, 1>(P, inter, stream);
+}
+
+}  // namespace
+
+extern "C" int spec_verify_kv_append(const void* q, const int64_t* q_strides, int q_heads,
+                                     const void* k, const int64_t* k_strides, const void* v,
+                                     const int64_t* v_strides, void* q_out,
+                                     const int64_t* q_out_strides, const sv_kv_cache* cache,
+                                     const int32_t* cu_draft, int total_drafts, int max_drafts,
+                                     const int64_t* freq, int rot_dim, int interleaved,
+                                     float rope_scale, const int32_t* positions,
+                                     int position_offset, void* workspace, size_t ws_bytes,
+                                     sv_stream_t stream) {
+  if (!cache || !k_strides || !v_strides) return SV_ERR_NULL;
+  const sv_kv_cache& c = *cache;
+  int rc = sv::check_cache(c);
+  if (rc) return rc;
+  if (total_drafts < 0 || max_drafts < 0 || q_heads < 0 || rot_dim < 0 || rot_dim % 2 ||
+      rot_dim > c.head_dim || (interleaved != 0 && interleaved != 1) || !(rope_scale > 0.f) ||
+      rope_scale > 3.0e38f || (long long)total_drafts + c.batch > INT32_MAX)
+    return SV_ERR_SCALAR;
+  if (!k || !v || !cu_draft || !workspace || (rot_dim > 0 && !freq)) return SV_ERR_NULL;
+  if (q_heads > 0 && (!q || !q_out || !q_strides || !q_out_strides)) return SV_ERR_NULL;
+  if (ws_bytes < sizeof(uint32_t)) return SV_ERR_WORKSPACE;
+  if (!sv::aligned(q, 2) || !sv::aligned(k, 2) || !sv::aligned(v, 2) || !sv::aligned(q_out, 2) ||
+      !sv::aligned(cu_draft, 4) || !sv::aligned(freq, 8) || !sv::aligned(positions, 4) ||
+      !sv::aligned(workspace, 256))
+    return SV_ERR_ALIGN;
+  if (c.batch == 0) return SV_OK;
+  AppendParams P = {};
+  P.q = static_cast<const char*>(q);
+  P.k = static_cast<const char*>(k);
+  P.v = static_cast<const char*>(v);
+  P.q_out = static_cast<char*>(q_out);
+  P.k_pages = static_cast<char*>(c.k_pages);
+  P.v_pages = static_cast<char*>(c.v_pages);
+  if (q_heads > 0) {
+    P.q_row = q_strides[0], P.q_head = q_strides[1];
+    P.o_row = q_out_strides[0], P.o_head = q_out_strides[1];
+  }
+  P.k_row = k_strides[0], P.k_head = k_strides[1];
+  P.v_row = v_strides[0], P.v_head = v_strides[1];
+  P.kp = c.k_strides[0], P.kt = c.k_strides[1], P.kh = c.k_strides[2];
+  P.vp = c.v_strides[0], P.vt = c.v_strides[1], P.vh = c.v_strides[2];
+  P.Hq = q_heads;
+  P.Hk = c.kv_heads;
+  P.D = c.head_dim;
+  P.rot = rot_dim;
+  P.B = c.batch;
+  P.T = total_drafts + c.batch;
+  P.G = max_drafts;
+  P.num_pages = c.num_pages;
+  P.page_size = c.page_size;
+  P.max_pages = c.max_pages;
+  P.rows = P.T >= 2048 ? kMaxRows : 1;
+  P.table = c.page_table;
+  P.kv_len = c.kv_len;
+  P.cu = cu_draft;
+  P.freq = reinterpret_cast<const long long*>(freq);
+  P.positions = positions;
+  P.offset = position_offset;
+  P.scale = rope_scale;
+  P.status = static_cast<unsigned int*>(workspace);
+  // The widest vector that every head's start and both halves of a rotation
+  // allow: 8 values (16 bytes), 4, or single pairs.
+  int vw = 8;
+  for (; vw > 1; vw >>= 1) {
+    if (vw == 2) { vw = 1; break; }
+    const long long strides[] = {P.q_row, P.q_head, P.o_row, P.o_head, P.k_row, P.k_head, P.v_row,
+                                 P.v_head, P.kp, P.kt, P.kh, P.vp, P.vt, P.vh};
+    bool ok = P.D % (2 * vw) == 0 && P.rot % (2 * vw) == 0;
+    for (long long s : strides) ok = ok && s % vw == 0;
+    for (const void* p : {q, k, v, (const void*)q_out, (const void*)c.k_pages, (const void*)c.v_pages})
+      ok = ok && sv::aligned(p, 2 * vw);
+    if (ok) break;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return c.dtype == SV_BF16 ? launch_width<__nv_bfloat16>(P, vw, interleaved, s)
+                            : launch_width<__half>(P, vw, interleaved, s);
+}

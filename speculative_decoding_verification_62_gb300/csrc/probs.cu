@@ -1,0 +1,457 @@
+// Verification of drafted tokens against given probabilities.
+//
+// Per request: draft i is accepted iff q_i(x_i) = 0 or u_i q_i(x_i) < p_i(x_i);
+// k is the first draft refused, or gamma_b.  The last token is drawn from
+//   w = max(0, p_k - q_k)   (k < gamma_b; from p_k where every w is 0)
+//   w = p_{gamma_b}         (every draft accepted)
+// by the inverse CDF: the smallest j with w_0 + .. + w_j > u w_total.
+//
+// The test is exact: u q is a product of two 24-bit numbers, formed in double.
+// The draw is exact up to the weights' grain: p and q are rounded to whole
+// multiples of 2^-56 (a float of 2^-32 or more is one already) and summed as
+// 64-bit integers, so no sum depends on an order, and u w_total is compared
+// after a 128-bit product.  A rounding moves a CDF boundary by at most
+// V 2^-57, so a uniform of 24 bits lands on the other side of one with a
+// chance below V^2 2^-57 (2^-23 at V = 128256 if every rounding went one way).
+// Sums saturate at 2^63 = 128 (a row that sums to about 1 stays far below).
+//
+// Bound: the one or two rows that the draw needs are read once from HBM; all
+// other reads are gathers.  A cluster of C CTAs shares a request, each warp a
+// contiguous range of the row.  The owner of the target re-reads only the
+// range of the warp that holds it, from L2.
+#include "../../include/spec_verify.h"
+#include "internal.h"
+
+#include <atomic>
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr unsigned long long kCap = 1ull << 63;
+
+struct ProbsParams {
+  const char* target;
+  const char* draft;  // null: the draft is certain of its token
+  int B, G, V, total, C;
+  const int32_t* tokens;
+  const int32_t* gamma;  // padded layout
+  const int32_t* cu;     // packed layout
+  const float* uniforms;
+  int32_t* out;
+  int32_t* accepted;
+  unsigned int* status;
+};
+
+__device__ __forceinline__ unsigned long long sat_add(unsigned long long a, unsigned long long b) {
+  const unsigned long long s = a + b;  // both at most 2^63
+  return s < kCap ? s : kCap;
+}
+
+template <int EB>
+__device__ __forceinline__ float load_one(const char* row, size_t i) {
+  if (EB == 4) return __ldg(reinterpret_cast<const float*>(row) + i);
+  return __uint_as_float((unsigned int)__ldg(reinterpret_cast<const unsigned short*>(row) + i) << 16);
+}
+
+// A probability as a whole multiple of 2^-56; what is none counts as 0, what
+// is above 1 as 1, and both are flagged.
+__device__ __forceinline__ unsigned long long fix(float p, unsigned int& flags) {
+  if (!(p >= 0.f && p <= 1.f)) {
+    flags |= SV_STATUS_BAD_PROB;
+    p = p > 1.f ? 1.f : 0.f;
+  }
+  return __float2ull_rn(p * 0x1p56f);
+}
+
+__device__ __forceinline__ unsigned long long weight(float p, float q, unsigned int& flags) {
+  const unsigned long long a = fix(p, flags), b = fix(q, flags);
+  return a > b ? a - b : 0ull;
+}
+
+// floor(u S) for a float u in [0, 1): u = m 2^-s with a 24-bit m.
+__device__ __forceinline__ unsigned long long scaled(float u, unsigned long long S) {
+  if (u == 0.f) return 0;
+  const unsigned int bits = __float_as_uint(u);
+  const unsigned int e = bits >> 23;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int s = 150 - (int)(e ? e : 1u);  // 24 .. 149
+  const unsigned long long hi = __umul64hi(m, S), lo = m * S;
+  if (s >= 128) return 0;
+  if (s >= 64) return hi >> (s - 64);
+  return (hi << (64 - s)) | (lo >> s);
+}
+
+__device__ __forceinline__ unsigned int cluster_rank() {
+  unsigned int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void store_to_rank(unsigned long long* p, unsigned int rank, unsigned long long v) {
+  unsigned int a = (unsigned int)__cvta_generic_to_shared(p), r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(r), "l"(v) : "memory");
+}
+
+// The weights that a draw sums: of rows p and q (q may be null), or of p with
+// token `skip` left out.
+struct Draw {
+  const char* p;
+  const char* q;
+  int skip;
+};
+
+template <int EB>
+__device__ __forceinline__ unsigned long long weight_at(const Draw& d, int i, unsigned int& flags) {
+  if (i == d.skip) return 0;
+  const float p = load_one<EB>(d.p, i);
+  return weight(p, d.q ? load_one<EB>(d.q, i) : 0.f, flags);
+}
+
+template <int EB>
+__device__ __forceinline__ float word_elem(const uint4& v, int j) {
+  const unsigned int w = j * EB / 4 == 0 ? v.x : j * EB / 4 == 1 ? v.y : j * EB / 4 == 2 ? v.z : v.w;
+  if (EB == 4) return __uint_as_float(w);
+  return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+}
+
+// The sum of one warp's units [u0, u1): a unit is 32 x 16 bytes of the row.
+// VEC: rows are 16-byte aligned and V is a whole number of 16-byte words.
+template <int EB, bool VEC, bool TWO>
+__device__ __forceinline__ unsigned long long range_sum(const Draw& d, int V, int u0, int u1,
+                                                        unsigned int& flags) {
+  constexpr int E = 16 / EB;
+  constexpr int kUnroll = 4;
+  const int lane = threadIdx.x & 31;
+  unsigned long long acc = 0;
+  if (VEC) {
+    const uint4* p = reinterpret_cast<const uint4*>(d.p);
+    const uint4* q = reinterpret_cast<const uint4*>(d.q);
+    const int words = V / E;
+    for (int u = u0; u < u1; u += kUnroll) {
+      uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        const int w = (u + r) * 32 + lane;
+        const bool in = u + r < u1 && w < words;
+        a[r] = in ? __ldcs(p + w) : make_uint4(0, 0, 0, 0);
+        if (TWO) b[r] = in ? __ldcs(q + w) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < kUnroll; ++r) {
+        unsigned long long s = 0;
+        const int e0 = ((u + r) * 32 + lane) * E;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const unsigned long long w =
+              weight(word_elem<EB>(a[r], j), TWO ? word_elem<EB>(b[r], j) : 0.f, flags);
+          s += (!TWO && e0 + j == d.skip) ? 0ull : w;
+        }
+        acc = sat_add(acc, s);
+      }
+    }
+  } else {
+    for (int u = u0; u < u1; ++u) {
+      unsigned long long s = 0;
+      float a[E], b[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int i = (u * E + j) * 32 + lane;
+        a[j] = i < V ? load_one<EB>(d.p, i) : 0.f;
+        b[j] = TWO && i < V ? load_one<EB>(d.q, i) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int i = (u * E + j) * 32 + lane;
+        const unsigned long long w = weight(a[j], b[j], flags);
+        s += (!TWO && i == d.skip) ? 0ull : w;
+      }
+      acc = sat_add(acc, s);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc = sat_add(acc, __shfl_xor_sync(0xffffffffu, acc, o));
+  return acc;
+}
+
+template <int EB, bool PK, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
+  __shared__ int s_k, s_gb, s_skip;
+  __shared__ unsigned long long s_warp[kWarps];
+  __shared__ unsigned long long s_rank[2][kMaxCluster];
+  __shared__ unsigned long long s_scan[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = P.C, b = blockIdx.x / C, V = P.V, G = P.G;
+  const int rank = C > 1 ? (int)cluster_rank() : 0;
+  unsigned int flags = 0;
+  if (C > 1) cluster_arrive();  // waited for before the first store to a peer
+  // rows of this request
+  int gb;
+  size_t trow, drow;
+  if (PK) {
+    const int c0 = P.cu[b], c1 = P.cu[b + 1];
+    const bool ok = c0 >= 0 && c1 >= c0 && c1 - c0 <= G && c1 <= P.total;
+    gb = ok ? c1 - c0 : 0;
+    drow = (size_t)(c0 < 0 ? 0 : (c0 > P.total ? P.total : c0));
+    trow = drow + b;
+    if (!ok) flags |= SV_STATUS_BAD_GAMMA;
+  } else {
+    gb = P.gamma[b];
+    if (gb < 0 || gb > G) flags |= SV_STATUS_BAD_GAMMA;
+    gb = gb < 0 ? 0 : (gb > G ? G : gb);
+    drow = (size_t)b * G;
+    trow = (size_t)b * (G + 1);
+  }
+  const size_t last_u = PK ? trow + gb : trow + G;
+  float u_last = P.uniforms[last_u];
+  // the tests: one lane a draft, in every CTA of the cluster
+  if (warp == 0) {
+    bool ok = true;
+    int x = 0;
+    if (lane < gb) {
+      x = P.tokens[drow + lane];
+      if (x < 0 || x >= V) {
+        flags |= SV_STATUS_BAD_TOKEN;
+        x = x < 0 ? 0 : V - 1;
+      }
+      float p = load_one<EB>(P.target, (trow + lane) * V + x);
+      float q = P.draft ? load_one<EB>(P.draft, (drow + lane) * V + x) : 1.f;
+      float u = P.uniforms[trow + lane];
+      if (!(p >= 0.f && p <= 1.f)) {
+        flags |= SV_STATUS_BAD_PROB;
+        p = p > 1.f ? 1.f : 0.f;
+      }
+      if (!(q >= 0.f && q <= 1.f)) {
+        flags |= SV_STATUS_BAD_PROB;
+        q = q > 1.f ? 1.f : 0.f;
+      }
+      if (!(u >= 0.f && u < 1.f)) {
+        flags |= SV_STATUS_BAD_UNIFORM;
+        u = 0.f;
+      }
+      ok = q == 0.f || (double)u * (double)q < (double)p;
+    }
+    const unsigned int refused = __ballot_sync(0xffffffffu, lane < gb && !ok);
+    const int k = refused ? __ffs(refused) - 1 : gb;
+    const int xk = __shfl_sync(0xffffffffu, x, k < 32 ? k : 0);
+    if (lane == 0) {
+      s_k = k;
+      s_gb = gb;
+      s_skip = k < gb && !P.draft ? xk : -1;
+    }
+    if (rank == 0) {
+      if (lane <= G && lane != k) P.out[(size_t)b * (G + 1) + lane] = lane < k ? x : -1;
+      if (lane == 0) P.accepted[b] = k;
+    }
+  }
+  if (!(u_last >= 0.f && u_last < 1.f)) {
+    flags |= SV_STATUS_BAD_UNIFORM;
+    u_last = 0.f;
+  }
+  __syncthreads();
+  const int k = s_k;
+  const bool refused = k < s_gb;
+  Draw d;
+  d.p = P.target + (trow + k) * V * EB;
+  d.q = refused && P.draft ? P.draft + (drow + k) * V * EB : nullptr;
+  d.skip = s_skip;
+  // this warp's units of the row
+  constexpr int kUnit = 32 * (16 / EB);
+  const int units = (V + kUnit - 1) / kUnit, NW = C * kWarps;
+  const int w0 = rank * kWarps;
+  unsigned long long S = 0, before = 0;
+  int pass = 0;
+  for (;; ++pass) {
+    const int gw = w0 + warp;
+    const int u0 = (int)((long long)units * gw / NW), u1 = (int)((long long)units * (gw + 1) / NW);
+    const unsigned long long ws = d.q ? range_sum<EB, VEC, true>(d, V, u0, u1, flags)
+                                      : range_sum<EB, VEC, false>(d, V, u0, u1, flags);
+    if (lane == 0) s_warp[warp] = ws;
+    __syncthreads();
+    if (C > 1) {
+      if (pass == 0) cluster_wait();  // every peer runs
+      if (tid < C) {
+        unsigned long long mine = 0;
+        for (int w = 0; w < kWarps; ++w) mine = sat_add(mine, s_warp[w]);
+        store_to_rank(&s_rank[pass][rank], tid, mine);
+      }
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      if (tid == 0) {
+        unsigned long long mine = 0;
+        for (int w = 0; w < kWarps; ++w) mine = sat_add(mine, s_warp[w]);
+        s_rank[pass][0] = mine;
+      }
+      __syncthreads();
+    }
+    S = 0;
+    for (int r = 0; r < C; ++r) {
+      if (r == rank) before = S;
+      S = sat_add(S, s_rank[pass][r]);
+    }
+    // every residual weight 0: the draw is from p_k
+    if (S != 0 || !refused || pass == 1) break;
+    d.q = nullptr;
+    d.skip = -1;
+    __syncthreads();
+  }
+  if (S == 0 || S >= kCap) flags |= SV_STATUS_BAD_PROB;
+  const unsigned long long goal = scaled(u_last, S);
+  int32_t* drawn = P.out + (size_t)b * (G + 1) + k;
+  if (S == 0) {
+    if (rank == 0 && tid == 0) *drawn = V - 1;
+  } else if (goal >= before && goal < sat_add(before, s_rank[pass][rank])) {
+    // the warp whose range holds the target, then a thread of this CTA
+    unsigned long long c = before;
+    int w = 0;
+    for (; w < kWarps - 1; ++w) {
+      const unsigned long long n = sat_add(c, s_warp[w]);
+      if (goal < n) break;
+      c = n;
+    }
+    const int gw = w0 + w;
+    const int e0 = (int)((long long)units * gw / NW) * kUnit;
+    int e1 = (int)((long long)units * (gw + 1) / NW) * kUnit;
+    if (e1 > V) e1 = V;
+    const int per = (e1 - e0 + kThreads - 1) / kThreads;
+    const int i0 = e0 + tid * per, i1 = i0 + per < e1 ? i0 + per : e1;
+    unsigned int ignored = 0;
+    unsigned long long mine = 0;
+    for (int i = i0; i < i1; ++i) mine = sat_add(mine, weight_at<EB>(d, i, ignored));
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = sat_add(incl, v);
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    for (int v = 0; v < warp; ++v) c = sat_add(c, s_scan[v]);
+    const unsigned long long prev = __shfl_up_sync(0xffffffffu, incl, 1);
+    const unsigned long long from = lane ? sat_add(c, prev) : c;
+    if (goal >= from && goal < sat_add(from, mine)) {
+      unsigned long long at = from;
+      for (int i = i0; i < i1; ++i) {
+        at = sat_add(at, weight_at<EB>(d, i, ignored));
+        if (goal < at) {
+          *drawn = i;
+          break;
+        }
+      }
+    }
+  }
+  const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
+  if (lane == 0 && any) atomicOr(P.status, any);
+}
+
+// CTAs a request: the largest cluster of at most 8 that keeps the grid within
+// two CTAs an SM, so that a small batch still reads with the whole GPU.
+int cluster_for(int B) {
+  static std::atomic<int> cached{0};
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const int c0 = cached.load(std::memory_order_relaxed);
+  if ((c0 >> 16) == dev + 1) {
+    sms = c0 & 0xffff;
+  } else {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    cached.store(((dev + 1) << 16) | sms, std::memory_order_relaxed);
+  }
+  int C = kMaxCluster;
+  while (C > 1 && (long long)B * C > 2ll * sms) C >>= 1;
+  return C;
+}
+
+template <int EB, bool PK, bool VEC>
+int launch(ProbsParams P, cudaStream_t stream) {
+  P.C = cluster_for(P.B);
+  if (P.C <= 0) return SV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned int)P.B * (unsigned int)P.C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned int)P.C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, probs_kernel<EB, PK, VEC>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+int verify_probs(const void* target, const void* draft, sv_dtype dtype, int B, int G, int V,
+                 const int32_t* cu, int total, const int32_t* tokens, const int32_t* gamma,
+                 const float* uniforms, int32_t* out, int32_t* accepted, void* ws, size_t ws_bytes,
+                 sv_stream_t stream, bool packed) {
+  if (B < 0 || G < 0 || G > SV_MAX_GAMMA || V < 1 || V > SV_MAX_VOCAB || total < 0)
+    return SV_ERR_SCALAR;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_SCALAR;
+  if (!target || !uniforms || !out || !accepted || !ws || (packed ? !cu : !gamma)) return SV_ERR_NULL;
+  if ((packed ? total > 0 : G > 0) && !tokens) return SV_ERR_NULL;
+  const size_t eb = dtype == SV_BF16 ? 2 : 4;
+  if (ws_bytes < spec_verify_workspace_size(B, G, V)) return SV_ERR_WORKSPACE;
+  if (!sv::aligned(target, eb) || !sv::aligned(draft, eb) || !sv::aligned(tokens, 4) ||
+      !sv::aligned(gamma, 4) || !sv::aligned(cu, 4) || !sv::aligned(uniforms, 4) ||
+      !sv::aligned(out, 4) || !sv::aligned(accepted, 4) || !sv::aligned(ws, 256))
+    return SV_ERR_ALIGN;
+  if (B == 0) return SV_OK;
+  ProbsParams P;
+  P.target = static_cast<const char*>(target);
+  P.draft = static_cast<const char*>(draft);
+  P.B = B;
+  P.G = G;
+  P.V = V;
+  P.total = total;
+  P.C = 1;
+  P.tokens = tokens;
+  P.gamma = gamma;
+  P.cu = cu;
+  P.uniforms = uniforms;
+  P.out = out;
+  P.accepted = accepted;
+  P.status = static_cast<unsigned int*>(ws);
+  // 16-byte loads where every row starts on a 16-byte boundary
+  const bool vec = (size_t)V * eb % 16 == 0 && sv::aligned(target, 16) && sv::aligned(draft, 16);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == SV_BF16) {
+    if (packed) return vec ? launch<2, true, true>(P, s) : launch<2, true, false>(P, s);
+    return vec ? launch<2, false, true>(P, s) : launch<2, false, false>(P, s);
+  }
+  if (packed) return vec ? launch<4, true, true>(P, s) : launch<4, true, false>(P, s);
+  return vec ? launch<4, false, true>(P, s) : launch<4, false, false>(P, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_verify_sample_probs(const void* target_probs, const void* draft_probs, sv_dtype dtype,
+                             int B, int G, int V, const int32_t* draft_tokens,
+                             const int32_t* gamma, const float* uniforms, int32_t* out_tokens,
+                             int32_t* num_accepted, void* workspace, size_t ws_bytes,
+                             sv_stream_t stream) {
+  return verify_probs(target_probs, draft_probs, dtype, B, G, V, nullptr, 0, draft_tokens, gamma,
+                      uniforms, out_tokens, num_accepted, workspace, ws_bytes, stream, false);
+}
+
+int spec_verify_sample_probs_packed(const void* target_probs, const void* draft_probs,
+                                    sv_dtype dtype, int B, int G, int V, const int32_t* cu_draft,
+                                    int total_drafts, const int32_t* draft_tokens,
+                                    const float* uniforms, int32_t* out_tokens,
+                                    int32_t* num_accepted, void* workspace, size_t ws_bytes,
+                                    sv_stream_t stream) {
+  return verify_probs(target_probs, draft_probs, dtype, B, G, V, cu_draft, total_drafts,
+                      draft_tokens, nullptr, uniforms, out_tokens, num_accepted, workspace,
+                      ws_bytes, stream, true);
+}
+
+}  // extern "C"

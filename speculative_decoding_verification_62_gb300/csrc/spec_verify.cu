@@ -72,6 +72,7 @@
 #include <float.h>
 
 #include "spec_verify.h"
+#include "internal.h"
 
 namespace {
 
@@ -4743,3 +4744,5 @@ int spec_verify_cluster_size(sv_dtype dtype, int B, int G, int V, int greedy) {
 }
 
 }  // extern "C"
+
+unsigned long long sv::wait_limit_ns() { return g_wait_ns.load(); }

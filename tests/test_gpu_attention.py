@@ -1,0 +1,273 @@
+"""Attention over the paged cache against the definition in 64 bits, within the error
+that its roundings allow; everything in the pools that no row sees holds NaN."""
+import math
+
+import pytest
+import torch
+
+from operator_refs import attend, tolerance
+from speculative_decoding_verification_62_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+class Batch:
+    def __init__(self, lens, gam, Hq, Hk, D, page, dtype, prefix=0, layout="nhd", seed=1, scale_q=1.5,
+                 spare=2, device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        gc = torch.Generator().manual_seed(seed)
+        self.lens, self.gam, self.Hq, self.Hk, self.D, self.page, self.prefix = lens, gam, Hq, Hk, D, page, prefix
+        self.dtype = DT[dtype]
+        B = len(lens)
+        need = [-(-(n + x + 1) // page) for n, x in zip(lens, gam)]
+        pre = -(-prefix // page)
+        total = sum(need) + pre + spare
+        perm = torch.randperm(total, generator=gc).int()
+        table = torch.full((B, max(need) + 1), -9, dtype=torch.int32)
+        shape = (total, page, Hk, D) if layout == "nhd" else (total, Hk, page, D)
+        kp = torch.full(shape, math.nan, dtype=self.dtype, device=device)
+        vp = torch.full(shape, math.nan, dtype=self.dtype, device=device)
+        if layout == "hnd":
+            kp, vp = kp.transpose(1, 2), vp.transpose(1, 2)
+        at = pre
+        self.k, self.v = [], []
+
+        def fill(ids, n):
+            k = torch.randn((n, Hk, D), generator=g, device=device).to(self.dtype)
+            v = (torch.randn((n, Hk, D), generator=g, device=device) + 0.25).to(self.dtype)
+            t = torch.arange(n, device=device)
+            kp[ids.long().to(device)[t // page], t % page] = k
+            vp[ids.long().to(device)[t // page], t % page] = v
+            return k.double(), v.double()
+        self.prefix_table = perm[:pre].to(device)
+        self.pk, self.pv = fill(perm[:pre], prefix) if prefix else (None, None)
+        for b in range(B):
+            ids = perm[at:at + need[b]]
+            at += need[b]
+            table[b, :need[b]] = ids
+            k, v = fill(ids, lens[b] + gam[b] + 1)
+            self.k.append(k)
+            self.v.append(v)
+        self.T = sum(gam) + B
+        self.q = (torch.randn((self.T, Hq, D), generator=g, device=device) * scale_q).to(self.dtype)
+        self.cu = torch.tensor([0] + torch.tensor(gam).cumsum(0).tolist(), dtype=torch.int32, device=device)
+        self.cache = binding.PagedCache(kp, vp, table.to(device), torch.tensor(lens, dtype=torch.int32, device=device))
+
+    def run(self, mask=None, lse=True, scale=None, ws=None, out=None, q=None, status=0):
+        if ws is None:
+            ws = binding.make_attention_workspace(self.T, self.Hq, self.D)
+        if out is None:
+            out = torch.full((self.T, self.Hq, self.D), 77.0, dtype=self.dtype, device="cuda")
+        l = torch.full((self.T, self.Hq), 77.0, device="cuda") if lse else None
+        binding.spec_verify_attention(self.q if q is None else q, self.cache, self.cu, max(self.gam), out, ws,
+                                      prefix_table=self.prefix_table, prefix_len=self.prefix, scale=scale,
+                                      draft_mask=mask, lse=l)
+        if status is not None:
+            assert binding.spec_verify_status(ws) == status
+        return out, l
+
+    def check(self, out, lse, mask=None, scale=None, only=None):
+        scale = self.D ** -0.5 if scale is None else scale
+        row = 0
+        worst = 0.0
+        for b, (n, x) in enumerate(zip(self.lens, self.gam)):
+            rows = slice(row, row + x + 1)
+            row += x + 1
+            if only is not None and b not in only:
+                continue
+            k, v = self.k[b], self.v[b]
+            i, j = torch.arange(x + 1, device="cuda")[:, None], torch.arange(n + x + 1, device="cuda")[None, :]
+            if mask is None:
+                seen = j <= n + i
+            else:
+                word = mask[rows].long()[:, None]
+                seen = (j < n) | (((word >> (j - n).clamp_min(0)) & 1) == 1)
+            if self.prefix:
+                k, v = torch.cat([self.pk, k]), torch.cat([self.pv, v])
+                seen = torch.cat([torch.ones((x + 1, self.prefix), dtype=torch.bool, device="cuda"), seen], 1)
+            o, l, spread, size = attend(self.q[rows].double(), k, v, seen, scale)
+            tol, tl = tolerance(o, l, spread, size, k.shape[0], self.D, float(v.abs().max()), self.dtype)
+            err = (out[rows].double() - o).abs()
+            assert not (err > tol).any() and not torch.isnan(err).any(), (
+                b, int((~(err <= tol)).sum()), float((err / tol).max()))
+            worst = max(worst, float((err / tol).max()))
+            if lse is not None:
+                g = lse[rows].double()
+                empty = torch.isinf(l)
+                assert torch.equal(g[empty], l[empty])
+                assert not ((g - l).abs()[~empty] > tl[~empty]).any()
+        return worst
+
+
+CASES = {
+    # lens, gamma, Hq, Hk, D, page, dtype, prefix, layout
+    "one_token": ([0], [0], 1, 1, 64, 16, "bf16", 0, "nhd"),
+    "one_tile": ([100], [3], 8, 2, 128, 16, "bf16", 0, "nhd"),
+    "tile_borders": ([127, 128, 124, 255, 0, 1], [0, 0, 3, 1, 5, 7], 4, 1, 128, 32, "bf16", 0, "nhd"),
+    "mha_f16": ([30, 500, 77], [2, 0, 4], 6, 6, 64, 16, "f16", 0, "hnd"),
+    "odd_dim_80": ([300, 11], [4, 1], 10, 2, 80, 64, "f16", 0, "nhd"),
+    "dim_8": ([300, 11], [4, 1], 4, 2, 8, 64, "bf16", 0, "nhd"),
+    "dim_40_group_3": ([130, 400], [6, 2], 9, 3, 40, 32, "bf16", 0, "hnd"),
+    "group_7": ([700, 3, 260], [5, 7, 0], 14, 2, 128, 128, "bf16", 0, "nhd"),
+    "group_128": ([200, 40], [1, 3], 128, 1, 64, 16, "bf16", 0, "nhd"),
+    "group_96": ([200, 40], [1, 3], 96, 1, 128, 16, "f16", 0, "nhd"),
+    "big_pages": ([1000, 20, 300], [3, 3, 3], 8, 2, 128, 512, "bf16", 0, "hnd"),
+    "split_long": ([20000], [3], 8, 1, 128, 64, "bf16", 0, "nhd"),
+    "split_long_f16_64": ([9001, 17], [7, 2], 16, 2, 64, 16, "f16", 0, "nhd"),
+    "many": ([(37 * b) % 400 for b in range(330)], [b % 4 for b in range(330)], 4, 2, 64, 16, "bf16", 0, "nhd"),
+    "prompt": ([0, 64], [399, 150], 4, 2, 128, 16, "bf16", 0, "nhd"),
+    "prompt_group_3": ([5], [600], 3, 1, 64, 32, "f16", 0, "nhd"),
+    "prefix_1": ([40, 0, 9], [2, 3, 0], 8, 2, 128, 16, "bf16", 1, "nhd"),
+    "prefix_small_batch": ([40, 0, 9], [2, 3, 0], 8, 2, 128, 16, "bf16", 300, "nhd"),
+    "prefix_two_blocks": ([b * 9 for b in range(40)], [b % 6 for b in range(40)], 8, 1, 128, 16, "bf16", 1000, "hnd"),
+    "prefix_three_blocks_f16": ([b * 3 for b in range(70)], [3] * 70, 4, 2, 64, 32, "f16", 2051, "nhd"),
+    "prefix_many_heads": ([b * 30 for b in range(30)], [4] * 30, 32, 8, 128, 64, "bf16", 4096, "nhd"),
+    "prefix_group_5": ([b * 30 for b in range(30)], [b % 5 for b in range(30)], 20, 4, 96, 128, "bf16", 1500, "nhd"),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_against_the_definition(name):
+    lens, gam, Hq, Hk, D, page, dt, prefix, layout = CASES[name]
+    w = Batch(lens, gam, Hq, Hk, D, page, dt, prefix, layout)
+    out, lse = w.run()
+    worst = w.check(out, lse)
+    print(name, "worst error over tolerance", worst)
+    again, lse2 = w.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)  # bit for bit
+
+
+@pytest.mark.parametrize("prefix", [0, 130])
+def test_draft_masks(prefix):
+    """Tree drafts: words with holes, words that name later rows, empty words."""
+    w = Batch([0, 100, 128, 250], [7, 31, 5, 9], 8, 2, 128, 16, "bf16", prefix)
+    g = torch.Generator().manual_seed(4)
+    mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (w.T,), generator=g, dtype=torch.int64).int().cuda()
+    mask[1] = 0
+    mask[20] = 0
+    words = mask.long() & 0xffffffff
+    out, lse = w.run(mask=mask)
+    w.check(out, lse, mask=words)
+    if prefix == 0:  # no token before, an empty word: nothing is seen
+        assert (out[1] == 0).all() and torch.isinf(lse[1]).all() and (lse[1] < 0).all()
+    # the causal words give what no mask gives
+    pos = torch.cat([torch.arange(x + 1) for x in w.gam])
+    causal = ((torch.ones(w.T, dtype=torch.int64) << (pos + 1)) - 1)
+    causal = torch.where(causal >= 2 ** 31, causal - 2 ** 32, causal).int().cuda()
+    a, la = w.run(mask=causal)
+    b, lb = w.run()
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_strided_queries_scale_and_large_scores():
+    w = Batch([50, 600], [3, 1], 8, 2, 64, 16, "bf16", 0)
+    wide = torch.randn((w.T, 14, 64), device="cuda").to(w.dtype)
+    q = wide[:, 3:11]
+    w.q = q
+    out, lse = w.run(scale=2.0)
+    w.check(out, lse, scale=2.0)
+    w.q = q * 20.0  # nearly one-hot weights, scores of hundreds
+    out, lse = w.run()
+    w.check(out, lse)
+
+
+def test_rising_scores_move_the_maximum():
+    """Keys whose scores grow along the sequence: the running maximum moves in every tile."""
+    w = Batch([1500, 900], [2, 6], 4, 1, 128, 16, "bf16", 700, scale_q=1.0)
+    page, c = w.page, w.cache
+    up = torch.ones(128, device="cuda")
+    w.q = (up * 1.0).expand(w.T, 4, 128).contiguous().to(w.dtype)
+
+    def raise_(k, ids):
+        t = torch.arange(k.shape[0], device="cuda")
+        k += (t.double() / 40.0)[:, None, None]
+        k.copy_(k.to(w.dtype).double())
+        c.k_pages[ids.long()[t // page], t % page] = k.to(w.dtype)
+    raise_(w.pk, w.prefix_table)
+    for b in range(2):
+        raise_(w.k[b], c.page_table[b])
+    out, lse = w.run()
+    w.check(out, lse)
+
+
+def test_infinite_scores_and_nan_stay_in_their_rows():
+    w = Batch([60, 200], [2, 1], 4, 2, 64, 16, "f16", 0)
+    w.q[1, 2] = math.nan
+    out, lse = w.run()
+    assert torch.isnan(out[1, 2]).all() and torch.isnan(lse[1, 2])
+    keep = torch.ones((w.T, 4), dtype=torch.bool)
+    keep[1, 2] = False
+    assert not torch.isnan(out[keep.cuda()]).any()
+    w.q[1, 2] = 0.0
+    out, lse = w.run()
+    w.check(out, lse)
+    # a key of -inf times a positive query: weight 0
+    w = Batch([60], [2], 1, 1, 64, 16, "bf16", 0)
+    w.q.abs_()
+    ids = w.cache.page_table[0].long()
+    w.cache.k_pages[ids[0], 5] = -math.inf
+    w.k[0][5] = -1e30
+    out, lse = w.run()
+    w.k[0][5] = -1e3
+    w.check(out, lse)
+
+
+def test_bad_requests_are_left_out():
+    S = {n: b for b, n in binding.STATUS_BITS.items()}
+    w = Batch([60, 200, 90], [2, 1, 3], 4, 2, 64, 16, "bf16", 0)
+    w.cache.kv_len[1] = 10 ** 6
+    out, lse = w.run(status=S["BAD_LENGTH"])
+    w.check(out, lse, only=[0, 2])
+    assert (out[3:5] == 77.0).all() and (lse[3:5] == 77.0).all()
+    w = Batch([60, 200, 90], [2, 1, 3], 4, 2, 64, 16, "bf16", 40)
+    cu = w.cu.clone()
+    w.cu[1] = 50
+    out, lse = w.run(status=S["BAD_GAMMA"])
+    w.check(out, lse, only=[2])
+    assert (out[:5] == 77.0).all()
+    w.cu.copy_(cu)
+    w.cache.page_table[0, 1] = 10 ** 6
+    out, lse = w.run(status=S["BAD_PAGE"])
+    w.check(out, lse, only=[1, 2])
+
+
+def test_two_workspaces_two_streams_and_graphs():
+    a = Batch([3000, 20, 500], [3, 0, 2], 8, 2, 128, 16, "bf16", 300, seed=2)
+    b = Batch([40, 2000], [1, 5], 6, 6, 64, 32, "f16", 0, seed=3)
+    ra, rb = a.run(), b.run()
+    wa, wb = (binding.make_attention_workspace(x.T, x.Hq, x.D) for x in (a, b))
+    oa, ob = torch.empty_like(ra[0]), torch.empty_like(rb[0])
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a.run(ws=wa, out=oa, lse=False, status=None)
+        with torch.cuda.stream(s2):
+            b.run(ws=wb, out=ob, lse=False, status=None)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, ra[0]) and torch.equal(ob, rb[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run(ws=wa, out=oa, lse=False, status=None)
+    oa.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(oa, ra[0])
+    # the captured call follows the lengths on the device
+    a.cache.kv_len.copy_(torch.tensor([129, 7, 0]))
+    a.lens = [129, 7, 0]
+    a.k = [k[:n + x + 1] for k, n, x in zip(a.k, a.lens, a.gam)]
+    a.v = [v[:n + x + 1] for v, n, x in zip(a.v, a.lens, a.gam)]
+    graph.replay()
+    torch.cuda.synchronize()
+    a.check(oa, None)
+
+
+def test_a_dirty_workspace_and_a_larger_one():
+    w = Batch([3000, 20], [3, 0], 8, 2, 128, 16, "bf16", 100)
+    ref, _ = w.run()
+    ws = torch.full((binding.make_attention_workspace(w.T + 50, 8, 128).numel(),), 255, dtype=torch.uint8, device="cuda")
+    ws[:4] = 0
+    out, _ = w.run(ws=ws)
+    assert torch.equal(ref, out)
