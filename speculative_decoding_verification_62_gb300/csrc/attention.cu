@@ -122,7 +122,10 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // or another warp of the CTA gave up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
                                          volatile int* abort) {
-  if (bar_try(bar, parity)) return true;
+  // ordinary waits end within these tries (a try suspends the warp for a while
+  // itself) and read no timer
+  for (int i = 0; i < 256; ++i)
+    if (bar_try(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
   for (;;) {
     for (int i = 0; i < 64; ++i)
@@ -180,12 +183,18 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
       : SV_R8(v, 0), SV_R8(v, 8), SV_R8(v, 16), SV_R8(v, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      SV_W8(v, 0), SV_W8(v, 8), SV_W8(v, 16), SV_W8(v, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SV_R8(v, 0), SV_R8(v, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      SV_W8(v, 0), SV_W8(v, 8)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_load() {
@@ -199,6 +208,33 @@ __device__ __forceinline__ void tmem_loaded32(uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_loaded16(uint32_t* v) {
+  asm volatile("" : SV_T8(v, 0), SV_T8(v, 8));
+}
+// pairs of floats in one instruction
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -551,30 +587,42 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       ++ns;
       if (active) {
         fence_after();
-        uint32_t v[kTile];
-#pragma unroll
-        for (int x = 0; x < kTile; x += 32) tmem_load32(s_col + x, v + x);
-        tmem_wait_load();
-#pragma unroll
-        for (int x = 0; x < kTile; x += 32) tmem_loaded32(v + x);
         const int key0 = (p.t0 + i) * kTile;
-        if (key0 + kTile > free) {
+        const bool masked = key0 + kTile > free;
+        // keys [key0 + 32 ch, + 32) that this row does not see
+        auto hide = [&](uint32_t* v, int ch) {
+          const int at = key0 + 32 * ch;
+          uint32_t see;  // bit x: key at + x is seen
           if (!p.prefix && P.mask) {
-#pragma unroll
-            for (int x = 0; x < kTile; ++x) {
-              const int d = key0 + x - p.kv;
-              if (d >= 0 && (d >= 32 || !((word >> (d & 31)) & 1u))) v[x] = __float_as_uint(ninf);
-            }
+            const int d = at - p.kv;  // the chunk's first key in the step's rows
+            see = d <= -32 ? ~0u : d < 0 ? (word << -d) | ((1u << -d) - 1u) : d < 32 ? word >> d : 0u;
           } else {
+            const int n = limit - at;
+            see = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u;
+          }
 #pragma unroll
-            for (int x = 0; x < kTile; ++x)
-              if (key0 + x >= limit) v[x] = __float_as_uint(ninf);
+          for (int x = 0; x < 32; ++x)
+            if (!((see >> x) & 1u)) v[x] = __float_as_uint(ninf);
+        };
+        // S is read twice, 32 columns at a time, the next ones on their way:
+        // for the maximum, then for the weights (128 values held at once spill)
+        uint32_t v[2][32];
+        float mx0 = ninf, mx1 = ninf;
+        tmem_load32(s_col, v[0]);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t* u = v[ch & 1];
+          tmem_wait_load();
+          tmem_loaded32(u);
+          tmem_load32(s_col + ((ch + 1) & 3) * 32, v[(ch + 1) & 1]);
+          if (masked) hide(u, ch);
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            mx0 = max3(mx0, __uint_as_float(u[x]), __uint_as_float(u[x + 1]));
+            mx1 = max3(mx1, __uint_as_float(u[x + 2]), __uint_as_float(u[x + 3]));
           }
         }
-        float mx[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-        for (int x = 0; x < kTile; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(v[x]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * P.sl2;
+        const float top = fmaxf(mx0, mx1) * P.sl2;
         if (i < step) {
           m = top;
         } else {
@@ -582,32 +630,47 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           if (__any_sync(0xffffffffu, grow)) {
             const float f = grow ? (m == ninf ? 0.f : exp2_fast(m - top)) : 1.f;
             // the products so far are complete: S of this tile came after them
-            for (int x = 0; x < DP; x += 32) {
-              uint32_t o[32];
-              tmem_load32(o_col + wg * kTile + x, o);
+            for (int x = 0; x < DP; x += 16) {
+              uint32_t o[16];
+              tmem_load16(o_col + wg * kTile + x, o);
               tmem_wait_load();
-              tmem_loaded32(o);
+              tmem_loaded16(o);
 #pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_store32(o_col + wg * kTile + x, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_store16(o_col + wg * kTile + x, o);
             }
             l *= f;
             if (grow) m = top;
           }
         }
-        const float sub = m == ninf ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t sub = pair(m == ninf ? 0.f : -m, m == ninf ? 0.f : -m);
+        const uint64_t sl2 = pair(P.sl2, P.sl2);
+        uint64_t sum0 = 0, sum1 = 0;  // two pairs of zeros
 #pragma unroll
-        for (int x = 0; x < kTile; x += 2) {
-          const float a = exp2_fast(fmaf(__uint_as_float(v[x]), P.sl2, -sub));
-          const float b = exp2_fast(fmaf(__uint_as_float(v[x + 1]), P.sl2, -sub));
-          sum[x & 2] += a;
-          sum[(x & 2) + 1] += b;
-          v[x / 2] = Type<T>::pack(a, b);
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t* u = v[ch & 1];
+          tmem_wait_load();
+          tmem_loaded32(u);
+          if (ch < 3) tmem_load32(s_col + (ch + 1) * 32, v[(ch + 1) & 1]);
+          if (masked) hide(u, ch);
+          uint32_t w16[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            float a, b, e, f;
+            unpair(pair_fma(pair(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), sl2, sub), a, b);
+            unpair(pair_fma(pair(__uint_as_float(u[x + 2]), __uint_as_float(u[x + 3])), sl2, sub), e, f);
+            a = exp2_fast(a), b = exp2_fast(b), e = exp2_fast(e), f = exp2_fast(f);
+            sum0 = pair_add(sum0, pair(a, b));
+            sum1 = pair_add(sum1, pair(e, f));
+            w16[x / 2] = Type<T>::pack(a, b);
+            w16[x / 2 + 1] = Type<T>::pack(e, f);
+          }
+          // over columns of S that are read already
+          tmem_store16(s_col + ch * 16, w16);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_store32(s_col, v);
-        tmem_store32(s_col + 32, v + 32);
+        float a, b;
+        unpair(pair_add(sum0, sum1), a, b);
+        l += a + b;
         tmem_wait_store();
         fence_before();
       }
