@@ -10,24 +10,27 @@
 // read once a request, and the prefix's once for all requests.
 //
 // Work: a unit is (request, block of query rows, key head) over the request's
-// own keys, or (pair of blocks of all requests' rows, key head) over the
-// prefix.  The units' tiles of 128 keys, prefix first, form one list, and each
-// of the CTAs (one an SM) takes an equal contiguous share of it, so a batch of
-// any raggedness, or one long request, loads every SM alike.  A unit that
-// crosses a share's border leaves one part a CTA; combine_kernel joins them
-// (and the prefix with the own keys) by their sums.  No part is waited for
-// inside a kernel, and parts are joined in list order: results repeat bit for
-// bit.
+// own keys, or (block or pair of blocks of all requests' rows, key head) over
+// the prefix.  Blocks are 128 rows: tokens x heads of the key head's group.  The
+// units' tiles of 64 keys form two lists, A (pairs of blocks over the prefix) and
+// B (everything else).  The CTAs (one an SM) are dealt out to A and B by their
+// weights, and each CTA of A, and each of a B CTA's two streams, takes an equal
+// contiguous share of its list, so a batch of any raggedness, or one long
+// request, loads every SM alike.  A unit that crosses a share's border leaves
+// one part a share; combine_kernel joins them (and the prefix with the own
+// keys) by their sums.  No part is waited for inside a kernel, and parts are
+// joined in list order: results repeat bit for bit.
 //
-// A CTA: two softmax warpgroups, a copy warp and a matrix warp.  Query blocks
-// are 128 rows (tokens x heads of the key head's group).  S = Q K^T and
-// O += P V are tcgen05 products with S, P and O in tensor memory: two streams
-// of (S, O), 512 columns.  With two row blocks (prefix) each stream has one
-// and both read every tile; with one, the streams take the tiles in turn and
-// are joined at the end, so that one stream's softmax runs beside the other's
-// products.  Keys and values arrive by TMA, a page (at most 128 tokens) and 64
-// values a box, in a ring of slots with 128-byte swizzle; the layout in the
-// page pool is only the tensor map's strides.
+// A CTA holds two streams.  A stream is a softmax warpgroup, a copy warp, a
+// matrix warp, a query tile in shared memory and 256 columns of tensor memory:
+// two score tiles S (128 rows x 64 keys) and the output O.  S = Q K^T and O += P V
+// are tcgen05 products; P overwrites its S.  With two score tiles the product
+// of the next keys runs beside the softmax.  In a B CTA the streams are
+// independent (a ring of five 64-key slots each): one stream's start and end of
+// a unit hide behind the other's.  In an A CTA each stream has one block and
+// both read every key and value slot of one ring of ten.  Keys and values
+// arrive by TMA, a page (at most 64 tokens) and 64 values a box, with 128-byte
+// swizzle; the layout of the page pool is only the tensor map's strides.
 //
 // S and the sums are 32 bits.  P is rounded to the cache's 16-bit type for the
 // product (at most half a step of a weight, below the rounding of the output's
@@ -48,20 +51,25 @@
 
 namespace {
 
-constexpr int kTile = 128;      // keys a tile, rows a block
-constexpr int kThreads = 320;   // warps 0-3 and 4-7: softmax; 8: copies; 9: products
-constexpr int kMaxCtas = 160;   // shares of the tile list (partial slots are sized for this)
-constexpr int kSlotRows = 256;
+constexpr int kRows = 128;      // rows a block
+constexpr int kTile = 64;       // keys a tile
+constexpr int kThreads = 384;   // warps 0-3, 4-7: softmax; 8, 10: copies; 9, 11: products
+constexpr int kMaxCtas = 160;   // CTAs at most (the slots of parts are sized for this)
+constexpr int kSlots = 4 * kMaxCtas;  // parts: two a stream
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
 constexpr int kControl = 3072;  // barriers and small tables behind the tiles
+// Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs.
+constexpr int kCostA = 10, kCostB = 9;
 
 template <int DP>
 struct Shape {
   static constexpr int halves = DP / 64;
+  static constexpr int q_bytes = kRows * DP * 2;
+  static constexpr int q_half = kRows * 128;     // 64 values of every row
   static constexpr int tile_bytes = kTile * DP * 2;
-  static constexpr int half_bytes = kTile * 128;  // 64 values of every token
-  static constexpr int slots = DP == 128 ? 5 : 8;
-  static constexpr int smem = (slots + 2) * tile_bytes + kControl;
+  static constexpr int half_bytes = kTile * 128;
+  static constexpr int slots = 10;               // in all; five a stream in B
+  static constexpr int smem = 2 * q_bytes + slots * tile_bytes + kControl;
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
@@ -72,16 +80,16 @@ struct AttnParams {
   const int32_t* kv_len;
   const int32_t* cu;
   const int32_t* prefix_table;
-  int prefix_len, prefix_tiles, prefix_blocks, prefix_units;
+  int prefix_len, prefix_tiles, pairs, odd;  // pairs of row blocks over the prefix, and a single one
   const uint32_t* mask;
   float sl2;  // scale log2(e)
   char* out;
   float* lse;
   unsigned int* status;
-  long long* starts;   // [B + 1]: first tile of each request, and the total
+  long long* starts;   // [B + 1]: first tile of each request in list B, and the list's end
   float* dense[2];     // own, prefix: rows of whole units [T * Hq][DP]
   float* dense_lse[2];
-  float* slot;         // [2 * kMaxCtas][kSlotRows][DP]
+  float* slot;         // [kSlots][kRows][DP]
   float* slot_lse;
   unsigned long long wait_ns;
 };
@@ -151,18 +159,50 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One thread of the warp, the same one at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+// D = A B (+ D) over four steps of 16 values, A and B in shared memory, both
+// K-major: a step is 32 bytes on.  The steps stand in one block of text so that
+// the operands move to uniform registers once, not at every product.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+// D = A B (+ D) over one step, or four: A in tensor memory (a step is 8
+// columns), B in shared memory with its 16 rows of 128 bytes a step.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -195,6 +235,14 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
       SV_W8(v, 0), SV_W8(v, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      SV_W8(v, 0), SV_W8(v, 8), SV_W8(v, 16), SV_W8(v, 24)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_load() {
@@ -271,7 +319,7 @@ struct Type<__half> {
 // 32-bit accumulators, A and B of one 16-bit type
 __host__ __device__ constexpr uint32_t instr_desc(uint32_t fmt, uint32_t n, bool b_mn) {
   return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn ? 1u : 0u) << 16) | ((n / 8) << 17) |
-         ((uint32_t)(kTile / 16) << 24);
+         ((uint32_t)(kRows / 16) << 24);
 }
 
 // ---------------------------------------------------------------------------
@@ -307,25 +355,50 @@ __device__ __forceinline__ long long request_tiles(const AttnParams& P, const Re
   return t * P.Hk;
 }
 
-// One CTA's run of tiles of one unit.
+// How the lists are dealt out.
+struct Plan {
+  long long a, b;          // tiles of the lists
+  long long per_a, per_b;  // of a CTA's share of A, of a stream's share of B
+  int ctas_a, ctas_b;
+};
+__device__ __forceinline__ Plan make_plan(const AttnParams& P, long long b_tiles, int ctas) {
+  Plan L;
+  L.a = (long long)P.Hk * P.pairs * P.prefix_tiles;
+  L.b = b_tiles;
+  const long long wa = L.a * kCostA, wb = L.b * kCostB;
+  int na = L.a == 0 ? 0 : L.b == 0 ? ctas : (int)((ctas * wa + (wa + wb) / 2) / (wa + wb));
+  if (L.a > 0 && na < 1) na = 1;
+  if (L.b > 0 && na > ctas - 1) na = ctas - 1;
+  L.ctas_a = na;
+  L.ctas_b = ctas - na;
+  L.per_a = na ? (L.a + na - 1) / na : 0;
+  L.per_b = L.ctas_b ? (L.b + 2 * L.ctas_b - 1) / (2 * L.ctas_b) : 0;
+  return L;
+}
+// tiles of list B before the requests' own
+__device__ __forceinline__ long long single_tiles(const AttnParams& P) {
+  return (long long)P.Hk * P.odd * P.prefix_tiles;
+}
+
+// A run of tiles of one unit.
 struct Piece {
-  bool prefix, two;  // two row blocks, one a stream; else the streams share one
+  bool prefix;
   int b, h;
-  int row0, ntok;    // first row and rows of the block(s)
-  int kv;            // own: keys before the step; row i of the block sees kv + first + i + 1
-  int first;         // own: the block's first row within the request
+  int row0, ntok;    // first row and rows of the block (A: of stream 0's block)
+  int kv, first;     // own: keys before the step, the block's first row within the request:
+                     // row i of the block sees keys below kv + first + i + 1
   int keys;          // keys of the unit
   int t0, t1;        // tiles [t0, t1) of unit_t
   int unit_t;
 };
 
-// Walks a CTA's share.  Every role walks it alone, from the same start.
+// Walks a share.  Every role walks it alone, from the same start.
 struct Walk {
   long long left;
-  bool prefix;
-  int unit;         // prefix unit
-  int b, rb, h;     // own unit
-  int off;          // first tile within the unit
+  bool pair, single;  // list A; the prefix's single block in list B
+  int unit;           // prefix unit
+  int b, rb, h;       // own unit
+  int off;            // first tile within the unit
   Req r;
 
   __device__ __forceinline__ void load_request(const AttnParams& P) {
@@ -339,29 +412,27 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const AttnParams& P, Piece& p) {
     if (left <= 0) return false;
-    if (prefix && unit >= P.prefix_units) {
-      prefix = false;
-      b = rb = h = off = 0;
+    if (single && unit >= P.Hk) {
+      single = false;
+      b = rb = h = 0;
       load_request(P);
     }
-    if (prefix) {
-      p.prefix = true;
+    p.prefix = pair || single;
+    if (p.prefix) {
       p.b = 0;
-      p.h = unit / P.prefix_blocks;
-      p.row0 = (unit - p.h * P.prefix_blocks) * 2 * P.tpq;
-      p.ntok = P.T - p.row0 < 2 * P.tpq ? P.T - p.row0 : 2 * P.tpq;
-      p.two = p.ntok > P.tpq;
+      p.h = pair ? unit / P.pairs : unit;
+      p.row0 = (pair ? (unit - p.h * P.pairs) * 2 : 2 * P.pairs) * P.tpq;
+      p.ntok = P.T - p.row0;
       p.kv = p.first = 0;
       p.keys = P.prefix_len;
       p.unit_t = P.prefix_tiles;
     } else {
       if (b >= P.B) return false;
-      p.prefix = p.two = false;
       p.b = b;
       p.h = h;
       p.first = rb * P.tpq;
       p.row0 = r.row0 + p.first;
-      p.ntok = r.n - p.first < P.tpq ? r.n - p.first : P.tpq;
+      p.ntok = r.n - p.first;
       p.kv = r.kv;
       p.keys = block_keys(P, r, rb);
       p.unit_t = tiles_of(p.keys);
@@ -370,7 +441,7 @@ struct Walk {
     p.t1 = left < p.unit_t - off ? off + (int)left : p.unit_t;
     left -= p.t1 - p.t0;
     off = 0;
-    if (prefix) {
+    if (p.prefix) {
       ++unit;
     } else if (++h == P.Hk) {
       h = 0;
@@ -385,64 +456,57 @@ struct Walk {
 };
 
 struct Control {
-  uint64_t kv_full[8], kv_empty[8], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full, o_free,
-      ml_ready, drain;
+  uint64_t kv_full[10], kv_empty[10];
+  // of each stream
+  uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], pv_done[2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
   int abort;
-  int start_b, start_prefix, start_unit, start_off, per_b;
-  long long start_rem, left;
+  int start_b[2];
+  long long start_rem[2];
+  unsigned int q_copied[2], kv_copied[2];
   long long scan[kThreads / 32];
-  float2 ml[2][kTile];
 };
 static_assert(sizeof(Control) <= kControl, "control block");
 
-// ---------------------------------------------------------------------------
-// Roles
-// ---------------------------------------------------------------------------
+// Where a stream's ring entries lie: A shares ten slots, B has five a stream.
+template <bool PAIR>
+__device__ __forceinline__ uint32_t slot_of(int s, unsigned int e) {
+  return PAIR ? e % 10u : s * 5u + e % 5u;
+}
+template <bool PAIR>
+__device__ __forceinline__ uint32_t turn_of(unsigned int e) {  // parity of the slot's use
+  return (PAIR ? e / 10u : e / 5u) & 1u;
+}
 // The order of a piece's tiles in the ring: keys one tile ahead of values.
 __device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_entry(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
 
-template <int DP>
-__device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* c, uint32_t q_smem,
-                                          uint32_t ring, const CUtensorMap* qmap,
-                                          const CUtensorMap* qmap_prefix, const CUtensorMap* kmap,
-                                          const CUtensorMap* vmap, unsigned int& entry,
-                                          unsigned int& qn) {
+// ---------------------------------------------------------------------------
+// Roles
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const AttnParams& P, Control* c) {
+  const bool ok = bar_wait(smem_addr(bar), parity, P.wait_ns, &c->abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Copies: B: stream s's queries, keys and values; A: warp 0 both streams' queries
+// and the keys, warp 1 the values.
+template <int DP, bool PAIR>
+__device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t q_smem,
+                                          uint32_t ring, const CUtensorMap* qmap, const CUtensorMap* kmap,
+                                          const CUtensorMap* vmap) {
   using S = Shape<DP>;
   const int lane = threadIdx.x & 31;
-  unsigned int flags = 0;
+  unsigned int flags = 0, base = 0, qn = 0, last = 0;
   Piece p;
   bool ok = true;
   while (ok && w.next(P, p)) {
-    // the block's query rows: [token][head of the group] in 128-byte rows
-    for (int s = 0; ok && s < (p.two ? 2 : 1); ++s, ++qn) {
-      const uint32_t slot = qn & 1;
-      ok = bar_wait(smem_addr(&c->q_empty[slot]), ((qn >> 1) & 1) ^ 1, P.wait_ns, &c->abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t bar = smem_addr(&c->q_full[slot]);
-      const int box = p.prefix ? P.tpq : P.own_tok;
-      if (lane == 0) {
-        bar_expect(bar, (uint32_t)(S::halves * 128 * P.group * box));
-        for (int x = 0; x < S::halves; ++x)
-          tma_load(q_smem + slot * S::tile_bytes + x * S::half_bytes, p.prefix ? qmap_prefix : qmap, bar,
-                   x * 64, 0, p.h, p.row0 + s * P.tpq);
-      }
-    }
     const int n = p.t1 - p.t0;
-    for (int e = 0; ok && e < 2 * n; ++e, ++entry) {
-      const bool is_v = e == 2 * n - 1 || (e > 0 && !(e & 1));
-      const int i = is_v ? (e == 2 * n - 1 ? n - 1 : e / 2 - 1) : (e + 1) / 2;
-      const int key0 = (p.t0 + i) * kTile;
-      const int keys = p.keys - key0 < kTile ? p.keys - key0 : kTile;
-      const int pages = (keys + P.box_rows - 1) / P.box_rows;  // boxes of at most a page
-      const int boxes = pages * S::halves;
-      // this lane's page, looked up before the wait for the slot
-      const int pg = lane / S::halves;
+    // a lane's page of tile i (a box is at most a page)
+    auto page_of = [&](int i) {
+      const int key = (p.t0 + i) * kTile + lane * P.box_rows;
       int id = 0;
-      if (lane < boxes) {
-        const int key = key0 + pg * P.box_rows;
+      if (lane * P.box_rows < kTile && key < p.keys) {
         id = p.prefix ? P.prefix_table[key >> P.page_shift]
                       : P.table[(size_t)p.b * P.max_pages + (key >> P.page_shift)];
         if (id < 0 || id >= P.num_pages) {
@@ -450,224 +514,245 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
           id = P.num_pages;  // past the pool: the copy fills zeros
         }
       }
-      const uint32_t slot = entry % S::slots;
-      ok = bar_wait(smem_addr(&c->kv_empty[slot]), ((entry / S::slots) & 1) ^ 1, P.wait_ns, &c->abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t bar = smem_addr(&c->kv_full[slot]);
-      if (lane == 0) bar_expect(bar, (uint32_t)(boxes * 128 * P.box_rows));
-      __syncwarp();
-      if (lane < boxes) {
-        const int half = lane - pg * S::halves;
-        const int key = key0 + pg * P.box_rows;
-        tma_load(ring + slot * S::tile_bytes + half * S::half_bytes + pg * P.box_rows * 128,
-                 is_v ? vmap : kmap, bar, half * 64, key & (P.page_size - 1), p.h, id);
+      return id;
+    };
+    // pages of the tile of the next entry and, in B, of the one before it
+    int at = 0, id = page_of(0), before = 0;
+    if (!PAIR || s == 0) {
+      // the block's query rows: [token][head of the group] in 128-byte rows
+#pragma unroll
+      for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
+        const int qs = PAIR ? x : s;
+        if (!(ok = warp_wait(&c->q_empty[qs], (qn & 1) ^ 1, P, c))) break;
+        const uint32_t bar = smem_addr(&c->q_full[qs]);
+        if (elect_one()) {
+          bar_expect(bar, (uint32_t)(S::halves * 128 * P.group * (p.prefix ? P.tpq : P.own_tok)));
+          for (int y = 0; y < S::halves; ++y)
+            tma_load(q_smem + qs * S::q_bytes + y * S::q_half, qmap + (p.prefix ? 1 : 0), bar, y * 64, 0, p.h,
+                     p.row0 + x * P.tpq);
+        }
+        __syncwarp();
       }
+      ++qn;
     }
+    for (int y = 0; ok && y < 2 * n; ++y) {
+      const bool is_v = y == 2 * n - 1 || (y > 0 && !(y & 1));
+      if (PAIR && is_v != (s == 1)) continue;
+      const int i = is_v ? (y == 2 * n - 1 ? n - 1 : y / 2 - 1) : (y + 1) / 2;
+      if (i > at) {
+        before = id;
+        id = page_of(i);
+        at = i;
+      }
+      const int mine = i == at ? id : before;
+      const unsigned int e = base + y;
+      const uint32_t slot = slot_of<PAIR>(s, e);
+      const int key0 = (p.t0 + i) * kTile;
+      const int keys = p.keys - key0 < kTile ? p.keys - key0 : kTile;
+      const int boxes = (keys + P.box_rows - 1) / P.box_rows;
+      const int in = key0 & (P.page_size - 1);
+      if (!(ok = warp_wait(&c->kv_empty[slot], turn_of<PAIR>(e) ^ 1, P, c))) break;
+      const uint32_t bar = smem_addr(&c->kv_full[slot]);
+      const CUtensorMap* map = is_v ? vmap : kmap;
+      uint32_t dst = ring + slot * S::tile_bytes;
+      if (elect_one()) bar_expect(bar, (uint32_t)(boxes * S::halves * 128 * P.box_rows));
+      for (int x = 0; x < boxes; ++x, dst += P.box_rows * 128) {
+        const int page = __shfl_sync(0xffffffffu, mine, x);
+        if (elect_one()) {
+          tma_load(dst, map, bar, 0, in, p.h, page);
+          if (S::halves == 2) tma_load(dst + S::half_bytes, map, bar, 64, in, p.h, page);
+        }
+      }
+      __syncwarp();
+      last = e + 1;
+    }
+    base += 2 * n;
+  }
+  if (lane == 0) {
+    c->q_copied[s] = qn;
+    c->kv_copied[s] = last;
   }
   const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && any) atomicOr(P.status, any);
 }
 
-template <typename T, int DP>
-__device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control* c, uint32_t q_smem,
+// Products of one stream.  (All 512 columns are allocated, so they start at 0.)
+template <typename T, int DP, bool PAIR>
+__device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t q_smem,
                                             uint32_t ring, unsigned char* ring_ptr) {
   using S = Shape<DP>;
   const int lane = threadIdx.x & 31;
-  const uint32_t tmem = c->tmem;
+  const uint32_t cols = s * 256;  // S, S, O of this stream
   constexpr uint32_t kQk = instr_desc(Type<T>::fmt, kTile, false);
   constexpr uint32_t kPv = instr_desc(Type<T>::fmt, DP, true);
-  unsigned int base = 0, qn = 0, pieces = 0, np[2] = {0, 0};
+  const uint32_t q = q_smem + s * S::q_bytes;
+  unsigned int base = 0, pieces = 0, tiles = 0;  // tiles: of the pieces so far
   Piece p;
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = bar_wait(smem_addr(bar), parity, P.wait_ns, &c->abort);
-    ok = __all_sync(0xffffffffu, ok);
-    return ok;
-  };
   while (ok && w.next(P, p)) {
-    const int n = p.t1 - p.t0, nv = p.two ? 2 * n : n;
-    // S of virtual tile j: stream j & 1
-    auto qk = [&](int j) {
-      const int s = j & 1, i = p.two ? j >> 1 : j;
-      const unsigned int e = base + k_entry(i), slot = e % S::slots;
-      const unsigned int qs = (p.two ? qn + s : qn) & 1, qp = ((p.two ? qn + s : qn) >> 1) & 1;
-      if ((p.two ? j < 2 : j == 0) && !wait(&c->q_full[qs], qp)) return;
-      if ((!p.two || s == 0) && !wait(&c->kv_full[slot], (e / S::slots) & 1)) return;
-      if (lane == 0) {
-        const uint32_t a = q_smem + qs * S::tile_bytes, b = ring + slot * S::tile_bytes;
+    const int n = p.t1 - p.t0;
+    auto qk = [&](int i) {
+      const unsigned int e = base + k_entry(i), t = tiles + i;
+      const uint32_t slot = slot_of<PAIR>(s, e);
+      if (i == 0 && !(ok = warp_wait(&c->q_full[s], pieces & 1, P, c))) return;
+      if (!(ok = warp_wait(&c->kv_full[slot], turn_of<PAIR>(e), P, c))) return;
+      if (elect_one()) {
+        const uint32_t b = ring + slot * S::tile_bytes;
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t at = (k / 4) * S::half_bytes + (k % 4) * 32;
-          mma_ss(tmem + s * kTile, mat_desc(a + at, 16), mat_desc(b + at, 16), kQk, k > 0);
-        }
-        mma_commit(smem_addr(&c->s_full[s]));
-        if (!p.two || s == 1) mma_commit(smem_addr(&c->kv_empty[slot]));
-        if (j + (p.two ? 2 : 1) >= nv) mma_commit(smem_addr(&c->q_empty[qs]));
+        for (int x = 0; x < S::halves; ++x)
+          mma_ss4(cols + (t & 1) * kTile, mat_desc(q + x * S::q_half, 16), mat_desc(b + x * S::half_bytes, 16),
+                  kQk, x > 0);
+        mma_commit(smem_addr(&c->s_full[s][t & 1]));
+        mma_commit(smem_addr(&c->kv_empty[slot]));
+        if (i == n - 1) mma_commit(smem_addr(&c->q_empty[s]));
       }
       __syncwarp();
     };
-    for (int j = 0; ok && j < 2 && j < nv; ++j) qk(j);
-    for (int j = 0; ok && j < nv; ++j) {
-      const int s = j & 1, i = p.two ? j >> 1 : j;
-      const unsigned int e = base + v_entry(i, n), slot = e % S::slots;
-      if (j == 0 && pieces > 0 && !wait(&c->o_free, (pieces - 1) & 1)) break;
+    qk(0);
+    if (ok && n > 1) qk(1);
+    for (int i = 0; ok && i < n; ++i) {
+      const unsigned int e = base + v_entry(i, n), t = tiles + i;
+      const uint32_t slot = slot_of<PAIR>(s, e);
+      if (i == 0 && pieces > 0 && !(ok = warp_wait(&c->o_free[s], (pieces - 1) & 1, P, c))) break;
       int keys = p.keys - (p.t0 + i) * kTile;
       keys = keys < kTile ? keys : kTile;
       const int steps = (keys + 15) / 16;
-      if (!p.two || s == 0) {
-        if (!wait(&c->kv_full[slot], (e / S::slots) & 1)) break;
-        if (keys & 15) {
-          // rows behind the last key of the last 16: what memory held there
-          // (weights of 0 times NaN would be NaN)
-          for (int x = lane; x < (steps * 16 - keys) * S::halves * 8; x += 32) {
-            const int row = keys + x / (S::halves * 8), in = x % (S::halves * 8);
-            *reinterpret_cast<uint4*>(ring_ptr + slot * S::tile_bytes + (in / 8) * S::half_bytes +
-                                      row * 128 + (in % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
+      if (!(ok = warp_wait(&c->kv_full[slot], turn_of<PAIR>(e), P, c))) break;
+      if (keys & 15) {
+        // rows behind the last key of the last 16: what memory held there
+        // (weights of 0 times NaN would be NaN).  In A both streams' warps
+        // write the same zeros.
+        for (int x = lane; x < (steps * 16 - keys) * S::halves * 8; x += 32) {
+          const int row = keys + x / (S::halves * 8), in = x % (S::halves * 8);
+          *reinterpret_cast<uint4*>(ring_ptr + slot * S::tile_bytes + (in / 8) * S::half_bytes + row * 128 +
+                                    (in % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
       }
-      if (!wait(&c->p_ready[s], np[s] & 1)) break;
-      ++np[s];
+      if (!(ok = warp_wait(&c->p_ready[s][t & 1], (t >> 1) & 1, P, c))) break;
       fence_after();
-      if (lane == 0) {
-        const uint32_t b = ring + slot * S::tile_bytes;
-        const uint32_t a = tmem + s * kTile, d = tmem + 2 * kTile + s * kTile;
-        for (int k = 0; k < steps; ++k)
-          mma_ts(d, a + k * 8, mat_desc(b + k * 2048, S::half_bytes), kPv, j > 1 || k > 0);
-        if (!p.two || s == 1) mma_commit(smem_addr(&c->kv_empty[slot]));
-        if (j == nv - 1) mma_commit(smem_addr(&c->o_full));
+      if (elect_one()) {
+        const uint32_t a = cols + (t & 1) * kTile, d = cols + 2 * kTile;
+        const uint64_t v = mat_desc(ring + slot * S::tile_bytes, S::half_bytes);
+        if (steps == 4) {
+          mma_ts4(d, a, v, kPv, i > 0);
+        } else {
+          for (int k = 0; k < steps; ++k) mma_ts(d, a + k * 8, v + k * 128, kPv, i > 0 || k > 0);
+        }
+        mma_commit(smem_addr(&c->kv_empty[slot]));
+        mma_commit(smem_addr(&c->pv_done[s]));
+        if (i == n - 1) mma_commit(smem_addr(&c->o_full[s]));
       }
       __syncwarp();
-      if (j + 2 < nv) qk(j + 2);
+      if (i + 2 < n) qk(i + 2);
     }
     base += 2 * n;
-    qn += p.two ? 2 : 1;
+    tiles += n;
     ++pieces;
   }
 }
 
-template <typename T, int DP>
-__device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Control* c) {
-  const int wg = threadIdx.x >> 7;                       // stream
+template <typename T, int DP, bool PAIR>
+__device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t part_base) {
   const int row = threadIdx.x & 127, lane = row & 31;
-  const uint32_t lanes = (uint32_t)(row & ~31) << 16;    // this warp's tensor-memory lanes
-  const uint32_t s_col = c->tmem + lanes + wg * kTile;
-  const uint32_t o_col = c->tmem + lanes + 2 * kTile;
+  const uint32_t lanes = (uint32_t)(row & ~31) << 16;  // this warp's tensor-memory lanes
+  const uint32_t s_cols = lanes + s * 256, o_col = s_cols + 2 * kTile;
   const float ninf = -INFINITY;
-  unsigned int ns = 0, pieces = 0, joins = 0;
+  const int tok = row / P.group, g = row - tok * P.group;
+  unsigned int tiles = 0, pieces = 0;
   Piece p;
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = bar_wait(smem_addr(bar), parity, P.wait_ns, &c->abort);
-    ok = __all_sync(0xffffffffu, ok);
-    return ok;
-  };
-  const int tok = row / P.group, g = row - tok * P.group;
   while (ok && w.next(P, p)) {
     const int n = p.t1 - p.t0;
-    const int blk = p.two ? wg : 0;  // row block of this stream
-    const int btok = p.ntok - blk * P.tpq < P.tpq ? p.ntok - blk * P.tpq : P.tpq;
+    const int skip = PAIR ? s * P.tpq : 0;  // rows of the other stream's block
+    int btok = p.ntok - skip;
+    btok = btok < P.tpq ? btok : P.tpq;
     const int rows = btok * P.group;
     const bool active = (row & ~31) < rows, mine = row < rows;
     // keys this row sees: all below `limit`, or below `free` and by its mask word
-    int limit = p.prefix ? P.prefix_len : p.kv + p.first + tok + 1;
-    int free = p.prefix ? P.prefix_len : (P.mask ? p.kv : p.kv + p.first + 1);
+    const int limit = p.prefix ? P.prefix_len : p.kv + p.first + tok + 1;
+    const int free = p.prefix ? P.prefix_len : (P.mask ? p.kv : p.kv + p.first + 1);
     uint32_t word = 0;
     if (!p.prefix && P.mask && mine) {
       word = P.mask[p.row0 + tok];
       if (p.keys - p.kv < 32) word &= (1u << (p.keys - p.kv)) - 1u;  // rows of the step
     }
     float m = ninf, l = 0.f;  // running maximum (times scale log2 e) and sum
-    const int step = p.two ? 1 : 2;
-    for (int i = p.two ? 0 : wg; i < n; i += step) {
-      if (!wait(&c->s_full[wg], ns & 1)) break;
-      ++ns;
+    for (int i = 0; i < n; ++i, ++tiles) {
+      const uint32_t s_col = s_cols + (tiles & 1) * kTile;
+      if (!(ok = warp_wait(&c->s_full[s][tiles & 1], (tiles >> 1) & 1, P, c))) break;
       if (active) {
         fence_after();
+        uint32_t v[kTile];
+        tmem_load32(s_col, v);
+        tmem_load32(s_col + 32, v + 32);
+        tmem_wait_load();
+        tmem_loaded32(v);
+        tmem_loaded32(v + 32);
         const int key0 = (p.t0 + i) * kTile;
-        const bool masked = key0 + kTile > free;
-        // keys [key0 + 32 ch, + 32) that this row does not see
-        auto hide = [&](uint32_t* v, int ch) {
-          const int at = key0 + 32 * ch;
-          uint32_t see;  // bit x: key at + x is seen
-          if (!p.prefix && P.mask) {
-            const int d = at - p.kv;  // the chunk's first key in the step's rows
-            see = d <= -32 ? ~0u : d < 0 ? (word << -d) | ((1u << -d) - 1u) : d < 32 ? word >> d : 0u;
-          } else {
-            const int n = limit - at;
-            see = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1u : 0u;
-          }
+        if (key0 + kTile > free) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!((see >> x) & 1u)) v[x] = __float_as_uint(ninf);
-        };
-        // S is read twice, 32 columns at a time, the next ones on their way:
-        // for the maximum, then for the weights (128 values held at once spill)
-        uint32_t v[2][32];
-        float mx0 = ninf, mx1 = ninf;
-        tmem_load32(s_col, v[0]);
+          for (int ch = 0; ch < 2; ++ch) {
+            const int at = key0 + 32 * ch;
+            uint32_t see;  // bit x: key at + x is seen
+            if (!p.prefix && P.mask) {
+              const int d = at - p.kv;  // the chunk's first key in the step's rows
+              see = d <= -32 ? ~0u : d < 0 ? (word << -d) | ((1u << -d) - 1u) : d < 32 ? word >> d : 0u;
+            } else {
+              const int k = limit - at;
+              see = k >= 32 ? ~0u : k > 0 ? (1u << k) - 1u : 0u;
+            }
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t* u = v[ch & 1];
-          tmem_wait_load();
-          tmem_loaded32(u);
-          tmem_load32(s_col + ((ch + 1) & 3) * 32, v[(ch + 1) & 1]);
-          if (masked) hide(u, ch);
-#pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            mx0 = max3(mx0, __uint_as_float(u[x]), __uint_as_float(u[x + 1]));
-            mx1 = max3(mx1, __uint_as_float(u[x + 2]), __uint_as_float(u[x + 3]));
+            for (int x = 0; x < 32; ++x)
+              if (!((see >> x) & 1u)) v[32 * ch + x] = __float_as_uint(ninf);
           }
         }
+        float mx0 = ninf, mx1 = ninf;
+#pragma unroll
+        for (int x = 0; x < kTile; x += 4) {
+          mx0 = max3(mx0, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+          mx1 = max3(mx1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+        }
         const float top = fmaxf(mx0, mx1) * P.sl2;
-        if (i < step) {
+        if (i == 0) {
           m = top;
         } else {
           const bool grow = top > m + 8.f || (m == ninf && top > ninf);
           if (__any_sync(0xffffffffu, grow)) {
             const float f = grow ? (m == ninf ? 0.f : exp2_fast(m - top)) : 1.f;
-            // the products so far are complete: S of this tile came after them
+            // (no product but the last can be under way: S of this tile came
+            // after the one before it, and the next waits for this tile's P)
+            if (!(ok = warp_wait(&c->pv_done[s], (tiles - 1) & 1, P, c))) break;
+            fence_after();
             for (int x = 0; x < DP; x += 16) {
               uint32_t o[16];
-              tmem_load16(o_col + wg * kTile + x, o);
+              tmem_load16(o_col + x, o);
               tmem_wait_load();
               tmem_loaded16(o);
 #pragma unroll
               for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_store16(o_col + wg * kTile + x, o);
+              tmem_store16(o_col + x, o);
             }
             l *= f;
             if (grow) m = top;
           }
         }
-        const uint64_t sub = pair(m == ninf ? 0.f : -m, m == ninf ? 0.f : -m);
-        const uint64_t sl2 = pair(P.sl2, P.sl2);
+        const float neg = m == ninf ? 0.f : -m;
+        const uint64_t sub = pair(neg, neg), sl2 = pair(P.sl2, P.sl2);
         uint64_t sum0 = 0, sum1 = 0;  // two pairs of zeros
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          uint32_t* u = v[ch & 1];
-          tmem_wait_load();
-          tmem_loaded32(u);
-          if (ch < 3) tmem_load32(s_col + (ch + 1) * 32, v[(ch + 1) & 1]);
-          if (masked) hide(u, ch);
-          uint32_t w16[16];
-#pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            float a, b, e, f;
-            unpair(pair_fma(pair(__uint_as_float(u[x]), __uint_as_float(u[x + 1])), sl2, sub), a, b);
-            unpair(pair_fma(pair(__uint_as_float(u[x + 2]), __uint_as_float(u[x + 3])), sl2, sub), e, f);
-            a = exp2_fast(a), b = exp2_fast(b), e = exp2_fast(e), f = exp2_fast(f);
-            sum0 = pair_add(sum0, pair(a, b));
-            sum1 = pair_add(sum1, pair(e, f));
-            w16[x / 2] = Type<T>::pack(a, b);
-            w16[x / 2 + 1] = Type<T>::pack(e, f);
-          }
-          // over columns of S that are read already
-          tmem_store16(s_col + ch * 16, w16);
+        for (int x = 0; x < kTile; x += 4) {
+          float a, b, e, f;
+          unpair(pair_fma(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl2, sub), a, b);
+          unpair(pair_fma(pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl2, sub), e, f);
+          a = exp2_fast(a), b = exp2_fast(b), e = exp2_fast(e), f = exp2_fast(f);
+          sum0 = pair_add(sum0, pair(a, b));
+          sum1 = pair_add(sum1, pair(e, f));
+          v[x / 2] = Type<T>::pack(a, b);
+          v[x / 2 + 1] = Type<T>::pack(e, f);
         }
+        tmem_store32(s_col, v);
         float a, b;
         unpair(pair_add(sum0, sum1), a, b);
         l += a + b;
@@ -675,39 +760,20 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
         fence_before();
       }
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&c->p_ready[wg]));
+      if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][tiles & 1]));
     }
     if (!ok) break;
-    // the piece's rows: this stream's columns, or half the columns of both
-    const int row_t = p.row0 + blk * P.tpq + tok;
-    float f0 = 0.f, f1 = 0.f, lse2;
-    if (p.two) {
-      f0 = l > 0.f || l != l ? 1.f / l : 0.f;
-      lse2 = m + log2f(l);
-    } else {
-      c->ml[wg][row] = make_float2(m, l);
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&c->ml_ready));
-      if (!wait(&c->ml_ready, joins & 1)) break;
-      ++joins;
-      const float2 a = c->ml[0][row], b = n > 1 ? c->ml[1][row] : make_float2(ninf, 0.f);
-      const float mm = fmaxf(a.x, b.x);
-      const float sub = mm == ninf ? 0.f : mm;
-      const float wa = a.x == ninf && a.y == 0.f ? 0.f : exp2_fast(a.x - sub);
-      const float wb = b.x == ninf && b.y == 0.f ? 0.f : exp2_fast(b.x - sub);
-      const float ll = a.y * wa + b.y * wb;
-      const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-      f0 = wa * inv;
-      f1 = wb * inv;
-      lse2 = mm + log2f(ll);
-    }
-    if (!wait(&c->o_full, pieces & 1)) break;
+    // the piece's rows, after its last product (a barrier of its own: parity
+    // would not tell that product from the one two before it)
+    if (!(ok = warp_wait(&c->o_full[s], pieces & 1, P, c))) break;
     ++pieces;
     if (active) {
       fence_after();
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float lse2 = m + log2f(l);
       const bool whole = p.t0 == 0 && p.t1 == p.unit_t;
       const bool direct = whole && !p.prefix && P.prefix_len == 0;
-      const size_t at = (size_t)row_t * P.Hq + (size_t)p.h * P.group + g;
+      const size_t at = (size_t)(p.row0 + skip + tok) * P.Hq + (size_t)p.h * P.group + g;
       float* part = nullptr;
       float* part_lse = nullptr;
       if (!direct) {
@@ -715,32 +781,20 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           part = P.dense[p.prefix] + at * DP;
           part_lse = P.dense_lse[p.prefix] + at;
         } else {
-          const size_t r = ((size_t)blockIdx.x * 2 + (p.t0 == 0)) * kSlotRows + blk * kTile + row;
+          const size_t r = (size_t)(part_base + (p.t0 == 0 ? (PAIR ? 2 : 1) : 0)) * kRows + row;
           part = P.slot + r * DP;
           part_lse = P.slot_lse + r;
         }
       }
-      const int x0 = p.two ? 0 : wg * (DP / 2), x1 = p.two ? DP : x0 + DP / 2;
-      const uint32_t first = o_col + (p.two ? wg * kTile : 0);
-      for (int x = x0; x < x1; x += 32) {
-        uint32_t o[32], o2[32];
-        tmem_load32(first + x, o);
-        if (!p.two && n > 1) tmem_load32(o_col + kTile + x, o2);
+#pragma unroll
+      for (int x = 0; x < DP; x += 32) {
+        uint32_t o[32];
+        tmem_load32(o_col + x, o);
         tmem_wait_load();
         tmem_loaded32(o);
-        if (!p.two && n > 1) {
-          tmem_loaded32(o2);
 #pragma unroll
-          for (int y = 0; y < 32; ++y) {
-            const float a = f0 == 0.f ? 0.f : __uint_as_float(o[y]) * f0;
-            const float b = f1 == 0.f ? 0.f : __uint_as_float(o2[y]) * f1;
-            o[y] = __float_as_uint(a + b);
-          }
-        } else {
-#pragma unroll
-          for (int y = 0; y < 32; ++y)
-            o[y] = f0 == 0.f ? 0u : __float_as_uint(__uint_as_float(o[y]) * f0);
-        }
+        for (int y = 0; y < 32; ++y)
+          o[y] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[y]) * inv);
         if (mine) {
           if (direct) {
 #pragma unroll
@@ -761,34 +815,78 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           }
         }
       }
-      if (mine && (p.two || wg == 0)) {
+      fence_before();
+      if (mine) {
         if (direct) {
           if (P.lse) P.lse[at] = lse2 * 0.693147180559945309f;
         } else {
           *part_lse = lse2;
         }
       }
-      fence_before();
     }
     __syncwarp();
-    if (lane == 0) bar_arrive(smem_addr(&c->o_free));
+    if (lane == 0) bar_arrive(smem_addr(&c->o_free[s]));
   }
 }
 
+template <typename T, int DP, bool PAIR>
+__device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsigned char* tiles, const Walk* walk,
+                                          const CUtensorMap* qmap, const CUtensorMap* kmap,
+                                          const CUtensorMap* vmap) {
+  using S = Shape<DP>;
+  const int warp = threadIdx.x >> 5;
+  const int s = warp < 8 ? warp >> 2 : (warp - 8) >> 1;
+  const uint32_t q_smem = smem_addr(tiles), ring = q_smem + 2 * S::q_bytes;
+  const Walk w = walk[PAIR ? 0 : s];
+  if (warp < 8)
+    softmax_role<T, DP, PAIR>(P, w, c, s, 4 * blockIdx.x + (PAIR ? s : 2 * s));
+  else if (!(warp & 1))
+    copy_role<DP, PAIR>(P, w, c, s, q_smem, ring, qmap, kmap, vmap);
+  else
+    matrix_role<T, DP, PAIR>(P, w, c, s, q_smem, ring, tiles + 2 * S::q_bytes);
+  fence_before();
+  __syncthreads();
+  if (c->abort) {
+    // a wait ran out: copies and products in flight end (each wait bounded)
+    // before shared and tensor memory are given back
+    int ignored = 0;
+    if (warp == 8 || warp == 10) {
+      for (int x = 0; x < 2; ++x) {
+        const unsigned int q = c->q_copied[PAIR ? 0 : x];
+        if (q > 0 && (PAIR || x == s)) (void)bar_wait(smem_addr(&c->q_full[x]), (q - 1) & 1, kDrainNs, &ignored);
+      }
+      // the last use of each slot that a copy was started for; in A the two
+      // warps' entries interleave: all up to the later one's last are waited
+      // for, an entry that was never started runs out
+      const unsigned int a = c->kv_copied[0], b = c->kv_copied[1];
+      const unsigned int end = PAIR ? (a > b ? a : b) : c->kv_copied[s], count = PAIR ? 10 : 5;
+      for (unsigned int e = end > count ? end - count : 0; e < end; ++e)
+        (void)bar_wait(smem_addr(&c->kv_full[slot_of<PAIR>(s, e)]), turn_of<PAIR>(e), kDrainNs, &ignored);
+    } else if (warp >= 8) {
+      if (elect_one()) mma_commit(smem_addr(&c->drain[s]));
+      __syncwarp();
+      (void)bar_wait(smem_addr(&c->drain[s]), 0, kDrainNs, &ignored);
+    }
+    __syncthreads();
+  }
+}
+
+struct Maps {
+  CUtensorMap q[2], k, v;  // queries of a request's own block, and of a prefix block
+};
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-    attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qmap_prefix,
-                     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const __grid_constant__ AttnParams P) {
+    attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams P) {
   using S = Shape<DP>;
   extern __shared__ __align__(1024) unsigned char tiles[];
-  Control* c = reinterpret_cast<Control*>(tiles + (S::slots + 2) * S::tile_bytes);
+  Control* c = reinterpret_cast<Control*>(tiles + 2 * S::q_bytes + S::slots * S::tile_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_addr(tiles) & 1023) {  // the swizzle's period; never expected
     if (tid == 0) atomicOr(P.status, (unsigned int)SV_STATUS_INTERNAL);
     return;
   }
-  // the share of the tile list: a scan over the requests' tiles
+  // the requests' tiles, scanned
   unsigned int flags = 0;
   const int chunk = (P.B + kThreads - 1) / kThreads;
   const int b0 = tid * chunk < P.B ? tid * chunk : P.B;
@@ -804,34 +902,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 31) c->scan[warp] = incl;
   if (tid == 0) {
     c->abort = 0;
-    c->start_b = P.B;
-    for (int i = 0; i < 8; ++i) {
-      bar_init(smem_addr(&c->kv_full[i]), 1);
-      bar_init(smem_addr(&c->kv_empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(smem_addr(&c->q_full[i]), 1);
-      bar_init(smem_addr(&c->q_empty[i]), 1);
-      bar_init(smem_addr(&c->s_full[i]), 1);
-      bar_init(smem_addr(&c->p_ready[i]), 4);
-    }
-    bar_init(smem_addr(&c->o_full), 1);
-    bar_init(smem_addr(&c->o_free), 8);
-    bar_init(smem_addr(&c->ml_ready), 8);
-    bar_init(smem_addr(&c->drain), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    c->start_b[0] = c->start_b[1] = P.B;
+    c->q_copied[0] = c->q_copied[1] = c->kv_copied[0] = c->kv_copied[1] = 0;
   }
   __syncthreads();
-  const long long prefix_all = (long long)P.prefix_units * P.prefix_tiles;
-  long long excl = prefix_all + incl - mine, total = prefix_all;
+  const long long singles = single_tiles(P);
+  long long excl = singles + incl - mine, total = singles;
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i < warp) excl += c->scan[i];
     total += c->scan[i];
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long g0 = per * blockIdx.x;
-  const long long left = total - g0 < per ? total - g0 : per;
+  const Plan L = make_plan(P, total, gridDim.x);
   if (blockIdx.x == 0) {
     long long at = excl;
     for (int b = b0; b < b1; ++b) {
@@ -842,18 +923,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) P.starts[P.B] = total;
     if (flags) atomicOr(P.status, flags);
   }
-  if (left <= 0) return;  // the whole CTA
-  if (g0 >= prefix_all && g0 >= excl && g0 < excl + mine) {
-    long long at = excl;
-    int b = b0;
-    unsigned int ignored = 0;
-    for (; b < b1 - 1; ++b) {
-      const long long t = request_tiles(P, request(P, b, ignored));
-      if (g0 < at + t) break;
-      at += t;
+  // this CTA's shares
+  const bool pair_cta = (int)blockIdx.x < L.ctas_a;
+  long long g0[2], left[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const long long per = pair_cta ? L.per_a : L.per_b, end = pair_cta ? L.a : L.b;
+    g0[s] = per * (pair_cta ? blockIdx.x : 2 * (blockIdx.x - L.ctas_a) + s);
+    left[s] = end - g0[s] < per ? end - g0[s] : per;
+  }
+  if (left[0] <= 0) return;  // the whole CTA (then stream 1 has nothing either)
+  if (!pair_cta) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (left[s] > 0 && g0[s] >= singles && g0[s] >= excl && g0[s] < excl + mine) {
+        long long at = excl;
+        int b = b0;
+        unsigned int ignored = 0;
+        for (; b < b1 - 1; ++b) {
+          const long long t = request_tiles(P, request(P, b, ignored));
+          if (g0[s] < at + t) break;
+          at += t;
+        }
+        c->start_b[s] = b;
+        c->start_rem[s] = g0[s] - at;
+      }
     }
-    c->start_b = b;
-    c->start_rem = g0 - at;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 10; ++i) {
+      bar_init(smem_addr(&c->kv_full[i]), 1);
+      bar_init(smem_addr(&c->kv_empty[i]), pair_cta ? 2 : 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      bar_init(smem_addr(&c->q_full[s]), 1);
+      bar_init(smem_addr(&c->q_empty[s]), 1);
+      for (int i = 0; i < 2; ++i) {
+        bar_init(smem_addr(&c->s_full[s][i]), 1);
+        bar_init(smem_addr(&c->p_ready[s][i]), 4);
+      }
+      bar_init(smem_addr(&c->pv_done[s]), 1);
+      bar_init(smem_addr(&c->o_full[s]), 1);
+      bar_init(smem_addr(&c->o_free[s]), 4);
+      bar_init(smem_addr(&c->drain[s]), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -864,54 +979,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  Walk w;
-  w.left = left;
-  w.prefix = g0 < prefix_all;
-  w.unit = w.b = w.rb = w.h = w.off = 0;
-  w.r = Req{0, 0, 0};
-  if (w.prefix) {
-    w.unit = (int)(g0 / P.prefix_tiles);
-    w.off = (int)(g0 - (long long)w.unit * P.prefix_tiles);
-  } else {
-    w.b = c->start_b;
-    w.load_request(P);
-    long long rem = c->start_rem;
-    for (; w.rb * P.tpq < w.r.n; ++w.rb) {
-      const int t = tiles_of(block_keys(P, w.r, w.rb));
-      if (rem < (long long)t * P.Hk) {
-        w.h = (int)(rem / t);
-        w.off = (int)(rem - (long long)w.h * t);
-        break;
+  Walk w[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    w[s].left = left[s] > 0 ? left[s] : 0;
+    w[s].pair = pair_cta;
+    w[s].single = !pair_cta && g0[s] < singles;
+    w[s].unit = w[s].b = w[s].rb = w[s].h = w[s].off = 0;
+    w[s].r = Req{0, 0, 0};
+    if (w[s].left == 0) continue;
+    if (w[s].pair || w[s].single) {
+      w[s].unit = (int)(g0[s] / P.prefix_tiles);
+      w[s].off = (int)(g0[s] - (long long)w[s].unit * P.prefix_tiles);
+    } else {
+      w[s].b = c->start_b[s];
+      w[s].load_request(P);
+      long long rem = c->start_rem[s];
+      for (; w[s].rb * P.tpq < w[s].r.n; ++w[s].rb) {
+        const int t = tiles_of(block_keys(P, w[s].r, w[s].rb));
+        if (rem < (long long)t * P.Hk) {
+          w[s].h = (int)(rem / t);
+          w[s].off = (int)(rem - (long long)w[s].h * t);
+          break;
+        }
+        rem -= (long long)t * P.Hk;
       }
-      rem -= (long long)t * P.Hk;
     }
   }
-  const uint32_t q_smem = smem_addr(tiles), ring = q_smem + 2 * S::tile_bytes;
-  unsigned int entry = 0, qn = 0;  // ring entries and query tiles copied (warp 8)
-  if (warp < 8)
-    softmax_role<T, DP>(P, w, c);
-  else if (warp == 8)
-    copy_role<DP>(P, w, c, q_smem, ring, &qmap, &qmap_prefix, &kmap, &vmap, entry, qn);
+  if (pair_cta)
+    run_roles<T, DP, true>(P, c, tiles, w, maps.q, &maps.k, &maps.v);
   else
-    matrix_role<T, DP>(P, w, c, q_smem, ring, tiles + 2 * S::tile_bytes);
-  fence_before();
-  __syncthreads();
-  if (c->abort) {
-    // a wait ran out: copies and products in flight end (each wait bounded)
-    // before shared and tensor memory are given back
-    int ignored = 0;
-    if (warp == 8) {
-      for (unsigned int i = qn > 2 ? qn - 2 : 0; i < qn; ++i)
-        (void)bar_wait(smem_addr(&c->q_full[i & 1]), (i >> 1) & 1, kDrainNs, &ignored);
-      for (unsigned int e = entry > (unsigned int)S::slots ? entry - S::slots : 0; e < entry; ++e)
-        (void)bar_wait(smem_addr(&c->kv_full[e % S::slots]), (e / S::slots) & 1, kDrainNs, &ignored);
-    } else if (warp == 9) {
-      if (lane == 0) mma_commit(smem_addr(&c->drain));
-      __syncwarp();
-      (void)bar_wait(smem_addr(&c->drain), 0, kDrainNs, &ignored);
-    }
-    __syncthreads();
-  }
+    run_roles<T, DP, false>(P, c, tiles, w, maps.q, &maps.k, &maps.v);
   if (warp == 9) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(c->tmem));
@@ -953,12 +1051,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
   unsigned int ignored = 0;
   const Req r = request(P, b, ignored);
   if (r.n <= 0) return;
-  const long long total = P.starts[P.B], per = (total + ctas - 1) / ctas;
+  const Plan L = make_plan(P, P.starts[P.B], ctas);
   const long long first = P.starts[b];
-  if (per <= 0) return;
+  if (L.per_b <= 0) return;
   // without a prefix, requests whose units all lie within one share are done
   const long long tiles_all = request_tiles(P, r);
-  if (P.prefix_len == 0 && first / per == (first + tiles_all - 1) / per) return;
+  if (P.prefix_len == 0 && first / L.per_b == (first + tiles_all - 1) / L.per_b) return;
   const int rows = r.n * P.Hq;
   for (int x = (blockIdx.y * 4 + (threadIdx.x >> 5)); x < rows; x += gridDim.y * 4) {
     const int i = x / P.Hq, head = x - i * P.Hq;
@@ -969,15 +1067,19 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     for (int y = 0; y < DP / 32; ++y) acc.o[y] = 0.f;
     acc.m = -INFINITY;
     acc.l = 0.f;
-    auto unit = [&](long long u0, int tiles, int which, int slot_row) {
+    // the parts of a unit at u0 of list A (of its stream s) or B
+    auto unit = [&](bool pair, int s, long long u0, int tiles, int which, int slot_row) {
+      const long long per = pair ? L.per_a : L.per_b;
       const long long c0 = u0 / per, c1 = (u0 + tiles - 1) / per;
       if (c0 == c1) {
         acc.add(P.dense[which] + at * DP, P.dense_lse[which][at]);
         return;
       }
       for (long long c = c0; c <= c1; ++c) {
-        const size_t s = ((size_t)c * 2 + (c == c0)) * kSlotRows + slot_row;
-        acc.add(P.slot + s * DP, P.slot_lse[s]);
+        const long long id = pair ? 4 * c + s + 2 * (c == c0)
+                                  : 4 * (L.ctas_a + c / 2) + 2 * (c & 1) + (c == c0);
+        const size_t at_slot = (size_t)id * kRows + slot_row;
+        acc.add(P.slot + at_slot * DP, P.slot_lse[at_slot]);
       }
     };
     const int rb = i / P.tpq;
@@ -985,14 +1087,14 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     for (int y = 0; y < rb; ++y) u0 += (long long)tiles_of(block_keys(P, r, y)) * P.Hk;
     const int tiles = tiles_of(block_keys(P, r, rb));
     u0 += (long long)h * tiles;
-    if (P.prefix_len == 0 && u0 / per == (u0 + tiles - 1) / per) continue;  // written already
+    if (P.prefix_len == 0 && u0 / L.per_b == (u0 + tiles - 1) / L.per_b) continue;  // written already
     if (P.prefix_len > 0) {
-      const int t = r.row0 + i, pair = t / (2 * P.tpq), in = t - pair * 2 * P.tpq;
-      const int blk = in / P.tpq;
-      unit((long long)(h * P.prefix_blocks + pair) * P.prefix_tiles, P.prefix_tiles, 1,
-           blk * kTile + (in - blk * P.tpq) * P.group + g);
+      const int t = r.row0 + i, blk = t / P.tpq, slot_row = (t - blk * P.tpq) * P.group + g;
+      const bool pair = blk < 2 * P.pairs;
+      unit(pair, blk & 1, (pair ? (long long)h * P.pairs + blk / 2 : (long long)h) * P.prefix_tiles, P.prefix_tiles,
+           1, slot_row);
     }
-    unit(u0, tiles, 0, (i - rb * P.tpq) * P.group + g);
+    unit(false, 0, u0, tiles, 0, (i - rb * P.tpq) * P.group + g);
     const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
     if (DP == 128) {
       if (lane * 4 < P.D)
@@ -1059,8 +1161,8 @@ AttnLayout attn_layout(long long T, int Hq, int D) {
   L.starts = take((size_t)(T + 1) * sizeof(long long));
   for (int i = 0; i < 2; ++i) L.dense[i] = take(rows * dp * 4);
   for (int i = 0; i < 2; ++i) L.dense_lse[i] = take(rows * 4);
-  L.slot = take((size_t)2 * kMaxCtas * kSlotRows * dp * 4);
-  L.slot_lse = take((size_t)2 * kMaxCtas * kSlotRows * 4);
+  L.slot = take((size_t)kSlots * kRows * dp * 4);
+  L.slot_lse = take((size_t)kSlots * kRows * 4);
   L.total = at;
   return L;
 }
@@ -1081,15 +1183,11 @@ int grid_size() {
   return sms;
 }
 
-struct Maps {
-  CUtensorMap q, q_prefix, k, v;
-};
-
 template <typename T, int DP>
 int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   const int grid = grid_size<T, DP>();
   if (grid <= 0) return SV_ERR_CUDA;
-  attention_kernel<T, DP><<<grid, kThreads, Shape<DP>::smem, stream>>>(m.q, m.q_prefix, m.k, m.v, P);
+  attention_kernel<T, DP><<<grid, kThreads, Shape<DP>::smem, stream>>>(m, P);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   // CTAs a request: four rows each, at most 64 of them
   const long long rows = ((long long)(P.G < P.T ? P.G + 1 : P.T) * P.Hq + 3) / 4;
@@ -1120,7 +1218,7 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   if (rc) return rc;
   const long long rows = (long long)total_drafts + c.batch;
   if (total_drafts < 0 || max_drafts < 0 || rows > INT32_MAX || prefix_len < 0 || q_heads < 1 ||
-      q_heads > 65535 || q_heads % c.kv_heads || q_heads / c.kv_heads > kTile || !(scale > 0.f) ||
+      q_heads > 65535 || q_heads % c.kv_heads || q_heads / c.kv_heads > kRows || !(scale > 0.f) ||
       !std::isfinite(scale * 1.44269504f) || (draft_mask && max_drafts > SV_MAX_GAMMA))
     return SV_ERR_SCALAR;
   for (int i = 0; i < 2; ++i)
@@ -1142,7 +1240,7 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   P.Hk = c.kv_heads;
   P.D = c.head_dim;
   P.group = q_heads / c.kv_heads;
-  P.tpq = kTile / P.group;
+  P.tpq = kRows / P.group;
   P.own_tok = max_drafts < P.tpq ? max_drafts + 1 : P.tpq;
   P.num_pages = c.num_pages;
   P.page_size = c.page_size;
@@ -1155,11 +1253,11 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   P.prefix_table = prefix_table;
   P.prefix_len = prefix_len;
   P.prefix_tiles = (prefix_len + kTile - 1) / kTile;
-  P.prefix_blocks = (P.T + 2 * P.tpq - 1) / (2 * P.tpq);
   if (prefix_len > 0) {
-    const long long units = (long long)P.prefix_blocks * P.Hk;
-    if (units > INT32_MAX) return SV_ERR_SCALAR;
-    P.prefix_units = (int)units;
+    const int blocks = (P.T + P.tpq - 1) / P.tpq;
+    P.pairs = blocks / 2;
+    P.odd = blocks & 1;
+    if ((long long)P.pairs * P.Hk > INT32_MAX) return SV_ERR_SCALAR;
   }
   P.mask = draft_mask;
   P.sl2 = scale * 1.44269504088896341f;
@@ -1185,7 +1283,7 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   const int64_t ks[3] = {c.k_strides[1], c.k_strides[2], c.k_strides[0]};
   const int64_t vs[3] = {c.v_strides[1], c.v_strides[2], c.v_strides[0]};
   const uint32_t cb[4] = {64, (uint32_t)P.box_rows, 1, 1};
-  if (!encode(&m.q, c.dtype, q, qd, qs, q_own) || !encode(&m.q_prefix, c.dtype, q, qd, qs, q_pre) ||
+  if (!encode(&m.q[0], c.dtype, q, qd, qs, q_own) || !encode(&m.q[1], c.dtype, q, qd, qs, q_pre) ||
       !encode(&m.k, c.dtype, c.k_pages, cd, ks, cb) || !encode(&m.v, c.dtype, c.v_pages, cd, vs, cb))
     return SV_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
