@@ -86,7 +86,7 @@ struct AttnParams {
   char* out;
   float* lse;
   unsigned int* status;
-  long long* starts;   // [B + 1]: first tile of each request in list B, and the list's end
+  int* starts;         // [B + 1]: first tile of each request in list B, and the list's end
   float* dense[2];     // own, prefix: rows of whole units [T * Hq][DP]
   float* dense_lse[2];
   float* slot;         // [kSlots][kRows][DP]
@@ -331,7 +331,7 @@ struct Req {
   int kv;    // own keys before the step
 };
 __device__ __forceinline__ Req request(const AttnParams& P, int b, unsigned int& flags) {
-  const int c0 = P.cu[b], c1 = P.cu[b + 1], kv = P.kv_len[b];
+  const int c0 = __ldg(P.cu + b), c1 = __ldg(P.cu + b + 1), kv = __ldg(P.kv_len + b);
   Req r{0, 0, 0};
   if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 > P.total) {
     flags |= SV_STATUS_BAD_GAMMA;
@@ -348,27 +348,31 @@ __device__ __forceinline__ int block_keys(const AttnParams& P, const Req& r, int
   return r.kv + last;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
-__device__ __forceinline__ long long request_tiles(const AttnParams& P, const Req& r) {
+// (the host refuses sizes whose lists could pass 2^30 tiles)
+__device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) {
   if (r.n <= 0) return 0;
-  long long t = 0;
+  int t = 0;
   for (int rb = 0; rb * P.tpq < r.n; ++rb) t += tiles_of(block_keys(P, r, rb));
   return t * P.Hk;
 }
 
 // How the lists are dealt out.
 struct Plan {
-  long long a, b;          // tiles of the lists
-  long long per_a, per_b;  // of a CTA's share of A, of a stream's share of B
+  int a, b;          // tiles of the lists
+  int per_a, per_b;  // of a CTA's share of A, of a stream's share of B
   int ctas_a, ctas_b;
 };
-__device__ __forceinline__ Plan make_plan(const AttnParams& P, long long b_tiles, int ctas) {
+__device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int ctas) {
   Plan L;
-  L.a = (long long)P.Hk * P.pairs * P.prefix_tiles;
+  L.a = P.Hk * P.pairs * P.prefix_tiles;
   L.b = b_tiles;
-  const long long wa = L.a * kCostA, wb = L.b * kCostB;
-  int na = L.a == 0 ? 0 : L.b == 0 ? ctas : (int)((ctas * wa + (wa + wb) / 2) / (wa + wb));
-  if (L.a > 0 && na < 1) na = 1;
-  if (L.b > 0 && na > ctas - 1) na = ctas - 1;
+  int na = 0;
+  if (L.a > 0) {
+    const float wa = (float)L.a * kCostA, wb = (float)L.b * kCostB;
+    na = (int)(ctas * (wa / (wa + wb)) + 0.5f);
+    na = na < 1 ? 1 : na;
+    if (L.b > 0 && na > ctas - 1) na = ctas - 1;
+  }
   L.ctas_a = na;
   L.ctas_b = ctas - na;
   L.per_a = na ? (L.a + na - 1) / na : 0;
@@ -376,9 +380,7 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& P, long long b_tiles
   return L;
 }
 // tiles of list B before the requests' own
-__device__ __forceinline__ long long single_tiles(const AttnParams& P) {
-  return (long long)P.Hk * P.odd * P.prefix_tiles;
-}
+__device__ __forceinline__ int single_tiles(const AttnParams& P) { return P.Hk * P.odd * P.prefix_tiles; }
 
 // A run of tiles of one unit.
 struct Piece {
@@ -394,7 +396,7 @@ struct Piece {
 
 // Walks a share.  Every role walks it alone, from the same start.
 struct Walk {
-  long long left;
+  int left;
   bool pair, single;  // list A; the prefix's single block in list B
   int unit;           // prefix unit
   int b, rb, h;       // own unit
@@ -438,7 +440,7 @@ struct Walk {
       p.unit_t = tiles_of(p.keys);
     }
     p.t0 = off;
-    p.t1 = left < p.unit_t - off ? off + (int)left : p.unit_t;
+    p.t1 = left < p.unit_t - off ? off + left : p.unit_t;
     left -= p.t1 - p.t0;
     off = 0;
     if (p.prefix) {
@@ -461,10 +463,9 @@ struct Control {
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], pv_done[2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
   int abort;
-  int start_b[2];
-  long long start_rem[2];
   unsigned int q_copied[2], kv_copied[2];
-  long long scan[kThreads / 32];
+  int scan[kThreads / 32];
+  Walk start[2];  // where the streams' shares begin
 };
 static_assert(sizeof(Control) <= kControl, "control block");
 
@@ -507,8 +508,8 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
       const int key = (p.t0 + i) * kTile + lane * P.box_rows;
       int id = 0;
       if (lane * P.box_rows < kTile && key < p.keys) {
-        id = p.prefix ? P.prefix_table[key >> P.page_shift]
-                      : P.table[(size_t)p.b * P.max_pages + (key >> P.page_shift)];
+        id = __ldg(p.prefix ? P.prefix_table + (key >> P.page_shift)
+                            : P.table + (size_t)p.b * P.max_pages + (key >> P.page_shift));
         if (id < 0 || id >= P.num_pages) {
           flags |= SV_STATUS_BAD_PAGE;
           id = P.num_pages;  // past the pool: the copy fills zeros
@@ -830,14 +831,14 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
 }
 
 template <typename T, int DP, bool PAIR>
-__device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsigned char* tiles, const Walk* walk,
-                                          const CUtensorMap* qmap, const CUtensorMap* kmap,
+__device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsigned char* tiles, const CUtensorMap* qmap,
+                                          const CUtensorMap* kmap,
                                           const CUtensorMap* vmap) {
   using S = Shape<DP>;
   const int warp = threadIdx.x >> 5;
   const int s = warp < 8 ? warp >> 2 : (warp - 8) >> 1;
   const uint32_t q_smem = smem_addr(tiles), ring = q_smem + 2 * S::q_bytes;
-  const Walk w = walk[PAIR ? 0 : s];
+  const Walk w = c->start[s];
   if (warp < 8)
     softmax_role<T, DP, PAIR>(P, w, c, s, 4 * blockIdx.x + (PAIR ? s : 2 * s));
   else if (!(warp & 1))
@@ -886,76 +887,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicOr(P.status, (unsigned int)SV_STATUS_INTERNAL);
     return;
   }
-  // the requests' tiles, scanned
+  // the requests' tiles, scanned; what else a CTA needs is set up meanwhile
   unsigned int flags = 0;
   const int chunk = (P.B + kThreads - 1) / kThreads;
   const int b0 = tid * chunk < P.B ? tid * chunk : P.B;
   const int b1 = b0 + chunk < P.B ? b0 + chunk : P.B;
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += request_tiles(P, request(P, b, flags));
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+  Req r{0, 0, 0};  // the thread's last request: its only one up to 384 requests
+  int mine = 0;
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&c->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (lane == 31) c->scan[warp] = incl;
-  if (tid == 0) {
+  for (int b = b0; b < b1; ++b) {
+    r = request(P, b, flags);
+    mine += request_tiles(P, r);
+  }
+  if (tid == kThreads - 1) {
     c->abort = 0;
-    c->start_b[0] = c->start_b[1] = P.B;
     c->q_copied[0] = c->q_copied[1] = c->kv_copied[0] = c->kv_copied[1] = 0;
-  }
-  __syncthreads();
-  const long long singles = single_tiles(P);
-  long long excl = singles + incl - mine, total = singles;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) excl += c->scan[i];
-    total += c->scan[i];
-  }
-  const Plan L = make_plan(P, total, gridDim.x);
-  if (blockIdx.x == 0) {
-    long long at = excl;
-    for (int b = b0; b < b1; ++b) {
-      P.starts[b] = at;
-      unsigned int ignored = 0;
-      at += request_tiles(P, request(P, b, ignored));
-    }
-    if (tid == 0) P.starts[P.B] = total;
-    if (flags) atomicOr(P.status, flags);
-  }
-  // this CTA's shares
-  const bool pair_cta = (int)blockIdx.x < L.ctas_a;
-  long long g0[2], left[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const long long per = pair_cta ? L.per_a : L.per_b, end = pair_cta ? L.a : L.b;
-    g0[s] = per * (pair_cta ? blockIdx.x : 2 * (blockIdx.x - L.ctas_a) + s);
-    left[s] = end - g0[s] < per ? end - g0[s] : per;
-  }
-  if (left[0] <= 0) return;  // the whole CTA (then stream 1 has nothing either)
-  if (!pair_cta) {
-#pragma unroll
     for (int s = 0; s < 2; ++s) {
-      if (left[s] > 0 && g0[s] >= singles && g0[s] >= excl && g0[s] < excl + mine) {
-        long long at = excl;
-        int b = b0;
-        unsigned int ignored = 0;
-        for (; b < b1 - 1; ++b) {
-          const long long t = request_tiles(P, request(P, b, ignored));
-          if (g0[s] < at + t) break;
-          at += t;
-        }
-        c->start_b[s] = b;
-        c->start_rem[s] = g0[s] - at;
-      }
-    }
-  }
-  if (tid == 0) {
-    for (int i = 0; i < 10; ++i) {
-      bar_init(smem_addr(&c->kv_full[i]), 1);
-      bar_init(smem_addr(&c->kv_empty[i]), pair_cta ? 2 : 1);
-    }
-    for (int s = 0; s < 2; ++s) {
+      c->start[s].left = 0;
       bar_init(smem_addr(&c->q_full[s]), 1);
       bar_init(smem_addr(&c->q_empty[s]), 1);
       for (int i = 0; i < 2; ++i) {
@@ -967,49 +920,91 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(smem_addr(&c->o_free[s]), 4);
       bar_init(smem_addr(&c->drain[s]), 1);
     }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_addr(&c->tmem))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) c->scan[warp] = incl;
+  __syncthreads();
+  const int singles = single_tiles(P);
+  int excl = singles + incl - mine, total = singles;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    const int v = c->scan[i];
+    if (i < warp) excl += v;
+    total += v;
+  }
+  const Plan L = make_plan(P, total, gridDim.x);
+  const bool pair_cta = (int)blockIdx.x < L.ctas_a;
+  if (tid < 10) {
+    bar_init(smem_addr(&c->kv_full[tid]), 1);
+    bar_init(smem_addr(&c->kv_empty[tid]), pair_cta ? 2 : 1);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // where the streams' shares begin, found by the thread whose requests hold it
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int per = pair_cta ? L.per_a : L.per_b, end = pair_cta ? L.a : L.b;
+    const int g0 = per * (pair_cta ? (int)blockIdx.x : 2 * ((int)blockIdx.x - L.ctas_a) + s);
+    const int left = end - g0 < per ? end - g0 : per;
+    if (left <= 0) continue;
+    const bool unit = pair_cta || g0 < singles;
+    if (unit ? tid == 0 : g0 >= excl && g0 < excl + mine) {
+      Walk w;
+      w.left = left;
+      w.pair = pair_cta;
+      w.single = unit && !pair_cta;
+      w.unit = w.b = w.rb = w.h = w.off = 0;
+      w.r = r;
+      if (unit) {
+        w.unit = g0 / P.prefix_tiles;
+        w.off = g0 - w.unit * P.prefix_tiles;
+      } else {
+        int rem = g0 - excl;
+        unsigned int ignored = 0;
+        for (w.b = b0; w.b < b1 - 1; ++w.b) {
+          const int t = request_tiles(P, request(P, w.b, ignored));
+          if (rem < t) break;
+          rem -= t;
+        }
+        if (b1 - b0 > 1) w.r = request(P, w.b, ignored);
+        for (; w.rb * P.tpq < w.r.n; ++w.rb) {
+          const int t = tiles_of(block_keys(P, w.r, w.rb));
+          if (rem < t * P.Hk) {
+            w.h = rem / t;
+            w.off = rem - w.h * t;
+            break;
+          }
+          rem -= t * P.Hk;
+        }
+      }
+      c->start[s] = w;
+    }
+  }
+  if (blockIdx.x == 0) {
+    int at = excl;
+    for (int b = b0; b < b1; ++b) {
+      P.starts[b] = at;
+      if (b + 1 < b1) {
+        unsigned int ignored = 0;
+        at += request_tiles(P, request(P, b, ignored));
+      }
+    }
+    if (tid == 0) P.starts[P.B] = total;
+    if (flags) atomicOr(P.status, flags);
   }
   fence_before();
   __syncthreads();
   fence_after();
-  Walk w[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    w[s].left = left[s] > 0 ? left[s] : 0;
-    w[s].pair = pair_cta;
-    w[s].single = !pair_cta && g0[s] < singles;
-    w[s].unit = w[s].b = w[s].rb = w[s].h = w[s].off = 0;
-    w[s].r = Req{0, 0, 0};
-    if (w[s].left == 0) continue;
-    if (w[s].pair || w[s].single) {
-      w[s].unit = (int)(g0[s] / P.prefix_tiles);
-      w[s].off = (int)(g0[s] - (long long)w[s].unit * P.prefix_tiles);
-    } else {
-      w[s].b = c->start_b[s];
-      w[s].load_request(P);
-      long long rem = c->start_rem[s];
-      for (; w[s].rb * P.tpq < w[s].r.n; ++w[s].rb) {
-        const int t = tiles_of(block_keys(P, w[s].r, w[s].rb));
-        if (rem < (long long)t * P.Hk) {
-          w[s].h = (int)(rem / t);
-          w[s].off = (int)(rem - (long long)w[s].h * t);
-          break;
-        }
-        rem -= (long long)t * P.Hk;
-      }
-    }
-  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (pair_cta)
-    run_roles<T, DP, true>(P, c, tiles, w, maps.q, &maps.k, &maps.v);
+    run_roles<T, DP, true>(P, c, tiles, maps.q, &maps.k, &maps.v);
   else
-    run_roles<T, DP, false>(P, c, tiles, w, maps.q, &maps.k, &maps.v);
+    run_roles<T, DP, false>(P, c, tiles, maps.q, &maps.k, &maps.v);
   if (warp == 9) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(c->tmem));
@@ -1020,92 +1015,161 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Joining parts: o = sum 2^(lse_i - m) o_i / sum 2^(lse_i - m), one warp a row
 // ---------------------------------------------------------------------------
-template <int DP>
+// The parts of one row: the prefix's, then the own.
+struct Unit {
+  bool pair;
+  int c0, count;   // first share, shares
+  int slot_row, stream, which;
+};
+// The running join of some of a row's parts: a lane holds W values.
+template <int W>
 struct Joined {
-  float o[DP / 32];
-  float m, l;
-  __device__ __forceinline__ void add(const float* part, float lse2) {
-    if (lse2 == -INFINITY) return;  // no key seen there
-    const float top = fmaxf(m, lse2);
-    const float a = m == -INFINITY ? 0.f : exp2f(m - top), b = exp2f(lse2 - top);
-    const int lane = threadIdx.x & 31;
-    if (DP == 128) {
-      const float4 v = *reinterpret_cast<const float4*>(part + lane * 4);
-      o[0] = o[0] * a + v.x * b;
-      o[1] = o[1] * a + v.y * b;
-      o[2 % (DP / 32)] = o[2 % (DP / 32)] * a + v.z * b;
-      o[3 % (DP / 32)] = o[3 % (DP / 32)] * a + v.w * b;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(part + lane * 2);
-      o[0] = o[0] * a + v.x * b;
-      o[1] = o[1] * a + v.y * b;
-    }
-    l = l * a + b;
-    m = lse2 != lse2 ? lse2 : top;  // fmaxf drops a NaN
-  }
+  float o[W], m, l;
 };
 
-template <typename T, int DP>
+// WARPS warps a row: one where rows are many; four, each with every fourth part,
+// where few rows have many parts (one request of 131000 tokens: 38 parts).
+template <typename T, int DP, int WARPS>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ AttnParams P, int ctas) {
-  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  constexpr int W = DP / 32, kAhead = 8;  // values a lane; rows of parts loaded at once
+  __shared__ float s_o[4][DP], s_m[4], s_l[4];
+  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned int ignored = 0;
   const Req r = request(P, b, ignored);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's writes
   if (r.n <= 0) return;
   const Plan L = make_plan(P, P.starts[P.B], ctas);
-  const long long first = P.starts[b];
+  const int first = P.starts[b];
   if (L.per_b <= 0) return;
   // without a prefix, requests whose units all lie within one share are done
-  const long long tiles_all = request_tiles(P, r);
-  if (P.prefix_len == 0 && first / L.per_b == (first + tiles_all - 1) / L.per_b) return;
+  if (P.prefix_len == 0 && first / L.per_b == (first + request_tiles(P, r) - 1) / L.per_b) return;
   const int rows = r.n * P.Hq;
-  for (int x = (blockIdx.y * 4 + (threadIdx.x >> 5)); x < rows; x += gridDim.y * 4) {
+  constexpr int kPerCta = 4 / WARPS;
+  for (int x = blockIdx.y * kPerCta + (WARPS == 1 ? warp : 0); x < rows; x += gridDim.y * kPerCta) {
     const int i = x / P.Hq, head = x - i * P.Hq;
     const int h = head / P.group, g = head - h * P.group;
     const size_t at = (size_t)(r.row0 + i) * P.Hq + head;
-    Joined<DP> acc;
-#pragma unroll
-    for (int y = 0; y < DP / 32; ++y) acc.o[y] = 0.f;
-    acc.m = -INFINITY;
-    acc.l = 0.f;
-    // the parts of a unit at u0 of list A (of its stream s) or B
-    auto unit = [&](bool pair, int s, long long u0, int tiles, int which, int slot_row) {
-      const long long per = pair ? L.per_a : L.per_b;
-      const long long c0 = u0 / per, c1 = (u0 + tiles - 1) / per;
-      if (c0 == c1) {
-        acc.add(P.dense[which] + at * DP, P.dense_lse[which][at]);
-        return;
-      }
-      for (long long c = c0; c <= c1; ++c) {
-        const long long id = pair ? 4 * c + s + 2 * (c == c0)
-                                  : 4 * (L.ctas_a + c / 2) + 2 * (c & 1) + (c == c0);
-        const size_t at_slot = (size_t)id * kRows + slot_row;
-        acc.add(P.slot + at_slot * DP, P.slot_lse[at_slot]);
-      }
-    };
     const int rb = i / P.tpq;
-    long long u0 = first;
-    for (int y = 0; y < rb; ++y) u0 += (long long)tiles_of(block_keys(P, r, y)) * P.Hk;
+    int u0 = first;
+    for (int y = 0; y < rb; ++y) u0 += tiles_of(block_keys(P, r, y)) * P.Hk;
     const int tiles = tiles_of(block_keys(P, r, rb));
-    u0 += (long long)h * tiles;
-    if (P.prefix_len == 0 && u0 / L.per_b == (u0 + tiles - 1) / L.per_b) continue;  // written already
-    if (P.prefix_len > 0) {
-      const int t = r.row0 + i, blk = t / P.tpq, slot_row = (t - blk * P.tpq) * P.group + g;
-      const bool pair = blk < 2 * P.pairs;
-      unit(pair, blk & 1, (pair ? (long long)h * P.pairs + blk / 2 : (long long)h) * P.prefix_tiles, P.prefix_tiles,
-           1, slot_row);
+    u0 += h * tiles;
+    Unit own, pre;
+    own.pair = false;
+    own.c0 = u0 / L.per_b;
+    own.count = (u0 + tiles - 1) / L.per_b - own.c0 + 1;
+    own.slot_row = (i - rb * P.tpq) * P.group + g;
+    own.stream = own.which = 0;
+    pre = own;
+    pre.count = 0;
+    if (P.prefix_len == 0) {
+      if (own.count == 1) continue;  // written already
+    } else {
+      const int t = r.row0 + i, blk = t / P.tpq;
+      pre.pair = blk < 2 * P.pairs;
+      pre.slot_row = (t - blk * P.tpq) * P.group + g;
+      pre.stream = blk & 1;
+      pre.which = 1;
+      const int per = pre.pair ? L.per_a : L.per_b;
+      const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * P.prefix_tiles;
+      pre.c0 = v0 / per;
+      pre.count = (v0 + P.prefix_tiles - 1) / per - pre.c0 + 1;
     }
-    unit(false, 0, u0, tiles, 0, (i - rb * P.tpq) * P.group + g);
-    const float inv = acc.l > 0.f || acc.l != acc.l ? 1.f / acc.l : 0.f;
-    if (DP == 128) {
+    const int all = pre.count + own.count;
+    const int skip = WARPS == 1 ? 0 : warp, parts = (all - skip + WARPS - 1) / WARPS;  // of this warp
+    // 32 parts at a time: their sums by lane, then their rows, eight loads under way
+    Joined<W> J;
+#pragma unroll
+    for (int y = 0; y < W; ++y) J.o[y] = 0.f;
+    J.m = -INFINITY;
+    J.l = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      const int k = (p0 + lane) * WARPS + skip;
+      const float* src = P.slot;
+      float lse2 = -INFINITY;
+      if (p0 + lane < parts) {
+        const Unit& u = k < pre.count ? pre : own;
+        const int j = k < pre.count ? k : k - pre.count;
+        if (u.count == 1) {
+          src = P.dense[u.which] + at * DP;
+          lse2 = P.dense_lse[u.which][at];
+        } else {
+          const int c = u.c0 + j;
+          const int id = u.pair ? 4 * c + u.stream + 2 * (j == 0) : 4 * (L.ctas_a + c / 2) + 2 * (c & 1) + (j == 0);
+          const size_t s = (size_t)id * kRows + u.slot_row;
+          src = P.slot + s * DP;
+          lse2 = P.slot_lse[s];
+        }
+      }
+      float top = lse2;  // (a NaN is dropped here, and kept by its weight)
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+      top = fmaxf(top, J.m);
+      const float scale = J.m == -INFINITY ? 0.f : exp2f(J.m - top);
+      const float w = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);  // -inf: no key seen there
+      float sum = w;
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+      J.l = J.l * scale + sum;
+      J.m = top;
+#pragma unroll
+      for (int y = 0; y < W; ++y) J.o[y] *= scale;
+      const int n = parts - p0 < 32 ? parts - p0 : 32;
+      for (int j0 = 0; j0 < n; j0 += kAhead) {
+        float v[kAhead][W], wj[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+          const float* pj = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), (j0 + j) & 31));
+          const bool in = j0 + j < n;
+          if (W == 4) {
+            const float4 q = in ? *reinterpret_cast<const float4*>(pj + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[j][0] = q.x, v[j][1] = q.y, v[j][2 % W] = q.z, v[j][3 % W] = q.w;
+          } else {
+            const float2 q = in ? *reinterpret_cast<const float2*>(pj + lane * 2) : make_float2(0.f, 0.f);
+            v[j][0] = q.x, v[j][1] = q.y;
+          }
+          if (!in) wj[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int y = 0; y < W; ++y) J.o[y] += wj[j] == 0.f ? 0.f : v[j][y] * wj[j];
+      }
+    }
+    if (WARPS > 1) {
+      // the warps' joins, in their order
+      __syncthreads();
+#pragma unroll
+      for (int y = 0; y < W; ++y) s_o[warp][lane * W + y] = J.o[y];
+      if (lane == 0) s_m[warp] = J.m, s_l[warp] = J.l;
+      __syncthreads();
+      if (warp != 0) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int y = 0; y < WARPS; ++y) top = fmaxf(top, s_m[y]);
+      J.l = 0.f;
+#pragma unroll
+      for (int y = 0; y < W; ++y) J.o[y] = 0.f;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        const float f = s_m[k] == -INFINITY && s_l[k] == 0.f ? 0.f : exp2f(s_m[k] - top);
+        J.l += s_l[k] * f;
+#pragma unroll
+        for (int y = 0; y < W; ++y) J.o[y] += f == 0.f ? 0.f : s_o[k][lane * W + y] * f;
+      }
+      J.m = top;
+    }
+    const float inv = J.l > 0.f || J.l != J.l ? 1.f / J.l : 0.f;
+    if (W == 4) {
       if (lane * 4 < P.D)
         *reinterpret_cast<uint2*>(P.out + (at * P.D + lane * 4) * 2) =
-            make_uint2(Type<T>::pack(acc.o[0] * inv, acc.o[1] * inv),
-                       Type<T>::pack(acc.o[2 % (DP / 32)] * inv, acc.o[3 % (DP / 32)] * inv));
+            make_uint2(Type<T>::pack(J.o[0] * inv, J.o[1] * inv), Type<T>::pack(J.o[2 % W] * inv, J.o[3 % W] * inv));
     } else if (lane * 2 < P.D) {
-      *reinterpret_cast<uint32_t*>(P.out + (at * P.D + lane * 2) * 2) =
-          Type<T>::pack(acc.o[0] * inv, acc.o[1] * inv);
+      *reinterpret_cast<uint32_t*>(P.out + (at * P.D + lane * 2) * 2) = Type<T>::pack(J.o[0] * inv, J.o[1] * inv);
     }
-    if (P.lse && lane == 0) P.lse[at] = (acc.m + log2f(acc.l)) * 0.693147180559945309f;
+    if (P.lse && lane == 0) P.lse[at] = (J.m + log2f(J.l)) * 0.693147180559945309f;
   }
 }
 
@@ -1158,7 +1222,7 @@ AttnLayout attn_layout(long long T, int Hq, int D) {
     at += sv::align256(bytes);
     return a;
   };
-  L.starts = take((size_t)(T + 1) * sizeof(long long));
+  L.starts = take((size_t)(T + 1) * sizeof(int));
   for (int i = 0; i < 2; ++i) L.dense[i] = take(rows * dp * 4);
   for (int i = 0; i < 2; ++i) L.dense_lse[i] = take(rows * 4);
   L.slot = take((size_t)kSlots * kRows * dp * 4);
@@ -1189,11 +1253,23 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   if (grid <= 0) return SV_ERR_CUDA;
   attention_kernel<T, DP><<<grid, kThreads, Shape<DP>::smem, stream>>>(m, P);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  // CTAs a request: four rows each, at most 64 of them
-  const long long rows = ((long long)(P.G < P.T ? P.G + 1 : P.T) * P.Hq + 3) / 4;
-  const dim3 g((unsigned int)P.B, (unsigned int)(rows < 64 ? rows : 64));
-  combine_kernel<T, DP><<<g, 128, 0, stream>>>(P, grid);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  // The launch itself overlaps the attention kernel, whose end the CTAs wait
+  // for.  Four warps a row where all rows are at most four waves of CTAs.
+  const long long rows = (long long)(P.G < P.T ? P.G + 1 : P.T) * P.Hq;
+  const bool few = (long long)P.T * P.Hq <= 4096;
+  const long long y = few ? rows : (rows + 3) / 4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned int)P.B, (unsigned int)(y < 1024 ? y : 1024));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few ? combine_kernel<T, DP, 4> : combine_kernel<T, DP, 1>, P, grid) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
 }
 
 }  // namespace
@@ -1257,15 +1333,19 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
     const int blocks = (P.T + P.tpq - 1) / P.tpq;
     P.pairs = blocks / 2;
     P.odd = blocks & 1;
-    if ((long long)P.pairs * P.Hk > INT32_MAX) return SV_ERR_SCALAR;
   }
+  // tiles of the longest lists that the arguments allow, in 32 bits
+  const double reach = (double)c.max_pages * c.page_size / kTile + 1.0;
+  if (((double)rows / P.tpq + c.batch) * P.Hk * reach > (double)(1 << 30) ||
+      ((double)rows / P.tpq + 1.0) * P.Hk * P.prefix_tiles > (double)(1 << 30))
+    return SV_ERR_SCALAR;
   P.mask = draft_mask;
   P.sl2 = scale * 1.44269504088896341f;
   P.out = static_cast<char*>(out);
   P.lse = lse;
   char* w = static_cast<char*>(workspace);
   P.status = reinterpret_cast<unsigned int*>(w);
-  P.starts = reinterpret_cast<long long*>(w + L.starts);
+  P.starts = reinterpret_cast<int*>(w + L.starts);
   for (int i = 0; i < 2; ++i) {
     P.dense[i] = reinterpret_cast<float*>(w + L.dense[i]);
     P.dense_lse[i] = reinterpret_cast<float*>(w + L.dense_lse[i]);
