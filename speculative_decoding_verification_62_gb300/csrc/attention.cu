@@ -12,25 +12,29 @@
 // Work: a unit is (request, block of query rows, key head) over the request's
 // own keys, or (block or pair of blocks of all requests' rows, key head) over
 // the prefix.  Blocks are 128 rows: tokens x heads of the key head's group.  The
-// units' tiles of 64 keys form two lists, A (pairs of blocks over the prefix) and
-// B (everything else).  The CTAs (one an SM) are dealt out to A and B by their
-// weights, and each CTA of A, and each of a B CTA's two streams, takes an equal
-// contiguous share of its list, so a batch of any raggedness, or one long
-// request, loads every SM alike.  A unit that crosses a share's border leaves
-// one part a share; combine_kernel joins them (and the prefix with the own
-// keys) by their sums.  No part is waited for inside a kernel, and parts are
-// joined in list order: results repeat bit for bit.
+// units' tiles of keys form two lists, A (pairs of blocks over the prefix, 128
+// keys a tile) and B (everything else, 64 keys).  The CTAs (one an SM) are dealt
+// out to A and B by their weights, and each CTA of A, and each of a B CTA's two
+// streams, takes an equal contiguous share of its list, so a batch of any
+// raggedness, or one long request, loads every SM alike.  A unit that crosses a
+// share's border leaves one part a share; combine_kernel joins them (and the
+// prefix with the own keys) by their sums.  No part is waited for inside a
+// kernel, and parts are joined in list order: results repeat bit for bit.
 //
-// A CTA holds two streams.  A stream is a softmax warpgroup, a copy warp, a
-// matrix warp, a query tile in shared memory and 256 columns of tensor memory:
-// two score tiles S (128 rows x 64 keys) and the output O.  S = Q K^T and O += P V
-// are tcgen05 products; P overwrites its S.  With two score tiles the product
-// of the next keys runs beside the softmax.  In a B CTA the streams are
-// independent (a ring of five 64-key slots each): one stream's start and end of
-// a unit hide behind the other's.  In an A CTA each stream has one block and
-// both read every key and value slot of one ring of ten.  Keys and values
-// arrive by TMA, a page (at most 64 tokens) and 64 values a box, with 128-byte
-// swizzle; the layout of the page pool is only the tensor map's strides.
+// A CTA holds two streams.  A stream is a softmax warpgroup, a matrix warp, a
+// query tile in shared memory and 256 columns of tensor memory for S and O.
+// S = Q K^T and O += P V are tcgen05 products; P overwrites its S.
+// B reads keys from memory once and is bound by that: its streams are independent
+// (each with a copy warp and a ring of five 64-key slots), so that one stream's
+// start and end of a unit hide behind the other's, and each has two score tiles,
+// so that the product of the next keys runs beside the softmax.
+// A is bound by the products: a product of 128 rows and 64 keys takes as long as
+// one of 128 keys, so its tiles have 128.  Each stream has one block of rows and
+// both read every key and value slot of one ring of five; one stream's softmax
+// runs beside the other's products, and P goes over in halves.
+// Keys and values arrive by TMA, a page (at most 64 tokens) and 64 values a box,
+// with 128-byte swizzle; the layout of the page pool is only the tensor map's
+// strides.
 //
 // S and the sums are 32 bits.  P is rounded to the cache's 16-bit type for the
 // product (at most half a step of a weight, below the rounding of the output's
@@ -52,24 +56,26 @@
 namespace {
 
 constexpr int kRows = 128;      // rows a block
-constexpr int kTile = 64;       // keys a tile
+constexpr int kTile = 64;       // keys a tile of list B, and a box
+constexpr int kPairTile = 128;  // keys a tile of list A
 constexpr int kThreads = 384;   // warps 0-3, 4-7: softmax; 8, 10: copies; 9, 11: products
 constexpr int kMaxCtas = 160;   // CTAs at most (the slots of parts are sized for this)
 constexpr int kSlots = 4 * kMaxCtas;  // parts: two a stream
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
 constexpr int kControl = 3072;  // barriers and small tables behind the tiles
 // Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs.
-constexpr int kCostA = 10, kCostB = 9;
+constexpr int kCostA = 18, kCostB = 9;
 
-template <int DP>
+template <int DP, bool PAIR>
 struct Shape {
+  static constexpr int keys = PAIR ? kPairTile : kTile;
   static constexpr int halves = DP / 64;
   static constexpr int q_bytes = kRows * DP * 2;
-  static constexpr int q_half = kRows * 128;     // 64 values of every row
-  static constexpr int tile_bytes = kTile * DP * 2;
-  static constexpr int half_bytes = kTile * 128;
-  static constexpr int slots = 10;               // in all; five a stream in B
-  static constexpr int smem = 2 * q_bytes + slots * tile_bytes + kControl;
+  static constexpr int q_half = kRows * 128;       // 64 values of every row
+  static constexpr int tile_bytes = keys * DP * 2;
+  static constexpr int half_bytes = keys * 128;
+  static constexpr int ring = 5 * kPairTile * DP * 2;
+  static constexpr int smem = 2 * q_bytes + ring + kControl;
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
@@ -80,7 +86,8 @@ struct AttnParams {
   const int32_t* kv_len;
   const int32_t* cu;
   const int32_t* prefix_table;
-  int prefix_len, prefix_tiles, pairs, odd;  // pairs of row blocks over the prefix, and a single one
+  int prefix_len, prefix_tiles, pair_tiles;  // tiles of the prefix in list B and in list A
+  int pairs, odd;                            // pairs of row blocks, and a single one
   const uint32_t* mask;
   float sl2;  // scale log2(e)
   char* out;
@@ -127,15 +134,19 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 // Waits for a phase, at most wait_ns; false (and *abort set) when that ran out
-// or another warp of the CTA gave up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
-                                         volatile int* abort) {
+// or another warp of the CTA gave up.  The loop stands once in the code: the
+// kernel's instructions have to stay in the cache.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
+                                           volatile int* abort) {
   // ordinary waits end within these tries (a try suspends the warp for a while
   // itself) and read no timer
+#pragma unroll 1
   for (int i = 0; i < 256; ++i)
     if (bar_try(bar, parity)) return true;
   const unsigned long long t0 = now_ns();
+#pragma unroll 1
   for (;;) {
+#pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (bar_try(bar, parity)) return true;
     if (*abort) return false;
@@ -144,6 +155,10 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned
       return false;
     }
   }
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
+                                         volatile int* abort) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, wait_ns, abort);
 }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                          int y, int z, int w) {
@@ -290,6 +305,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// 32 bytes: a lane has a row of its own, so that each store fills a sector
+__device__ __forceinline__ void store8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), SV_W8(v, 0) : "memory");
+}
 // Shared-memory matrix descriptors, 128-byte swizzle: K-major (rows of 64
 // values, eight rows 1024 bytes apart) and MN-major (tokens as rows; the next
 // 64 values of a token `lead` bytes on, eight tokens 1024 bytes apart).
@@ -352,6 +371,7 @@ __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / 
 __device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) {
   if (r.n <= 0) return 0;
   int t = 0;
+#pragma unroll 1
   for (int rb = 0; rb * P.tpq < r.n; ++rb) t += tiles_of(block_keys(P, r, rb));
   return t * P.Hk;
 }
@@ -364,7 +384,7 @@ struct Plan {
 };
 __device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int ctas) {
   Plan L;
-  L.a = P.Hk * P.pairs * P.prefix_tiles;
+  L.a = P.Hk * P.pairs * P.pair_tiles;
   L.b = b_tiles;
   int na = 0;
   if (L.a > 0) {
@@ -406,6 +426,7 @@ struct Walk {
   __device__ __forceinline__ void load_request(const AttnParams& P) {
     unsigned int ignored = 0;
     r = Req{0, 0, 0};
+#pragma unroll 1
     while (b < P.B) {
       r = request(P, b, ignored);
       if (r.n > 0) return;
@@ -427,7 +448,7 @@ struct Walk {
       p.ntok = P.T - p.row0;
       p.kv = p.first = 0;
       p.keys = P.prefix_len;
-      p.unit_t = P.prefix_tiles;
+      p.unit_t = pair ? P.pair_tiles : P.prefix_tiles;
     } else {
       if (b >= P.B) return false;
       p.b = b;
@@ -460,7 +481,7 @@ struct Walk {
 struct Control {
   uint64_t kv_full[10], kv_empty[10];
   // of each stream
-  uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], pv_done[2], o_full[2], o_free[2], drain[2];
+  uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
   int abort;
   unsigned int q_copied[2], kv_copied[2];
@@ -469,14 +490,13 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kControl, "control block");
 
-// Where a stream's ring entries lie: A shares ten slots, B has five a stream.
+// Barriers of a stream's ring entries (A: both streams', 0 to 4).
 template <bool PAIR>
 __device__ __forceinline__ uint32_t slot_of(int s, unsigned int e) {
-  return PAIR ? e % 10u : s * 5u + e % 5u;
+  return (PAIR ? 0u : s * 5u) + e % 5u;
 }
-template <bool PAIR>
 __device__ __forceinline__ uint32_t turn_of(unsigned int e) {  // parity of the slot's use
-  return (PAIR ? e / 10u : e / 5u) & 1u;
+  return (e / 5u) & 1u;
 }
 // The order of a piece's tiles in the ring: keys one tile ahead of values.
 __device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
@@ -496,18 +516,19 @@ template <int DP, bool PAIR>
 __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t q_smem,
                                           uint32_t ring, const CUtensorMap* qmap, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap) {
-  using S = Shape<DP>;
+  using S = Shape<DP, PAIR>;
   const int lane = threadIdx.x & 31;
   unsigned int flags = 0, base = 0, qn = 0, last = 0;
   Piece p;
   bool ok = true;
+#pragma unroll 1
   while (ok && w.next(P, p)) {
     const int n = p.t1 - p.t0;
     // a lane's page of tile i (a box is at most a page)
     auto page_of = [&](int i) {
-      const int key = (p.t0 + i) * kTile + lane * P.box_rows;
+      const int key = (p.t0 + i) * S::keys + lane * P.box_rows;
       int id = 0;
-      if (lane * P.box_rows < kTile && key < p.keys) {
+      if (lane * P.box_rows < S::keys && key < p.keys) {
         id = __ldg(p.prefix ? P.prefix_table + (key >> P.page_shift)
                             : P.table + (size_t)p.b * P.max_pages + (key >> P.page_shift));
         if (id < 0 || id >= P.num_pages) {
@@ -536,6 +557,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
       }
       ++qn;
     }
+#pragma unroll 1
     for (int y = 0; ok && y < 2 * n; ++y) {
       const bool is_v = y == 2 * n - 1 || (y > 0 && !(y & 1));
       if (PAIR && is_v != (s == 1)) continue;
@@ -548,17 +570,17 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
       const int mine = i == at ? id : before;
       const unsigned int e = base + y;
       const uint32_t slot = slot_of<PAIR>(s, e);
-      const int key0 = (p.t0 + i) * kTile;
-      const int keys = p.keys - key0 < kTile ? p.keys - key0 : kTile;
+      int key = (p.t0 + i) * S::keys;
+      const int keys = p.keys - key < S::keys ? p.keys - key : S::keys;
       const int boxes = (keys + P.box_rows - 1) / P.box_rows;
-      const int in = key0 & (P.page_size - 1);
-      if (!(ok = warp_wait(&c->kv_empty[slot], turn_of<PAIR>(e) ^ 1, P, c))) break;
+      if (!(ok = warp_wait(&c->kv_empty[slot], turn_of(e) ^ 1, P, c))) break;
       const uint32_t bar = smem_addr(&c->kv_full[slot]);
       const CUtensorMap* map = is_v ? vmap : kmap;
       uint32_t dst = ring + slot * S::tile_bytes;
       if (elect_one()) bar_expect(bar, (uint32_t)(boxes * S::halves * 128 * P.box_rows));
-      for (int x = 0; x < boxes; ++x, dst += P.box_rows * 128) {
-        const int page = __shfl_sync(0xffffffffu, mine, x);
+#pragma unroll 1
+      for (int x = 0; x < boxes; ++x, dst += P.box_rows * 128, key += P.box_rows) {
+        const int page = __shfl_sync(0xffffffffu, mine, x), in = key & (P.page_size - 1);
         if (elect_one()) {
           tma_load(dst, map, bar, 0, in, p.h, page);
           if (S::halves == 2) tma_load(dst + S::half_bytes, map, bar, 64, in, p.h, page);
@@ -577,80 +599,127 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
   if (lane == 0 && any) atomicOr(P.status, any);
 }
 
-// Products of one stream.  (All 512 columns are allocated, so they start at 0.)
+// Products of one stream, by one thread.  (All 512 columns are allocated, so they start at 0.)
 template <typename T, int DP, bool PAIR>
 __device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t q_smem,
                                             uint32_t ring, unsigned char* ring_ptr) {
-  using S = Shape<DP>;
-  const int lane = threadIdx.x & 31;
-  const uint32_t cols = s * 256;  // S, S, O of this stream
-  constexpr uint32_t kQk = instr_desc(Type<T>::fmt, kTile, false);
+  using S = Shape<DP, PAIR>;
+  if (!elect_one()) return;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return bar_wait(smem_addr(bar), parity, P.wait_ns, &c->abort); };
+  const uint32_t cols = s * 256;  // S (128 columns: B: two tiles), O of this stream
+  constexpr uint32_t kQk = instr_desc(Type<T>::fmt, S::keys, false);
   constexpr uint32_t kPv = instr_desc(Type<T>::fmt, DP, true);
+  constexpr int kAhead = PAIR ? 1 : 2;  // score tiles
   const uint32_t q = q_smem + s * S::q_bytes;
   unsigned int base = 0, pieces = 0, tiles = 0;  // tiles: of the pieces so far
   Piece p;
   bool ok = true;
+#pragma unroll 1
   while (ok && w.next(P, p)) {
     const int n = p.t1 - p.t0;
     auto qk = [&](int i) {
       const unsigned int e = base + k_entry(i), t = tiles + i;
-      const uint32_t slot = slot_of<PAIR>(s, e);
-      if (i == 0 && !(ok = warp_wait(&c->q_full[s], pieces & 1, P, c))) return;
-      if (!(ok = warp_wait(&c->kv_full[slot], turn_of<PAIR>(e), P, c))) return;
-      if (elect_one()) {
+      const uint32_t slot = slot_of<PAIR>(s, e), buf = PAIR ? 0 : t & 1;
+      if (i == 0 && !(ok = wait(&c->q_full[s], pieces & 1))) return;
+      if (!(ok = wait(&c->kv_full[slot], turn_of(e)))) return;
+      {
         const uint32_t b = ring + slot * S::tile_bytes;
 #pragma unroll
         for (int x = 0; x < S::halves; ++x)
-          mma_ss4(cols + (t & 1) * kTile, mat_desc(q + x * S::q_half, 16), mat_desc(b + x * S::half_bytes, 16),
-                  kQk, x > 0);
-        mma_commit(smem_addr(&c->s_full[s][t & 1]));
-        mma_commit(smem_addr(&c->kv_empty[slot]));
+          mma_ss4(cols + buf * kTile, mat_desc(q + x * S::q_half, 16), mat_desc(b + x * S::half_bytes, 16), kQk, x > 0);
+        mma_commit(smem_addr(&c->s_full[s][buf]));  // (the softmax warps hand the keys' slot back)
         if (i == n - 1) mma_commit(smem_addr(&c->q_empty[s]));
       }
-      __syncwarp();
     };
     qk(0);
-    if (ok && n > 1) qk(1);
+    if (!PAIR && ok && n > 1) qk(1);
+#pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
       const unsigned int e = base + v_entry(i, n), t = tiles + i;
       const uint32_t slot = slot_of<PAIR>(s, e);
-      if (i == 0 && pieces > 0 && !(ok = warp_wait(&c->o_free[s], (pieces - 1) & 1, P, c))) break;
-      int keys = p.keys - (p.t0 + i) * kTile;
-      keys = keys < kTile ? keys : kTile;
+      if (i == 0 && pieces > 0 && !(ok = wait(&c->o_free[s], (pieces - 1) & 1))) break;
+      int keys = p.keys - (p.t0 + i) * S::keys;
+      keys = keys < S::keys ? keys : S::keys;
       const int steps = (keys + 15) / 16;
-      if (!(ok = warp_wait(&c->kv_full[slot], turn_of<PAIR>(e), P, c))) break;
+      if (!(ok = wait(&c->kv_full[slot], turn_of(e)))) break;
       if (keys & 15) {
         // rows behind the last key of the last 16: what memory held there
         // (weights of 0 times NaN would be NaN).  In A both streams' warps
         // write the same zeros.
-        for (int x = lane; x < (steps * 16 - keys) * S::halves * 8; x += 32) {
+#pragma unroll 1
+        for (int x = 0; x < (steps * 16 - keys) * S::halves * 8; ++x) {
           const int row = keys + x / (S::halves * 8), in = x % (S::halves * 8);
           *reinterpret_cast<uint4*>(ring_ptr + slot * S::tile_bytes + (in / 8) * S::half_bytes + row * 128 +
                                     (in % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
       }
-      if (!(ok = warp_wait(&c->p_ready[s][t & 1], (t >> 1) & 1, P, c))) break;
-      fence_after();
-      if (elect_one()) {
-        const uint32_t a = cols + (t & 1) * kTile, d = cols + 2 * kTile;
-        const uint64_t v = mat_desc(ring + slot * S::tile_bytes, S::half_bytes);
-        if (steps == 4) {
-          mma_ts4(d, a, v, kPv, i > 0);
-        } else {
-          for (int k = 0; k < steps; ++k) mma_ts(d, a + k * 8, v + k * 128, kPv, i > 0 || k > 0);
+      const uint32_t d = cols + 2 * kTile;
+      const uint64_t v = mat_desc(ring + slot * S::tile_bytes, S::half_bytes);
+#pragma unroll
+      for (int x = 0; x < (PAIR ? 2 : 1); ++x) {
+        const uint32_t buf = PAIR ? x : t & 1;
+        if (!(ok = wait(&c->p_ready[s][buf], PAIR ? t & 1 : (t >> 1) & 1))) break;
+        fence_after();
+        const uint32_t a = PAIR ? cols + x * 32 : cols + buf * kTile;
+        const int left = steps - 4 * x;
+        {
+          if (left >= 4) {
+            mma_ts4(d, a, v + x * 512, kPv, i > 0 || x > 0);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < left; ++k) mma_ts(d, a + k * 8, v + x * 512 + k * 128, kPv, i > 0 || x > 0 || k > 0);
+          }
+          if (!PAIR || x == 1) {
+            mma_commit(smem_addr(&c->kv_empty[slot]));
+            if (i == n - 1) mma_commit(smem_addr(&c->o_full[s]));
+          }
         }
-        mma_commit(smem_addr(&c->kv_empty[slot]));
-        mma_commit(smem_addr(&c->pv_done[s]));
-        if (i == n - 1) mma_commit(smem_addr(&c->o_full[s]));
       }
-      __syncwarp();
-      if (i + 2 < n) qk(i + 2);
+      if (ok && i + kAhead < n) qk(i + kAhead);
     }
     base += 2 * n;
     tiles += n;
     ++pieces;
+  }
+}
+
+// Which of the 32 keys from `at` a row sees: all below `limit`, or, with a mask
+// word, those below kv and those of the step that it names.
+__device__ __forceinline__ uint32_t seen(int at, int limit, bool by_word, uint32_t word, int kv) {
+  if (by_word) {
+    const int d = at - kv;  // the first key's place in the step's rows
+    return d <= -32 ? ~0u : d < 0 ? (word << -d) | ((1u << -d) - 1u) : d < 32 ? word >> d : 0u;
+  }
+  const int k = limit - at;
+  return k >= 32 ? ~0u : k > 0 ? (1u << k) - 1u : 0u;
+}
+__device__ __forceinline__ void hide(uint32_t* v, uint32_t see) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!((see >> x) & 1u)) v[x] = __float_as_uint(-INFINITY);
+}
+__device__ __forceinline__ void max32(const uint32_t* v, float& a, float& b) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 4) {
+    a = max3(a, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+    b = max3(b, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+  }
+}
+// Weights of 32 scores: 2^(scale s - m), packed into v[0 .. 15], and their sums.
+template <typename T>
+__device__ __forceinline__ void weights32(const uint32_t* v, uint32_t* out, uint64_t sl2, uint64_t sub, uint64_t& sum0,
+                                          uint64_t& sum1) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 4) {
+    float a, b, e, f;
+    unpair(pair_fma(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl2, sub), a, b);
+    unpair(pair_fma(pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl2, sub), e, f);
+    a = exp2_fast(a), b = exp2_fast(b), e = exp2_fast(e), f = exp2_fast(f);
+    sum0 = pair_add(sum0, pair(a, b));
+    sum1 = pair_add(sum1, pair(e, f));
+    out[x / 2] = Type<T>::pack(a, b);
+    out[x / 2 + 1] = Type<T>::pack(e, f);
   }
 }
 
@@ -661,9 +730,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
   const uint32_t s_cols = lanes + s * 256, o_col = s_cols + 2 * kTile;
   const float ninf = -INFINITY;
   const int tok = row / P.group, g = row - tok * P.group;
-  unsigned int tiles = 0, pieces = 0;
+  using S = Shape<DP, PAIR>;
+  unsigned int tiles = 0, pieces = 0, base = 0;
   Piece p;
   bool ok = true;
+#pragma unroll 1
   while (ok && w.next(P, p)) {
     const int n = p.t1 - p.t0;
     const int skip = PAIR ? s * P.tpq : 0;  // rows of the other stream's block
@@ -671,98 +742,130 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
     btok = btok < P.tpq ? btok : P.tpq;
     const int rows = btok * P.group;
     const bool active = (row & ~31) < rows, mine = row < rows;
-    // keys this row sees: all below `limit`, or below `free` and by its mask word
+    // keys this row sees: all below `limit` or by its mask word; `free`: the keys
+    // that every row of the block sees
+    const bool by_word = !p.prefix && P.mask;
     const int limit = p.prefix ? P.prefix_len : p.kv + p.first + tok + 1;
     const int free = p.prefix ? P.prefix_len : (P.mask ? p.kv : p.kv + p.first + 1);
     uint32_t word = 0;
-    if (!p.prefix && P.mask && mine) {
+    if (by_word && mine) {
       word = P.mask[p.row0 + tok];
       if (p.keys - p.kv < 32) word &= (1u << (p.keys - p.kv)) - 1u;  // rows of the step
     }
     float m = ninf, l = 0.f;  // running maximum (times scale log2 e) and sum
-    for (int i = 0; i < n; ++i, ++tiles) {
-      const uint32_t s_col = s_cols + (tiles & 1) * kTile;
-      if (!(ok = warp_wait(&c->s_full[s][tiles & 1], (tiles >> 1) & 1, P, c))) break;
-      if (active) {
+    // Moves the maximum to the new scores' where that grows by more than 8.
+    auto settle = [&](int i, float top) {
+      if (i == 0) {
+        m = top;
+        return;
+      }
+      const bool grow = top > m + 8.f || (m == ninf && top > ninf);
+      if (!__any_sync(0xffffffffu, grow)) return;
+      const float f = grow ? (m == ninf ? 0.f : exp2_fast(m - top)) : 1.f;
+      // O is at rest once the last tile's product is done.  In A S of this tile
+      // came after it; in B its values' slot has been handed back (the slot's
+      // next use cannot end before this tile's own product).
+      if (!PAIR) {
+        const unsigned int e = base + v_entry(i - 1, n);
+        if (!(ok = warp_wait(&c->kv_empty[slot_of<PAIR>(s, e)], turn_of(e), P, c))) return;
         fence_after();
-        uint32_t v[kTile];
-        tmem_load32(s_col, v);
-        tmem_load32(s_col + 32, v + 32);
+      }
+#pragma unroll 1
+      for (int x = 0; x < DP; x += 16) {
+        uint32_t o[16];
+        tmem_load16(o_col + x, o);
         tmem_wait_load();
-        tmem_loaded32(v);
-        tmem_loaded32(v + 32);
-        const int key0 = (p.t0 + i) * kTile;
-        if (key0 + kTile > free) {
+        tmem_loaded16(o);
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const int at = key0 + 32 * ch;
-            uint32_t see;  // bit x: key at + x is seen
-            if (!p.prefix && P.mask) {
-              const int d = at - p.kv;  // the chunk's first key in the step's rows
-              see = d <= -32 ? ~0u : d < 0 ? (word << -d) | ((1u << -d) - 1u) : d < 32 ? word >> d : 0u;
-            } else {
-              const int k = limit - at;
-              see = k >= 32 ? ~0u : k > 0 ? (1u << k) - 1u : 0u;
-            }
+        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+        tmem_store16(o_col + x, o);
+      }
+      l *= f;
+      if (grow) m = top;
+    };
+    const uint64_t sl2 = pair(P.sl2, P.sl2);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, ++tiles) {
+      const uint32_t buf = PAIR ? 0 : tiles & 1, s_col = s_cols + buf * kTile;
+      if (!(ok = warp_wait(&c->s_full[s][buf], PAIR ? tiles & 1 : (tiles >> 1) & 1, P, c))) break;
+      if (threadIdx.x % 128 == 0) bar_arrive(smem_addr(&c->kv_empty[slot_of<PAIR>(s, base + k_entry(i))]));
+      const int key0 = (p.t0 + i) * S::keys;
+      const bool masked = key0 + S::keys > free;
+      uint64_t sum0 = 0, sum1 = 0;  // two pairs of zeros
+      if (PAIR) {
+        // S is read twice, 32 columns at a time, the next ones on their way: for
+        // the maximum, then for the weights (128 values held at once spill)
+        uint32_t v[2][32];
+        if (active) {
+          fence_after();
+          float mx0 = ninf, mx1 = ninf;
+          tmem_load32(s_col, v[0]);
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((see >> x) & 1u)) v[32 * ch + x] = __float_as_uint(ninf);
+          for (int ch = 0; ch < 4; ++ch) {
+            tmem_wait_load();
+            tmem_loaded32(v[ch & 1]);
+            tmem_load32(s_col + ((ch + 1) & 3) * 32, v[(ch + 1) & 1]);
+            if (masked) hide(v[ch & 1], seen(key0 + 32 * ch, limit, by_word, word, p.kv));
+            max32(v[ch & 1], mx0, mx1);
           }
-        }
-        float mx0 = ninf, mx1 = ninf;
-#pragma unroll
-        for (int x = 0; x < kTile; x += 4) {
-          mx0 = max3(mx0, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-          mx1 = max3(mx1, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-        }
-        const float top = fmaxf(mx0, mx1) * P.sl2;
-        if (i == 0) {
-          m = top;
-        } else {
-          const bool grow = top > m + 8.f || (m == ninf && top > ninf);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? (m == ninf ? 0.f : exp2_fast(m - top)) : 1.f;
-            // (no product but the last can be under way: S of this tile came
-            // after the one before it, and the next waits for this tile's P)
-            if (!(ok = warp_wait(&c->pv_done[s], (tiles - 1) & 1, P, c))) break;
-            fence_after();
-            for (int x = 0; x < DP; x += 16) {
-              uint32_t o[16];
-              tmem_load16(o_col + x, o);
-              tmem_wait_load();
-              tmem_loaded16(o);
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_store16(o_col + x, o);
-            }
-            l *= f;
-            if (grow) m = top;
-          }
+          settle(i, fmaxf(mx0, mx1) * P.sl2);
         }
         const float neg = m == ninf ? 0.f : -m;
-        const uint64_t sub = pair(neg, neg), sl2 = pair(P.sl2, P.sl2);
-        uint64_t sum0 = 0, sum1 = 0;  // two pairs of zeros
+        const uint64_t sub = pair(neg, neg);
 #pragma unroll
-        for (int x = 0; x < kTile; x += 4) {
-          float a, b, e, f;
-          unpair(pair_fma(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl2, sub), a, b);
-          unpair(pair_fma(pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl2, sub), e, f);
-          a = exp2_fast(a), b = exp2_fast(b), e = exp2_fast(e), f = exp2_fast(f);
-          sum0 = pair_add(sum0, pair(a, b));
-          sum1 = pair_add(sum1, pair(e, f));
-          v[x / 2] = Type<T>::pack(a, b);
-          v[x / 2 + 1] = Type<T>::pack(e, f);
+        for (int ch = 0; ch < 4; ++ch) {
+          if (active) {
+            uint32_t w16[16];
+            tmem_wait_load();
+            tmem_loaded32(v[ch & 1]);
+            if (ch < 3) tmem_load32(s_col + (ch + 1) * 32, v[(ch + 1) & 1]);
+            if (masked) hide(v[ch & 1], seen(key0 + 32 * ch, limit, by_word, word, p.kv));
+            weights32<T>(v[ch & 1], w16, sl2, sub, sum0, sum1);
+            tmem_store16(s_col + ch * 16, w16);  // over columns of S that are read already
+          }
+          if (ch & 1) {
+            if (active) {
+              tmem_wait_store();
+              fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][ch >> 1]));
+          }
         }
-        tmem_store32(s_col, v);
-        float a, b;
-        unpair(pair_add(sum0, sum1), a, b);
-        l += a + b;
-        tmem_wait_store();
-        fence_before();
+      } else {
+        if (active) {
+          fence_after();
+          uint32_t v[kTile];
+          tmem_load32(s_col, v);
+          tmem_load32(s_col + 32, v + 32);
+          tmem_wait_load();
+          tmem_loaded32(v);
+          tmem_loaded32(v + 32);
+          if (masked) {
+            hide(v, seen(key0, limit, by_word, word, p.kv));
+            hide(v + 32, seen(key0 + 32, limit, by_word, word, p.kv));
+          }
+          float mx0 = ninf, mx1 = ninf;
+          max32(v, mx0, mx1);
+          max32(v + 32, mx0, mx1);
+          settle(i, fmaxf(mx0, mx1) * P.sl2);
+          if (!ok) break;
+          const float neg = m == ninf ? 0.f : -m;
+          const uint64_t sub = pair(neg, neg);
+          weights32<T>(v, v, sl2, sub, sum0, sum1);
+          weights32<T>(v + 32, v + 16, sl2, sub, sum0, sum1);
+          tmem_store32(s_col, v);
+          tmem_wait_store();
+          fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][buf]));
       }
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][tiles & 1]));
+      float a, b;
+      unpair(pair_add(sum0, sum1), a, b);
+      l += a + b;
     }
+    base += 2 * n;
     if (!ok) break;
     // the piece's rows, after its last product (a barrier of its own: parity
     // would not tell that product from the one two before it)
@@ -787,7 +890,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           part_lse = P.slot_lse + r;
         }
       }
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < DP; x += 32) {
         uint32_t o[32];
         tmem_load32(o_col + x, o);
@@ -811,8 +914,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
             }
           } else {
 #pragma unroll
-            for (int y = 0; y < 32; y += 4)
-              *reinterpret_cast<uint4*>(part + x + y) = make_uint4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+            for (int y = 0; y < 32; y += 8) store8(part + x + y, o + y);
           }
         }
       }
@@ -834,7 +936,7 @@ template <typename T, int DP, bool PAIR>
 __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsigned char* tiles, const CUtensorMap* qmap,
                                           const CUtensorMap* kmap,
                                           const CUtensorMap* vmap) {
-  using S = Shape<DP>;
+  using S = Shape<DP, PAIR>;
   const int warp = threadIdx.x >> 5;
   const int s = warp < 8 ? warp >> 2 : (warp - 8) >> 1;
   const uint32_t q_smem = smem_addr(tiles), ring = q_smem + 2 * S::q_bytes;
@@ -852,6 +954,7 @@ __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsig
     // before shared and tensor memory are given back
     int ignored = 0;
     if (warp == 8 || warp == 10) {
+#pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const unsigned int q = c->q_copied[PAIR ? 0 : x];
         if (q > 0 && (PAIR || x == s)) (void)bar_wait(smem_addr(&c->q_full[x]), (q - 1) & 1, kDrainNs, &ignored);
@@ -860,9 +963,10 @@ __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsig
       // warps' entries interleave: all up to the later one's last are waited
       // for, an entry that was never started runs out
       const unsigned int a = c->kv_copied[0], b = c->kv_copied[1];
-      const unsigned int end = PAIR ? (a > b ? a : b) : c->kv_copied[s], count = PAIR ? 10 : 5;
-      for (unsigned int e = end > count ? end - count : 0; e < end; ++e)
-        (void)bar_wait(smem_addr(&c->kv_full[slot_of<PAIR>(s, e)]), turn_of<PAIR>(e), kDrainNs, &ignored);
+      const unsigned int end = PAIR ? (a > b ? a : b) : c->kv_copied[s];
+#pragma unroll 1
+      for (unsigned int e = end > 5 ? end - 5 : 0; e < end; ++e)
+        (void)bar_wait(smem_addr(&c->kv_full[slot_of<PAIR>(s, e)]), turn_of(e), kDrainNs, &ignored);
     } else if (warp >= 8) {
       if (elect_one()) mma_commit(smem_addr(&c->drain[s]));
       __syncwarp();
@@ -879,9 +983,9 @@ struct Maps {
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams P) {
-  using S = Shape<DP>;
+  using S = Shape<DP, false>;
   extern __shared__ __align__(1024) unsigned char tiles[];
-  Control* c = reinterpret_cast<Control*>(tiles + 2 * S::q_bytes + S::slots * S::tile_bytes);
+  Control* c = reinterpret_cast<Control*>(tiles + 2 * S::q_bytes + S::ring);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_addr(tiles) & 1023) {  // the swizzle's period; never expected
     if (tid == 0) atomicOr(P.status, (unsigned int)SV_STATUS_INTERNAL);
@@ -900,6 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     r = request(P, b, flags);
     mine += request_tiles(P, r);
@@ -915,7 +1020,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(smem_addr(&c->s_full[s][i]), 1);
         bar_init(smem_addr(&c->p_ready[s][i]), 4);
       }
-      bar_init(smem_addr(&c->pv_done[s]), 1);
       bar_init(smem_addr(&c->o_full[s]), 1);
       bar_init(smem_addr(&c->o_free[s]), 4);
       bar_init(smem_addr(&c->drain[s]), 1);
@@ -961,17 +1065,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.unit = w.b = w.rb = w.h = w.off = 0;
       w.r = r;
       if (unit) {
-        w.unit = g0 / P.prefix_tiles;
-        w.off = g0 - w.unit * P.prefix_tiles;
+        const int t = pair_cta ? P.pair_tiles : P.prefix_tiles;
+        w.unit = g0 / t;
+        w.off = g0 - w.unit * t;
       } else {
         int rem = g0 - excl;
         unsigned int ignored = 0;
+#pragma unroll 1
         for (w.b = b0; w.b < b1 - 1; ++w.b) {
           const int t = request_tiles(P, request(P, w.b, ignored));
           if (rem < t) break;
           rem -= t;
         }
         if (b1 - b0 > 1) w.r = request(P, w.b, ignored);
+#pragma unroll 1
         for (; w.rb * P.tpq < w.r.n; ++w.rb) {
           const int t = tiles_of(block_keys(P, w.r, w.rb));
           if (rem < t * P.Hk) {
@@ -987,6 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (blockIdx.x == 0) {
     int at = excl;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       P.starts[b] = at;
       if (b + 1 < b1) {
@@ -1045,12 +1153,14 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
   if (P.prefix_len == 0 && first / L.per_b == (first + request_tiles(P, r) - 1) / L.per_b) return;
   const int rows = r.n * P.Hq;
   constexpr int kPerCta = 4 / WARPS;
+#pragma unroll 1
   for (int x = blockIdx.y * kPerCta + (WARPS == 1 ? warp : 0); x < rows; x += gridDim.y * kPerCta) {
     const int i = x / P.Hq, head = x - i * P.Hq;
     const int h = head / P.group, g = head - h * P.group;
     const size_t at = (size_t)(r.row0 + i) * P.Hq + head;
     const int rb = i / P.tpq;
     int u0 = first;
+#pragma unroll 1
     for (int y = 0; y < rb; ++y) u0 += tiles_of(block_keys(P, r, y)) * P.Hk;
     const int tiles = tiles_of(block_keys(P, r, rb));
     u0 += h * tiles;
@@ -1071,9 +1181,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
       pre.stream = blk & 1;
       pre.which = 1;
       const int per = pre.pair ? L.per_a : L.per_b;
-      const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * P.prefix_tiles;
+      const int t_unit = pre.pair ? P.pair_tiles : P.prefix_tiles;
+      const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * t_unit;
       pre.c0 = v0 / per;
-      pre.count = (v0 + P.prefix_tiles - 1) / per - pre.c0 + 1;
+      pre.count = (v0 + t_unit - 1) / per - pre.c0 + 1;
     }
     const int all = pre.count + own.count;
     const int skip = WARPS == 1 ? 0 : warp, parts = (all - skip + WARPS - 1) / WARPS;  // of this warp
@@ -1083,6 +1194,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     for (int y = 0; y < W; ++y) J.o[y] = 0.f;
     J.m = -INFINITY;
     J.l = 0.f;
+#pragma unroll 1
     for (int p0 = 0; p0 < parts; p0 += 32) {
       const int k = (p0 + lane) * WARPS + skip;
       const float* src = P.slot;
@@ -1115,6 +1227,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
 #pragma unroll
       for (int y = 0; y < W; ++y) J.o[y] *= scale;
       const int n = parts - p0 < 32 ? parts - p0 : 32;
+#pragma unroll 1
       for (int j0 = 0; j0 < n; j0 += kAhead) {
         float v[kAhead][W], wj[kAhead];
 #pragma unroll
@@ -1240,7 +1353,7 @@ int grid_size() {
   if ((c0 >> 16) == dev + 1) return c0 & 0xffff;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaFuncSetAttribute(attention_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Shape<DP>::smem) != cudaSuccess)
+                           Shape<DP, false>::smem) != cudaSuccess)
     return 0;
   sms = sms < kMaxCtas ? sms : kMaxCtas;
   cached.store(((dev + 1) << 16) | sms, std::memory_order_relaxed);
@@ -1251,7 +1364,7 @@ template <typename T, int DP>
 int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   const int grid = grid_size<T, DP>();
   if (grid <= 0) return SV_ERR_CUDA;
-  attention_kernel<T, DP><<<grid, kThreads, Shape<DP>::smem, stream>>>(m, P);
+  attention_kernel<T, DP><<<grid, kThreads, Shape<DP, false>::smem, stream>>>(m, P);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   // The launch itself overlaps the attention kernel, whose end the CTAs wait
   // for.  Four warps a row where all rows are at most four waves of CTAs.
@@ -1329,6 +1442,7 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   P.prefix_table = prefix_table;
   P.prefix_len = prefix_len;
   P.prefix_tiles = (prefix_len + kTile - 1) / kTile;
+  P.pair_tiles = (prefix_len + kPairTile - 1) / kPairTile;
   if (prefix_len > 0) {
     const int blocks = (P.T + P.tpq - 1) / P.tpq;
     P.pairs = blocks / 2;
