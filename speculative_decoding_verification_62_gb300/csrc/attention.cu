@@ -64,7 +64,7 @@ constexpr int kSlots = 4 * kMaxCtas;  // parts: two a stream
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
 constexpr int kControl = 3072;  // barriers and small tables behind the tiles
 // Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs.
-constexpr int kCostA = 18, kCostB = 9;
+constexpr int kCostA = 30, kCostB = 9;
 
 template <int DP, bool PAIR>
 struct Shape {
@@ -238,6 +238,17 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
       : SV_R8(v, 0), SV_R8(v, 8), SV_R8(v, 16), SV_R8(v, 24)
       : "r"(addr));
 }
+// The same, and the largest of them (NaN left out)
+__device__ __forceinline__ float tmem_load32_max(uint32_t addr, uint32_t* v) {
+  float m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : SV_R8(v, 0), SV_R8(v, 8), SV_R8(v, 16), SV_R8(v, 24), "=f"(m)
+      : "r"(addr));
+  return m;
+}
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -272,6 +283,7 @@ __device__ __forceinline__ void tmem_loaded32(uint32_t* v) {
 __device__ __forceinline__ void tmem_wait_store() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_loaded(float& m) { asm volatile("" : "+f"(m)); }
 __device__ __forceinline__ void tmem_loaded16(uint32_t* v) {
   asm volatile("" : SV_T8(v, 0), SV_T8(v, 8));
 }
@@ -699,12 +711,14 @@ __device__ __forceinline__ void hide(uint32_t* v, uint32_t see) {
   for (int x = 0; x < 32; ++x)
     if (!((see >> x) & 1u)) v[x] = __float_as_uint(-INFINITY);
 }
-__device__ __forceinline__ void max32(const uint32_t* v, float& a, float& b) {
+__device__ __forceinline__ float max32(const uint32_t* v) {
+  float a = -INFINITY, b = -INFINITY;
 #pragma unroll
   for (int x = 0; x < 32; x += 4) {
     a = max3(a, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
     b = max3(b, __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
   }
+  return fmaxf(a, b);
 }
 // Weights of 32 scores: 2^(scale s - m), packed into v[0 .. 15], and their sums.
 template <typename T>
@@ -793,61 +807,57 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       const bool masked = key0 + S::keys > free;
       uint64_t sum0 = 0, sum1 = 0;  // two pairs of zeros
       if (PAIR) {
-        // S is read twice, 32 columns at a time, the next ones on their way: for
-        // the maximum, then for the weights (128 values held at once spill)
-        uint32_t v[2][32];
+        uint32_t v[kPairTile];
+        uint64_t sub = 0;
         if (active) {
           fence_after();
-          float mx0 = ninf, mx1 = ninf;
-          tmem_load32(s_col, v[0]);
+          float mx[4];
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) mx[ch] = tmem_load32_max(s_col + 32 * ch, v + 32 * ch);
+          tmem_wait_load();
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
-            tmem_wait_load();
-            tmem_loaded32(v[ch & 1]);
-            tmem_load32(s_col + ((ch + 1) & 3) * 32, v[(ch + 1) & 1]);
-            if (masked) hide(v[ch & 1], seen(key0 + 32 * ch, limit, by_word, word, p.kv));
-            max32(v[ch & 1], mx0, mx1);
+            tmem_loaded32(v + 32 * ch);
+            tmem_loaded(mx[ch]);
           }
-          settle(i, fmaxf(mx0, mx1) * P.sl2);
-        }
-        const float neg = m == ninf ? 0.f : -m;
-        const uint64_t sub = pair(neg, neg);
+          if (masked) {
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          if (active) {
-            uint32_t w16[16];
-            tmem_wait_load();
-            tmem_loaded32(v[ch & 1]);
-            if (ch < 3) tmem_load32(s_col + (ch + 1) * 32, v[(ch + 1) & 1]);
-            if (masked) hide(v[ch & 1], seen(key0 + 32 * ch, limit, by_word, word, p.kv));
-            weights32<T>(v[ch & 1], w16, sl2, sub, sum0, sum1);
-            tmem_store16(s_col + ch * 16, w16);  // over columns of S that are read already
-          }
-          if (ch & 1) {
-            if (active) {
-              tmem_wait_store();
-              fence_before();
+            for (int ch = 0; ch < 4; ++ch) {
+              hide(v + 32 * ch, seen(key0 + 32 * ch, limit, by_word, word, p.kv));
+              mx[ch] = max32(v + 32 * ch);
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][ch >> 1]));
           }
+          settle(i, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * P.sl2);
+          const float neg = m == ninf ? 0.f : -m;
+          sub = pair(neg, neg);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (active) {
+            weights32<T>(v + 64 * x, v + 32 * x, sl2, sub, sum0, sum1);
+            weights32<T>(v + 64 * x + 32, v + 32 * x + 16, sl2, sub, sum0, sum1);
+            tmem_store32(s_col + 32 * x, v + 32 * x);
+            tmem_wait_store();
+            fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][x]));
         }
       } else {
         if (active) {
           fence_after();
           uint32_t v[kTile];
-          tmem_load32(s_col, v);
-          tmem_load32(s_col + 32, v + 32);
+          float mx0 = tmem_load32_max(s_col, v), mx1 = tmem_load32_max(s_col + 32, v + 32);
           tmem_wait_load();
           tmem_loaded32(v);
           tmem_loaded32(v + 32);
+          tmem_loaded(mx0);
+          tmem_loaded(mx1);
           if (masked) {
             hide(v, seen(key0, limit, by_word, word, p.kv));
             hide(v + 32, seen(key0 + 32, limit, by_word, word, p.kv));
+            mx0 = max32(v), mx1 = max32(v + 32);
           }
-          float mx0 = ninf, mx1 = ninf;
-          max32(v, mx0, mx1);
-          max32(v + 32, mx0, mx1);
           settle(i, fmaxf(mx0, mx1) * P.sl2);
           if (!ok) break;
           const float neg = m == ninf ? 0.f : -m;
