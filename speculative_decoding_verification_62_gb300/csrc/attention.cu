@@ -614,7 +614,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
 // Products of one stream, by one thread.  (All 512 columns are allocated, so they start at 0.)
 template <typename T, int DP, bool PAIR>
 __device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t q_smem,
-                                            uint32_t ring, unsigned char* ring_ptr) {
+                                            uint32_t ring) {
   using S = Shape<DP, PAIR>;
   if (!elect_one()) return;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return bar_wait(smem_addr(bar), parity, P.wait_ns, &c->abort); };
@@ -654,18 +654,6 @@ __device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control
       keys = keys < S::keys ? keys : S::keys;
       const int steps = (keys + 15) / 16;
       if (!(ok = wait(&c->kv_full[slot], turn_of(e)))) break;
-      if (keys & 15) {
-        // rows behind the last key of the last 16: what memory held there
-        // (weights of 0 times NaN would be NaN).  In A both streams' warps
-        // write the same zeros.
-#pragma unroll 1
-        for (int x = 0; x < (steps * 16 - keys) * S::halves * 8; ++x) {
-          const int row = keys + x / (S::halves * 8), in = x % (S::halves * 8);
-          *reinterpret_cast<uint4*>(ring_ptr + slot * S::tile_bytes + (in / 8) * S::half_bytes + row * 128 +
-                                    (in % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
       const uint32_t d = cols + 2 * kTile;
       const uint64_t v = mat_desc(ring + slot * S::tile_bytes, S::half_bytes);
 #pragma unroll
@@ -738,7 +726,8 @@ __device__ __forceinline__ void weights32(const uint32_t* v, uint32_t* out, uint
 }
 
 template <typename T, int DP, bool PAIR>
-__device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t part_base) {
+__device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Control* c, int s, uint32_t part_base,
+                                             unsigned char* ring) {
   const int row = threadIdx.x & 127, lane = row & 31;
   const uint32_t lanes = (uint32_t)(row & ~31) << 16;  // this warp's tensor-memory lanes
   const uint32_t s_cols = lanes + s * 256, o_col = s_cols + 2 * kTile;
@@ -797,6 +786,22 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       l *= f;
       if (grow) m = top;
     };
+    // The value rows behind the last key of its 16 hold what memory held there, and
+    // weights of 0 times NaN would be NaN: this warpgroup clears them before it
+    // hands P over.  (In A both streams' write the same zeros.)
+    auto clear_tail = [&](int i, int keys) {
+      const unsigned int e = base + v_entry(i, n);
+      const uint32_t slot = slot_of<PAIR>(s, e);
+      if (!(ok = warp_wait(&c->kv_full[slot], turn_of(e), P, c))) return;
+      constexpr int kRow = S::halves * 8;  // 16-byte words of a row
+#pragma unroll 1
+      for (int x = row; x < ((keys + 15) / 16 * 16 - keys) * kRow; x += 128) {
+        const int r = keys + x / kRow, in = x % kRow;
+        *reinterpret_cast<uint4*>(ring + slot * S::tile_bytes + (in / 8) * S::half_bytes + r * 128 + (in % 8) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    };
     const uint64_t sl2 = pair(P.sl2, P.sl2);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++tiles) {
@@ -805,6 +810,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       if (threadIdx.x % 128 == 0) bar_arrive(smem_addr(&c->kv_empty[slot_of<PAIR>(s, base + k_entry(i))]));
       const int key0 = (p.t0 + i) * S::keys;
       const bool masked = key0 + S::keys > free;
+      const int keys = p.keys - key0;
+      const bool tail = keys < S::keys && (keys & 15);
       uint64_t sum0 = 0, sum1 = 0;  // two pairs of zeros
       if (PAIR) {
         uint32_t v[kPairTile];
@@ -831,6 +838,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           const float neg = m == ninf ? 0.f : -m;
           sub = pair(neg, neg);
         }
+        if (tail) clear_tail(i, keys);
+        if (!ok) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (active) {
@@ -868,6 +877,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           tmem_wait_store();
           fence_before();
         }
+        if (tail) clear_tail(i, keys);
+        if (!ok) break;
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][buf]));
       }
@@ -952,11 +963,11 @@ __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsig
   const uint32_t q_smem = smem_addr(tiles), ring = q_smem + 2 * S::q_bytes;
   const Walk w = c->start[s];
   if (warp < 8)
-    softmax_role<T, DP, PAIR>(P, w, c, s, 4 * blockIdx.x + (PAIR ? s : 2 * s));
+    softmax_role<T, DP, PAIR>(P, w, c, s, 4 * blockIdx.x + (PAIR ? s : 2 * s), tiles + 2 * S::q_bytes);
   else if (!(warp & 1))
     copy_role<DP, PAIR>(P, w, c, s, q_smem, ring, qmap, kmap, vmap);
   else
-    matrix_role<T, DP, PAIR>(P, w, c, s, q_smem, ring, tiles + 2 * S::q_bytes);
+    matrix_role<T, DP, PAIR>(P, w, c, s, q_smem, ring);
   fence_before();
   __syncthreads();
   if (c->abort) {
