@@ -8,7 +8,9 @@ cannot be loaded or built, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import threading
 
 import torch
@@ -331,47 +333,76 @@ def spec_verify_greedy(target_logits, draft_tokens, gamma, out_tokens, num_accep
         raise SpecVerifyError(rc)
 
 
-def _one_device(**tensors):
-    """The CUDA device that holds every given tensor (None: an argument left out)."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
-    return dev
+# The calls below check their tensors with few Python steps: a small batch's kernel
+# takes 4 to 10 us, less than a careless wrapper.
+def _arg(t, name, dtype, shape, index):
+    """Address of a contiguous tensor of that dtype and shape (None: any) on CUDA device `index`."""
+    if isinstance(t, torch.Tensor):
+        if (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+        _dev(t, name, dtype, shape)  # raises what it finds wrong
+        raise ValueError(f"{name} is on {t.device}, other arguments on cuda:{index}")
+    raise TypeError(f"{name} must be a CUDA tensor")
 
 
-def _probs_draft(draft_probs, dtype, shape):
-    if draft_probs is None:
-        return None
-    return _dev(draft_probs, "draft_probs", dtype, shape)
+def _index(t, name):
+    """CUDA device index of the tensor that the others go by."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _on(index):
+    """Makes `index` the current device for a launch; nothing to do in the usual case."""
+    if torch.cuda.current_device() == index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(index)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1 us less than the public way
+
+
+def _stream_of(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _two(a, b):
+    return (ctypes.c_int64 * 2)(a, b)
+
+
+def _probs_args(target_probs, draft_probs, draft_shape, index):
+    """Addresses and type code of the rows."""
+    code = _dtype_code(target_probs)
+    tp = _arg(target_probs, "target_probs", target_probs.dtype, None, index)
+    dp = None
+    if draft_probs is not None:
+        dp = _arg(draft_probs, "draft_probs", target_probs.dtype, draft_shape, index)
+    return tp, dp, code
 
 
 def spec_verify_sample_probs(target_probs, draft_probs, draft_tokens, gamma, uniforms, out_tokens,
                              num_accepted, workspace, stream=None) -> None:
     """Sampling verify step on probabilities instead of logits; draft_probs None: the
     drafts were certain (looked up).  See include/spec_verify.h."""
-    dev = _one_device(target_probs=target_probs, draft_probs=draft_probs,
-                      draft_tokens=draft_tokens, gamma=gamma, uniforms=uniforms,
-                      out_tokens=out_tokens, num_accepted=num_accepted, workspace=workspace)
+    lib = _lib or load_library()
+    index = _index(target_probs, "target_probs")
     B, G1, V = target_probs.shape
     G = G1 - 1
-    code = _dtype_code(target_probs)
-    with torch.cuda.device(dev):
-        rc = load_library().spec_verify_sample_probs(
-            _dev(target_probs, "target_probs"),
-            _probs_draft(draft_probs, target_probs.dtype, (B, G, V)), code, B, G, V,
-            _dev(draft_tokens, "draft_tokens", torch.int32, (B, G)),
-            _dev(gamma, "gamma", torch.int32, (B,)),
-            _dev(uniforms, "uniforms", torch.float32, (B, G + 1)),
-            _dev(out_tokens, "out_tokens", torch.int32, (B, G + 1)),
-            _dev(num_accepted, "num_accepted", torch.int32, (B,)),
-            _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    tp, dp, code = _probs_args(target_probs, draft_probs, (B, G, V), index)
+    i32 = torch.int32
+    with _on(index):
+        rc = lib.spec_verify_sample_probs(
+            tp, dp, code, B, G, V, _arg(draft_tokens, "draft_tokens", i32, (B, G), index),
+            _arg(gamma, "gamma", i32, (B,), index),
+            _arg(uniforms, "uniforms", torch.float32, (B, G1), index),
+            _arg(out_tokens, "out_tokens", i32, (B, G1), index),
+            _arg(num_accepted, "num_accepted", i32, (B,), index),
+            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel(),
+            _stream_of(stream, index))
     if rc != 0:
         raise SpecVerifyError(rc)
 
@@ -379,26 +410,25 @@ def spec_verify_sample_probs(target_probs, draft_probs, draft_tokens, gamma, uni
 def spec_verify_sample_probs_packed(target_probs, draft_probs, cu_draft, draft_tokens, uniforms,
                                     out_tokens, num_accepted, workspace, stream=None) -> None:
     """spec_verify_sample_probs on the packed layout; see include/spec_verify.h."""
-    dev = _one_device(target_probs=target_probs, draft_probs=draft_probs, cu_draft=cu_draft,
-                      draft_tokens=draft_tokens, uniforms=uniforms, out_tokens=out_tokens,
-                      num_accepted=num_accepted, workspace=workspace)
+    lib = _lib or load_library()
+    index = _index(target_probs, "target_probs")
     B = cu_draft.numel() - 1
     total = draft_tokens.numel()
-    V = target_probs.shape[1]
+    rows, V = target_probs.shape
     G = out_tokens.shape[1] - 1
-    if target_probs.shape[0] != total + B:
+    if rows != total + B:
         raise ValueError("target_probs must have total_drafts + B rows")
-    code = _dtype_code(target_probs)
-    with torch.cuda.device(dev):
-        rc = load_library().spec_verify_sample_probs_packed(
-            _dev(target_probs, "target_probs"),
-            _probs_draft(draft_probs, target_probs.dtype, (total, V)), code, B, G, V,
-            _dev(cu_draft, "cu_draft", torch.int32, (B + 1,)), total,
-            _dev(draft_tokens, "draft_tokens", torch.int32, (total,)),
-            _dev(uniforms, "uniforms", torch.float32, (total + B,)),
-            _dev(out_tokens, "out_tokens", torch.int32, (B, G + 1)),
-            _dev(num_accepted, "num_accepted", torch.int32, (B,)),
-            _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    tp, dp, code = _probs_args(target_probs, draft_probs, (total, V), index)
+    i32 = torch.int32
+    with _on(index):
+        rc = lib.spec_verify_sample_probs_packed(
+            tp, dp, code, B, G, V, _arg(cu_draft, "cu_draft", i32, (B + 1,), index), total,
+            _arg(draft_tokens, "draft_tokens", i32, (total,), index),
+            _arg(uniforms, "uniforms", torch.float32, (rows,), index),
+            _arg(out_tokens, "out_tokens", i32, (B, G + 1), index),
+            _arg(num_accepted, "num_accepted", i32, (B,), index),
+            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel(),
+            _stream_of(stream, index))
     if rc != 0:
         raise SpecVerifyError(rc)
 
@@ -415,8 +445,10 @@ class PagedCache:
     """
 
     def __init__(self, k_pages, v_pages, page_table, kv_len):
-        self.device = _one_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table,
-                                  kv_len=kv_len)
+        self.index = _index(k_pages, "k_pages")
+        for name, t in (("v_pages", v_pages), ("page_table", page_table), ("kv_len", kv_len)):
+            if _index(t, name) != self.index:
+                raise ValueError(f"{name} is on {t.device}, k_pages on {k_pages.device}")
         if k_pages.dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"k_pages must be bfloat16 or float16, got {k_pages.dtype}")
         if v_pages.dtype != k_pages.dtype:
@@ -455,6 +487,7 @@ class PagedCache:
             SV_BF16 if k_pages.dtype == torch.bfloat16 else SV_F16, n, page, heads, dim,
             (ctypes.c_int64 * 3)(*k_pages.stride()[:3]), (ctypes.c_int64 * 3)(*v_pages.stride()[:3]),
             ptr(page_table), width, B, ptr(kv_len))
+        self.ref = ctypes.byref(self.struct)
 
     def commit(self, num_accepted) -> None:
         """After a verification: every request keeps its last token and its accepted
@@ -476,20 +509,25 @@ def make_attention_workspace(total_rows: int, q_heads: int, head_dim: int,
 
 
 def _heads(t, name, cache, rows, heads):
-    """Pointer and (row, head) strides of a [rows, heads, head_dim] view."""
+    """Address and (row, head) strides of a [rows, heads, head_dim] view."""
+    if (isinstance(t, torch.Tensor) and t.dtype is cache.dtype and t.get_device() == cache.index
+            and t.shape == (rows, heads, cache.head_dim)):
+        row, head, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), _two(row, head)
+    if _index(t, name) != cache.index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.index}")
     if t.dtype != cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
     if tuple(t.shape) != (rows, heads, cache.head_dim):
         raise ValueError(f"{name} must have shape {(rows, heads, cache.head_dim)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1:
-        raise ValueError(f"{name} must have contiguous heads")
-    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 2)(t.stride(0), t.stride(1))
+    raise ValueError(f"{name} must have contiguous heads")
 
 
 def _cu_rows(cu_draft, cache, rows):
     if rows < cache.batch:
         raise ValueError(f"a step of {cache.batch} requests has at least as many rows, got {rows}")
-    return _dev(cu_draft, "cu_draft", torch.int32, (cache.batch + 1,)), rows - cache.batch
+    return _arg(cu_draft, "cu_draft", torch.int32, (cache.batch + 1,), cache.index)
 
 
 def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, workspace,
@@ -498,32 +536,34 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     """Append a step's keys and values to the paged cache and rotate its queries and keys;
     q and q_out may be None, freq (rope.fixed_point) None for no rotation.  See
     include/spec_verify.h."""
-    dev = _one_device(k_pages=cache.k_pages, q=q, k=k, v=v, cu_draft=cu_draft, freq=freq,
-                      q_out=q_out, workspace=workspace, positions=positions)
+    lib = _lib or load_library()
+    index = cache.index
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
+    _index(k, "k")
     rows = k.shape[0]
-    cu, total = _cu_rows(cu_draft, cache, rows)
+    cu = _cu_rows(cu_draft, cache, rows)
     kp, ks = _heads(k, "k", cache, rows, cache.kv_heads)
     vp, vs = _heads(v, "v", cache, rows, cache.kv_heads)
     heads, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
+        _index(q, "q")
         heads = q.shape[1]
         qp, qs = _heads(q, "q", cache, rows, heads)
         op, os_ = _heads(q_out, "q_out", cache, rows, heads)
-        if (rows > 1 and q_out.stride(0) < cache.head_dim) or (heads > 1 and q_out.stride(1) < cache.head_dim):
+        if (rows > 1 and os_[0] < cache.head_dim) or (heads > 1 and os_[1] < cache.head_dim):
             raise ValueError("q_out overlaps itself")
-    rot = 0
+    rot, fp = 0, None
     if freq is not None:
-        rot = 2 * freq.numel()
-        _dev(freq, "freq", torch.int64, (rot // 2,))
-    with torch.cuda.device(dev):
-        rc = load_library().spec_verify_kv_append(
-            qp, qs, heads, kp, ks, vp, vs, op, os_, ctypes.byref(cache.struct), cu, total,
-            int(max_drafts), None if freq is None else _dev(freq, "freq"), rot, int(bool(interleaved)),
-            float(rope_scale), _dev(positions, "positions", torch.int32, (rows,)),
-            int(position_offset), _dev(workspace, "workspace", torch.uint8), workspace.numel(),
-            _stream(stream))
+        half = freq.numel()
+        rot, fp = 2 * half, _arg(freq, "freq", torch.int64, (half,), index)
+    with _on(index):
+        rc = lib.spec_verify_kv_append(
+            qp, qs, heads, kp, ks, vp, vs, op, os_, cache.ref, cu, rows - cache.batch, max_drafts, fp,
+            rot, 1 if interleaved else 0, rope_scale,
+            None if positions is None else _arg(positions, "positions", torch.int32, (rows,), index),
+            position_offset, _arg(workspace, "workspace", torch.uint8, None, index),
+            workspace.numel(), _stream_of(stream, index))
     if rc != 0:
         raise SpecVerifyError(rc)
 
@@ -532,29 +572,29 @@ def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix
                           prefix_len=0, scale=None, draft_mask=None, lse=None, stream=None) -> None:
     """Attention of a step's rows over the paged cache (and a prefix that the batch shares);
     scale None: head_dim ** -0.5.  See include/spec_verify.h."""
-    dev = _one_device(k_pages=cache.k_pages, q=q, cu_draft=cu_draft, out=out, workspace=workspace,
-                      prefix_table=prefix_table, draft_mask=draft_mask, lse=lse)
+    lib = _lib or load_library()
+    index = cache.index
+    _index(q, "q")
     rows, heads = q.shape[0], q.shape[1]
-    cu, total = _cu_rows(cu_draft, cache, rows)
+    cu = _cu_rows(cu_draft, cache, rows)
     qp, qs = _heads(q, "q", cache, rows, heads)
-    prefix_len = int(prefix_len)
-    pages = -(-prefix_len // cache.page_size)
+    pt = mask = None
     if prefix_len > 0:
-        if prefix_table is None or prefix_table.numel() < pages:
-            raise ValueError(f"prefix_table must hold {pages} pages")
-        pt = _dev(prefix_table, "prefix_table", torch.int32)
-    else:
-        pt = None
-    if draft_mask is not None and draft_mask.dtype not in (torch.int32, torch.uint32):
-        raise TypeError("draft_mask must be int32 or uint32 words")
-    scale = cache.head_dim ** -0.5 if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        rc = load_library().spec_verify_attention(
-            qp, qs, heads, ctypes.byref(cache.struct), pt, prefix_len, cu, total, int(max_drafts),
-            scale, _dev(draft_mask, "draft_mask", None, (rows,)),
-            _dev(out, "out", q.dtype, (rows, heads, cache.head_dim)),
-            _dev(lse, "lse", torch.float32, (rows, heads)),
-            _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+        if prefix_table is None or prefix_table.numel() * cache.page_size < prefix_len:
+            raise ValueError(f"prefix_table must hold {-(-prefix_len // cache.page_size)} pages")
+        pt = _arg(prefix_table, "prefix_table", torch.int32, None, index)
+    if draft_mask is not None:
+        if draft_mask.dtype not in (torch.int32, torch.uint32):
+            raise TypeError("draft_mask must be int32 or uint32 words")
+        mask = _arg(draft_mask, "draft_mask", draft_mask.dtype, (rows,), index)
+    with _on(index):
+        rc = lib.spec_verify_attention(
+            qp, qs, heads, cache.ref, pt, prefix_len, cu, rows - cache.batch, max_drafts,
+            cache.head_dim ** -0.5 if scale is None else scale, mask,
+            _arg(out, "out", cache.dtype, (rows, heads, cache.head_dim), index),
+            None if lse is None else _arg(lse, "lse", torch.float32, (rows, heads), index),
+            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel(),
+            _stream_of(stream, index))
     if rc != 0:
         raise SpecVerifyError(rc)
 

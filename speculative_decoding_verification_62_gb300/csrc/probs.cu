@@ -7,13 +7,13 @@
 // by the inverse CDF: the smallest j with w_0 + .. + w_j > u w_total.
 //
 // The test is exact: u q is a product of two 24-bit numbers, formed in double.
-// The draw is exact up to the weights' grain: p and q are rounded to whole
-// multiples of 2^-56 (a float of 2^-32 or more is one already) and summed as
-// 64-bit integers, so no sum depends on an order, and u w_total is compared
-// after a 128-bit product.  A rounding moves a CDF boundary by at most
-// V 2^-57, so a uniform of 24 bits lands on the other side of one with a
-// chance below V^2 2^-57 (2^-23 at V = 128256 if every rounding went one way).
-// Sums saturate at 2^63 = 128 (a row that sums to about 1 stays far below).
+// The draw is exact up to the weights' grain: p and q are cut to whole multiples
+// of 2^-54 (a float of 2^-31 or more is one already) and summed as 64-bit
+// integers, so no sum depends on an order, and u w_total is compared after a
+// 128-bit product.  Cutting moves a CDF boundary by at most n 2^-54, n the
+// entries below 2^-31, so that a uniform lands on the other side of a boundary
+// with a chance below V n 2^-54 (2^-25 at V = 128256 with 4 % such entries).
+// Sums saturate at 2^63 = 512 (a row that sums to about 1 stays far below).
 //
 // Bound: the one or two rows that the draw needs are read once from HBM; all
 // other reads are gathers.  A cluster of C CTAs shares a request, each warp a
@@ -55,19 +55,41 @@ __device__ __forceinline__ float load_one(const char* row, size_t i) {
   return __uint_as_float((unsigned int)__ldg(reinterpret_cast<const unsigned short*>(row) + i) << 16);
 }
 
-// A probability as a whole multiple of 2^-56; what is none counts as 0, what
-// is above 1 as 1, and both are flagged.
-__device__ __forceinline__ unsigned long long fix(float p, unsigned int& flags) {
-  if (!(p >= 0.f && p <= 1.f)) {
-    flags |= SV_STATUS_BAD_PROB;
-    p = p > 1.f ? 1.f : 0.f;
-  }
-  return __float2ull_rn(p * 0x1p56f);
+// A probability's bits; what is none counts as 0, what is above 1 as 1, and both
+// are flagged (-0 is 0).
+__device__ __forceinline__ unsigned int clean(unsigned int bits, unsigned int& flags) {
+  if (bits <= 0x3f800000u) return bits;
+  if (bits == 0x80000000u) return 0u;
+  flags |= SV_STATUS_BAD_PROB;
+  return bits <= 0x7f800000u ? 0x3f800000u : 0u;
 }
 
-__device__ __forceinline__ unsigned long long weight(float p, float q, unsigned int& flags) {
-  const unsigned long long a = fix(p, flags), b = fix(q, flags);
-  return a > b ? a - b : 0ull;
+// Shifts by any amount; 32 and more (a negative amount among them) give 0.
+__device__ __forceinline__ unsigned int shl(unsigned int v, int n) {
+  unsigned int r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
+  return r;
+}
+__device__ __forceinline__ unsigned int shr(unsigned int v, int n) {
+  unsigned int r;
+  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
+  return r;
+}
+// A probability in units of 2^-54 is m 2^(e - 96) with its 24-bit significand m and
+// exponent field e: `high` += that where e >= 96 (a multiplication by a power of
+// two, one multiply-add into 64 bits), `low` += its whole part below (under 2^23;
+// the conversion instructions would take 8 times as long).
+__device__ __forceinline__ void add_fixed(unsigned int bits, unsigned long long& high, unsigned int& low) {
+  const int e = (int)(bits >> 23);
+  const unsigned int m = (bits & 0x7fffffu) | 0x800000u;
+  high += (unsigned long long)m * shl(1u, e - 96);
+  low += shr(m >> 1, 95 - e);
+}
+__device__ __forceinline__ unsigned long long fixed(unsigned int bits) {
+  unsigned long long high = 0;
+  unsigned int low = 0;
+  add_fixed(bits, high, low);
+  return high + low;
 }
 
 // floor(u S) for a float u in [0, 1): u = m 2^-s with a 24-bit m.
@@ -109,17 +131,49 @@ struct Draw {
 };
 
 template <int EB>
-__device__ __forceinline__ unsigned long long weight_at(const Draw& d, int i, unsigned int& flags) {
+__device__ __forceinline__ unsigned long long weight_at(const Draw& d, int i) {
+  unsigned int ignored = 0;
   if (i == d.skip) return 0;
-  const float p = load_one<EB>(d.p, i);
-  return weight(p, d.q ? load_one<EB>(d.q, i) : 0.f, flags);
+  const unsigned long long p = fixed(clean(__float_as_uint(load_one<EB>(d.p, i)), ignored));
+  if (!d.q) return p;
+  const unsigned long long q = fixed(clean(__float_as_uint(load_one<EB>(d.q, i)), ignored));
+  return p > q ? p - q : 0ull;
 }
 
 template <int EB>
-__device__ __forceinline__ float word_elem(const uint4& v, int j) {
+__device__ __forceinline__ unsigned int word_bits(const uint4& v, int j) {
   const unsigned int w = j * EB / 4 == 0 ? v.x : j * EB / 4 == 1 ? v.y : j * EB / 4 == 2 ? v.z : v.w;
-  if (EB == 4) return __uint_as_float(w);
-  return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+  if (EB == 4) return w;
+  return j & 1 ? w & 0xffff0000u : w << 16;
+}
+
+// The weights of N (at most 64) pairs, summed: at most N 2^54.
+template <int N, bool TWO>
+__device__ __forceinline__ unsigned long long batch_sum(unsigned int (&p)[N], unsigned int (&q)[N],
+                                                        unsigned int& flags) {
+  unsigned int top = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) top = max(top, TWO ? max(p[j], q[j]) : p[j]);
+  if (top > 0x3f800000u) {  // something that is no probability, or -0
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      p[j] = clean(p[j], flags);
+      if (TWO) q[j] = clean(q[j], flags);
+    }
+  }
+  unsigned long long hp = 0, hq = 0;
+  unsigned int lp = 0, lq = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (TWO) {
+      const bool more = p[j] > q[j];  // as floats: both are at least 0
+      add_fixed(more ? p[j] : 0u, hp, lp);
+      add_fixed(more ? q[j] : 0u, hq, lq);
+    } else {
+      add_fixed(p[j], hp, lp);
+    }
+  }
+  return hp + lp - hq - lq;
 }
 
 // The sum of one warp's units [u0, u1): a unit is 32 x 16 bytes of the row.
@@ -135,6 +189,7 @@ __device__ __forceinline__ unsigned long long range_sum(const Draw& d, int V, in
     const uint4* p = reinterpret_cast<const uint4*>(d.p);
     const uint4* q = reinterpret_cast<const uint4*>(d.q);
     const int words = V / E;
+#pragma unroll 1
     for (int u = u0; u < u1; u += kUnroll) {
       uint4 a[kUnroll], b[kUnroll];
 #pragma unroll
@@ -146,34 +201,30 @@ __device__ __forceinline__ unsigned long long range_sum(const Draw& d, int V, in
       }
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
-        unsigned long long s = 0;
-        const int e0 = ((u + r) * 32 + lane) * E;
+        unsigned int x[E], y[E];
+        const int skip = d.skip - ((u + r) * 32 + lane) * E;
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-          const unsigned long long w =
-              weight(word_elem<EB>(a[r], j), TWO ? word_elem<EB>(b[r], j) : 0.f, flags);
-          s += (!TWO && e0 + j == d.skip) ? 0ull : w;
+          x[j] = word_bits<EB>(a[r], j);
+          y[j] = TWO ? word_bits<EB>(b[r], j) : 0u;
+          if (!TWO && j == skip) x[j] = 0u;
         }
-        acc = sat_add(acc, s);
+        acc = sat_add(acc, batch_sum<E, TWO>(x, y, flags));
       }
     }
   } else {
-    for (int u = u0; u < u1; ++u) {
-      unsigned long long s = 0;
-      float a[E], b[E];
+    constexpr int N = 2 * E;
+#pragma unroll 1
+    for (int u = u0; u < u1; u += 2) {
+      unsigned int x[N], y[N];
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
+      for (int j = 0; j < N; ++j) {
         const int i = (u * E + j) * 32 + lane;
-        a[j] = i < V ? load_one<EB>(d.p, i) : 0.f;
-        b[j] = TWO && i < V ? load_one<EB>(d.q, i) : 0.f;
+        const bool in = u + j / E < u1 && i < V && i != d.skip;
+        x[j] = in ? __float_as_uint(load_one<EB>(d.p, i)) : 0u;
+        y[j] = TWO && in ? __float_as_uint(load_one<EB>(d.q, i)) : 0u;
       }
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int i = (u * E + j) * 32 + lane;
-        const unsigned long long w = weight(a[j], b[j], flags);
-        s += (!TWO && i == d.skip) ? 0ull : w;
-      }
-      acc = sat_add(acc, s);
+      acc = sat_add(acc, batch_sum<N, TWO>(x, y, flags));
     }
   }
 #pragma unroll
@@ -224,14 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
       float p = load_one<EB>(P.target, (trow + lane) * V + x);
       float q = P.draft ? load_one<EB>(P.draft, (drow + lane) * V + x) : 1.f;
       float u = P.uniforms[trow + lane];
-      if (!(p >= 0.f && p <= 1.f)) {
-        flags |= SV_STATUS_BAD_PROB;
-        p = p > 1.f ? 1.f : 0.f;
-      }
-      if (!(q >= 0.f && q <= 1.f)) {
-        flags |= SV_STATUS_BAD_PROB;
-        q = q > 1.f ? 1.f : 0.f;
-      }
+      p = __uint_as_float(clean(__float_as_uint(p), flags));
+      q = __uint_as_float(clean(__float_as_uint(q), flags));
       if (!(u >= 0.f && u < 1.f)) {
         flags |= SV_STATUS_BAD_UNIFORM;
         u = 0.f;
@@ -323,9 +368,8 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
     if (e1 > V) e1 = V;
     const int per = (e1 - e0 + kThreads - 1) / kThreads;
     const int i0 = e0 + tid * per, i1 = i0 + per < e1 ? i0 + per : e1;
-    unsigned int ignored = 0;
     unsigned long long mine = 0;
-    for (int i = i0; i < i1; ++i) mine = sat_add(mine, weight_at<EB>(d, i, ignored));
+    for (int i = i0; i < i1; ++i) mine = sat_add(mine, weight_at<EB>(d, i));
     unsigned long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -340,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
     if (goal >= from && goal < sat_add(from, mine)) {
       unsigned long long at = from;
       for (int i = i0; i < i1; ++i) {
-        at = sat_add(at, weight_at<EB>(d, i, ignored));
+        at = sat_add(at, weight_at<EB>(d, i));
         if (goal < at) {
           *drawn = i;
           break;
