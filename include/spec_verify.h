@@ -94,7 +94,7 @@ enum {
                                      request's outputs are incomplete and the workspace must
                                      be zero-filled again before reuse */
   SV_STATUS_BAD_PROB = 128u,      /* a probability outside [0, 1] or NaN: counted as 0 (above 1:
-                                     as 1); or a row that sums to 0, or to 512 or more */
+                                     as 1); or a row that sums to 0, or to 65536 or more */
   SV_STATUS_BAD_PAGE = 256u,      /* a page number outside the pool: not written, read as zeros */
   SV_STATUS_BAD_LENGTH = 512u     /* kv_len negative, or a step past the request's page table:
                                      that row or request is left out */
@@ -214,7 +214,7 @@ int spec_verify_draw(const void *logits, sv_dtype dtype, int B, int V, const flo
  * draw as in steps 2 and 3.  Rows need not sum to 1: a draw uses its weights'
  * own total.  Of a request, the calls read p and q at the drafts, row k of
  * target_probs and, after a rejection, row k of draft_probs.  The tests are
- * exact; the draw's weights are p and q cut to whole multiples of 2^-54, summed
+ * exact; the draw's weights are rounded to whole multiples of 2^-47, summed
  * exactly, and compared with u times the total exactly.  A residual whose
  * weights are all 0 draws from p_k; a row of zeros draws V - 1 and sets
  * SV_STATUS_BAD_PROB.  An entry that is no probability (negative, NaN, above 1)

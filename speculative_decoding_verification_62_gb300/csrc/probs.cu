@@ -7,13 +7,14 @@
 // by the inverse CDF: the smallest j with w_0 + .. + w_j > u w_total.
 //
 // The test is exact: u q is a product of two 24-bit numbers, formed in double.
-// The draw is exact up to the weights' grain: p and q are cut to whole multiples
-// of 2^-54 (a float of 2^-31 or more is one already) and summed as 64-bit
-// integers, so no sum depends on an order, and u w_total is compared after a
-// 128-bit product.  Cutting moves a CDF boundary by at most n 2^-54, n the
-// entries below 2^-31, so that a uniform lands on the other side of a boundary
-// with a chance below V n 2^-54 (2^-25 at V = 128256 with 4 % such entries).
-// Sums saturate at 2^63 = 512 (a row that sums to about 1 stays far below).
+// The draw is exact up to the weights' grain: each weight is a whole multiple of
+// 2^-47, found by additions alone (weight() below), and weights are summed as
+// integers, so that no sum depends on an order; u w_total is compared after a
+// 128-bit product.  Weights below 2^-22 are rounded (by at most 2^-47, and by
+// 2^-48 where p and q differ much), and the roundings of n entries move a boundary
+// by about 2^-48 sqrt(n): a uniform lands on the other side of one of V boundaries
+// with a chance of about V sqrt(V) 2^-48 (2^-23 at V = 128256, if all entries
+// were that small).  Sums saturate at 2^63 = 65536 (a row sums to about 1).
 //
 // Bound: the one or two rows that the draw needs are read once from HBM; all
 // other reads are gathers.  A cluster of C CTAs shares a request, each warp a
@@ -64,32 +65,71 @@ __device__ __forceinline__ unsigned int clean(unsigned int bits, unsigned int& f
   return bits <= 0x7f800000u ? 0x3f800000u : 0u;
 }
 
-// Shifts by any amount; 32 and more (a negative amount among them) give 0.
-__device__ __forceinline__ unsigned int shl(unsigned int v, int n) {
-  unsigned int r;
-  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
-  return r;
+// A weight in units of 2^-47 is hi 2^24 + 2 lo + le.  With d = p - q rounded and e
+// its exact error (q <= p, so that (p - d) - q is exact), adding 1 rounds d to a
+// multiple of 2^-23, which stands in the sum's low bits; what is left of d, at most
+// 2^-24, is rounded to a multiple of 2^-46 by adding 1.5 2^-23 in the same way, and
+// e, at most 2^-25, to one of 2^-47 by adding 1.5 2^-24.  Additions run at twice the
+// rate of integer instructions, and a conversion to 64-bit integers at an eighth.
+constexpr unsigned int kOne = 0x3f800000u;     // 1
+constexpr unsigned int kRest = 0x34400000u;    // 1.5 2^-23
+constexpr unsigned int kError = 0x33c00000u;   // 1.5 2^-24
+struct Parts {
+  unsigned int hi, lo, le;  // sums of the parts, with kOne, kRest and kError in each
+};
+
+// Two weights at a time.
+template <bool TWO>
+__device__ __forceinline__ void add_weights(unsigned int p0, unsigned int p1, unsigned int q0, unsigned int q1,
+                                            Parts& sum) {
+  auto pack = [](unsigned int a, unsigned int b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+  };
+  auto add = [](unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+  };
+  // a - b
+  auto sub = [&](unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(0xbf800000bf800000ull), "l"(a));
+    return r;
+  };
+  const unsigned long long one = 0x3f8000003f800000ull, minus_one = 0xbf800000bf800000ull,
+                           rest = 0x3440000034400000ull, error = 0x33c0000033c00000ull;
+  const unsigned long long p = pack(p0, p1);
+  unsigned long long d = p, e = 0;
+  if (TWO) {
+    const unsigned long long q = pack(min(p0, q0), min(p1, q1));  // as floats: none is negative
+    d = sub(p, q);
+    e = sub(sub(p, d), q);
+  }
+  const unsigned long long t = add(d, one);
+  const unsigned long long t2 = add(sub(d, add(t, minus_one)), rest);
+  unsigned int a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(t));
+  sum.hi += a + b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(t2));
+  sum.lo += a + b;
+  if (TWO) {
+    const unsigned long long t3 = add(e, error);
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(t3));
+    sum.le += a + b;
+  }
 }
-__device__ __forceinline__ unsigned int shr(unsigned int v, int n) {
-  unsigned int r;
-  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
-  return r;
+// The sum of n weights from their parts' sums (n at most 256: hi stays below 2^32)
+template <bool TWO>
+__device__ __forceinline__ unsigned long long joined(const Parts& s, unsigned int n) {
+  return ((unsigned long long)(s.hi - n * kOne) << 24) + 2 * (long long)(int)(s.lo - n * kRest) +
+         (TWO ? (long long)(int)(s.le - n * kError) : 0ll);
 }
-// A probability in units of 2^-54 is m 2^(e - 96) with its 24-bit significand m and
-// exponent field e: `high` += that where e >= 96 (a multiplication by a power of
-// two, one multiply-add into 64 bits), `low` += its whole part below (under 2^23;
-// the conversion instructions would take 8 times as long).
-__device__ __forceinline__ void add_fixed(unsigned int bits, unsigned long long& high, unsigned int& low) {
-  const int e = (int)(bits >> 23);
-  const unsigned int m = (bits & 0x7fffffu) | 0x800000u;
-  high += (unsigned long long)m * shl(1u, e - 96);
-  low += shr(m >> 1, 95 - e);
-}
-__device__ __forceinline__ unsigned long long fixed(unsigned int bits) {
-  unsigned long long high = 0;
-  unsigned int low = 0;
-  add_fixed(bits, high, low);
-  return high + low;
+__device__ __forceinline__ unsigned long long weight(unsigned int p, unsigned int q) {
+  Parts s{0u, 0u, 0u};
+  add_weights<true>(p, 0u, q, 0u, s);
+  return joined<true>(s, 2);
 }
 
 // floor(u S) for a float u in [0, 1): u = m 2^-s with a 24-bit m.
@@ -134,10 +174,8 @@ template <int EB>
 __device__ __forceinline__ unsigned long long weight_at(const Draw& d, int i) {
   unsigned int ignored = 0;
   if (i == d.skip) return 0;
-  const unsigned long long p = fixed(clean(__float_as_uint(load_one<EB>(d.p, i)), ignored));
-  if (!d.q) return p;
-  const unsigned long long q = fixed(clean(__float_as_uint(load_one<EB>(d.q, i)), ignored));
-  return p > q ? p - q : 0ull;
+  const unsigned int p = clean(__float_as_uint(load_one<EB>(d.p, i)), ignored);
+  return weight(p, d.q ? clean(__float_as_uint(load_one<EB>(d.q, i)), ignored) : 0u);
 }
 
 template <int EB>
@@ -147,33 +185,25 @@ __device__ __forceinline__ unsigned int word_bits(const uint4& v, int j) {
   return j & 1 ? w & 0xffff0000u : w << 16;
 }
 
-// The weights of N (at most 64) pairs, summed: at most N 2^54.
+// Adds the weights of N entries.
 template <int N, bool TWO>
-__device__ __forceinline__ unsigned long long batch_sum(unsigned int (&p)[N], unsigned int (&q)[N],
-                                                        unsigned int& flags) {
+__device__ __forceinline__ void add_batch(unsigned int (&p)[N], unsigned int (&q)[N], Parts& sum,
+                                          unsigned int& flags) {
   unsigned int top = 0;
 #pragma unroll
-  for (int j = 0; j < N; ++j) top = max(top, TWO ? max(p[j], q[j]) : p[j]);
-  if (top > 0x3f800000u) {  // something that is no probability, or -0
+  for (int j = 0; j < N; j += 2) {
+    top = __vimax3_u32(top, p[j], p[j + 1]);
+    if (TWO) top = __vimax3_u32(top, q[j], q[j + 1]);
+  }
+  if (top > kOne) {  // something that is no probability, or -0
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       p[j] = clean(p[j], flags);
       if (TWO) q[j] = clean(q[j], flags);
     }
   }
-  unsigned long long hp = 0, hq = 0;
-  unsigned int lp = 0, lq = 0;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    if (TWO) {
-      const bool more = p[j] > q[j];  // as floats: both are at least 0
-      add_fixed(more ? p[j] : 0u, hp, lp);
-      add_fixed(more ? q[j] : 0u, hq, lq);
-    } else {
-      add_fixed(p[j], hp, lp);
-    }
-  }
-  return hp + lp - hq - lq;
+  for (int j = 0; j < N; j += 2) add_weights<TWO>(p[j], p[j + 1], q[j], q[j + 1], sum);
 }
 
 // The sum of one warp's units [u0, u1): a unit is 32 x 16 bytes of the row.
@@ -199,6 +229,7 @@ __device__ __forceinline__ unsigned long long range_sum(const Draw& d, int V, in
         a[r] = in ? __ldcs(p + w) : make_uint4(0, 0, 0, 0);
         if (TWO) b[r] = in ? __ldcs(q + w) : make_uint4(0, 0, 0, 0);
       }
+      Parts sum{0u, 0u, 0u};
 #pragma unroll
       for (int r = 0; r < kUnroll; ++r) {
         unsigned int x[E], y[E];
@@ -209,8 +240,9 @@ __device__ __forceinline__ unsigned long long range_sum(const Draw& d, int V, in
           y[j] = TWO ? word_bits<EB>(b[r], j) : 0u;
           if (!TWO && j == skip) x[j] = 0u;
         }
-        acc = sat_add(acc, batch_sum<E, TWO>(x, y, flags));
+        add_batch<E, TWO>(x, y, sum, flags);
       }
+      acc = sat_add(acc, joined<TWO>(sum, kUnroll * E));
     }
   } else {
     constexpr int N = 2 * E;
@@ -224,7 +256,9 @@ __device__ __forceinline__ unsigned long long range_sum(const Draw& d, int V, in
         x[j] = in ? __float_as_uint(load_one<EB>(d.p, i)) : 0u;
         y[j] = TWO && in ? __float_as_uint(load_one<EB>(d.q, i)) : 0u;
       }
-      acc = sat_add(acc, batch_sum<N, TWO>(x, y, flags));
+      Parts sum{0u, 0u, 0u};
+      add_batch<N, TWO>(x, y, sum, flags);
+      acc = sat_add(acc, joined<TWO>(sum, N));
     }
   }
 #pragma unroll

@@ -184,7 +184,7 @@ def test_bad_values_are_flagged_and_stay_inside():
     run(t, d, torch.full_like(tok, 300), gam, u, status=S["BAD_TOKEN"])
     run(t, d, tok, torch.tensor([0, 1, 2, 3, -1, 2], dtype=torch.int32), u, status=S["BAD_GAMMA"])
     run(t, d, tok, gam, u + 1.0, status=S["BAD_UNIFORM"])
-    ones = torch.ones((1, 1, 1000))
+    ones = torch.ones((1, 1, 70000))
     run(ones, None, torch.zeros((1, 0), dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
         torch.tensor([[0.9]]), status=S["BAD_PROB"])
 
