@@ -11,9 +11,10 @@
 // floats as a fraction in [-1/2, 1/2), and cos and sin are taken of that.
 //
 // Bound: q, k and v are read once and written once.  Few rows: latency (the
-// page look-up depends on the request look-up).  A CTA handles kRows rows (one
-// where there are few): their angles are formed once, in shared memory, and
-// serve every head.
+// page look-up depends on the request look-up).  A CTA handles four rows (one
+// where there are few): their angles are formed once, in shared memory, and serve
+// every head.  A thread's first values are under way before the look-ups, and the
+// rows of a task are read together.
 #include "../../include/spec_verify.h"
 #include "internal.h"
 
@@ -23,7 +24,7 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 4;
+constexpr int kManyRows = 2048;  // from here on four rows a CTA
 
 struct AppendParams {
   const char* q;
@@ -34,7 +35,7 @@ struct AppendParams {
   char* v_pages;
   long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;  // elements
   long long kp, kt, kh, vp, vt, vh;  // cache strides: page, token, head
-  int Hq, Hk, D, rot, B, T, G, num_pages, page_size, max_pages, rows;
+  int Hq, Hk, D, rot, B, T, G, num_pages, page_size, max_pages;
   const int32_t* table;
   const int32_t* kv_len;
   const int32_t* cu;
@@ -113,16 +114,75 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int B, int t) {
   return lo;
 }
 
-template <typename T, int VW, bool INTER>
+// A task: two vectors of a head (VW 1: a pair of values), one task a thread and
+// row.  Turning heads pair values j and j + rot / 2 (INTER: neighbours).
+template <int VW>
+struct Words {
+  Vec<VW> x, y;
+};
+template <>
+struct Words<1> {
+  unsigned short x, y;
+};
+
+template <typename T, int VW, bool INTER, int ROWS>
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
-  extern __shared__ float2 s_turn[];  // [rows][rot / 2] cos, sin
-  __shared__ RowInfo s_row[kMaxRows];
-  __shared__ int s_req[kMaxRows];
+  extern __shared__ float2 s_turn[];  // [ROWS][rot / 2] cos, sin
+  __shared__ RowInfo s_row[ROWS];
+  __shared__ long long s_pos[ROWS];
+  __shared__ int s_ok[ROWS];
   const int tid = threadIdx.x, lane = tid & 31;
   const int half = P.rot / 2;
-  const int r0 = blockIdx.x * P.rows;
-  const int nrows = P.T - r0 < P.rows ? P.T - r0 : P.rows;
-  __shared__ long long s_pos[kMaxRows];
+  const int r0 = blockIdx.x * ROWS;
+  const int nrows = P.T - r0 < ROWS ? P.T - r0 : ROWS;
+  const int per_head = VW == 1 ? (P.D + 1) / 2 : P.D / (2 * VW);
+  const int Hs = P.Hq + P.Hk;  // heads that turn
+  const int n = (Hs + P.Hk) * per_head;
+  constexpr int kTasks = ROWS == 1 ? 2 : 1;  // under way together
+
+  // of a task: its head, the values that it moves (elements of the head)
+  struct Task {
+    int h, s, j, j2;
+    bool turns;
+  };
+  auto task_of = [&](int e) {
+    Task t;
+    t.h = e / per_head;
+    t.s = e - t.h * per_head;
+    t.turns = t.h < Hs && t.s < (VW == 1 ? half : P.rot / (2 * VW));
+    const bool apart = t.turns && !INTER;
+    t.j = t.s * (apart ? VW : 2 * VW);
+    t.j2 = apart ? t.j + half : t.j + VW;
+    return t;
+  };
+  auto source = [&](const Task& t, int row) {
+    if (t.h < P.Hq) return P.q + ((long long)row * P.q_row + (long long)t.h * P.q_head) * 2;
+    if (t.h < Hs) return P.k + ((long long)row * P.k_row + (long long)(t.h - P.Hq) * P.k_head) * 2;
+    return P.v + ((long long)row * P.v_row + (long long)(t.h - Hs) * P.v_head) * 2;
+  };
+  Words<VW> w[kTasks][ROWS];
+  auto fetch = [&](int e0) {
+#pragma unroll
+    for (int k = 0; k < kTasks; ++k) {
+      if (e0 + k * kThreads >= n) continue;
+      const Task t = task_of(e0 + k * kThreads);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        if (r >= nrows) continue;
+        const char* src = source(t, r0 + r);
+        if constexpr (VW == 1) {
+          const unsigned short* a = reinterpret_cast<const unsigned short*>(src);
+          w[k][r].x = a[t.j];
+          w[k][r].y = t.j2 < P.D ? a[t.j2] : (unsigned short)0;
+        } else {
+          w[k][r].x = load_vec<VW>(src + t.j * 2);
+          w[k][r].y = load_vec<VW>(src + t.j2 * 2);
+        }
+      }
+    }
+  };
+  fetch(tid);
+
   if (tid < 32) {
     const int b0 = request_of(P.cu, P.B, r0);
     unsigned int flags = 0;
@@ -130,16 +190,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
       const int t = r0 + lane;
       int b = b0;
       while (b + 1 < P.B && (long long)P.cu[b + 1] + b + 1 <= t) ++b;
-      const int c0 = P.cu[b], c1 = P.cu[b + 1];
+      const int c0 = P.cu[b], c1 = P.cu[b + 1], len = P.kv_len[b];
       const int i = t - b - c0;
       RowInfo info{-1, -1};
       long long pos = 0;
       if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 + P.B > P.T || i < 0 || i > c1 - c0) {
         flags = SV_STATUS_BAD_GAMMA;
       } else {
-        const int n = P.kv_len[b];
-        const long long slot = (long long)n + i;
-        if (n < 0 || slot >= (long long)P.max_pages * P.page_size) {
+        const long long slot = (long long)len + i;
+        if (len < 0 || slot >= (long long)P.max_pages * P.page_size) {
           flags = SV_STATUS_BAD_LENGTH;
         } else {
           const int page = P.table[(size_t)b * P.max_pages + slot / P.page_size];
@@ -150,12 +209,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
             info.k_at = page * P.kp + in * P.kt;
             info.v_at = page * P.vp + in * P.vt;
           }
-          pos = P.positions ? (long long)P.positions[t] : (long long)P.offset + slot;
         }
+        pos = P.positions ? (long long)P.positions[t] : (long long)P.offset + slot;
       }
       s_row[lane] = info;
       s_pos[lane] = pos;
-      s_req[lane] = flags & SV_STATUS_BAD_GAMMA ? -1 : b;
+      s_ok[lane] = flags != SV_STATUS_BAD_GAMMA;
     }
     const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0 && any) atomicOr(P.status, any);
@@ -169,95 +228,77 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
     s_turn[e] = make_float2(cs * P.scale, sn * P.scale);
   }
   __syncthreads();
-  const int per_head = VW == 1 ? (P.D + 1) / 2 : P.D / (2 * VW);
-  const int Hs = P.Hq + P.Hk;  // heads that turn
-  for (int r = 0; r < nrows; ++r) {
-    const int t = r0 + r;
-    if (s_req[r] < 0) continue;
-    const RowInfo info = s_row[r];
-    const float2* turn = s_turn + r * half;
-    const char* q = P.q + (size_t)t * P.q_row * 2;
-    const char* k = P.k + (size_t)t * P.k_row * 2;
-    const char* v = P.v + (size_t)t * P.v_row * 2;
-    char* o = P.q_out + (size_t)t * P.o_row * 2;
-    const int n = (Hs + P.Hk) * per_head;
-    for (int e = tid; e < n; e += kThreads) {
-      const int h = e / per_head, s = e - h * per_head;
-      const char* src;
-      char* dst;
-      if (h < P.Hq) {
-        src = q + (long long)h * P.q_head * 2;
-        dst = o + (long long)h * P.o_head * 2;
-      } else if (h < Hs) {
-        if (info.k_at < 0) continue;
-        src = k + (long long)(h - P.Hq) * P.k_head * 2;
-        dst = P.k_pages + (info.k_at + (long long)(h - P.Hq) * P.kh) * 2;
-      } else {
-        if (info.k_at < 0) continue;
-        src = v + (long long)(h - Hs) * P.v_head * 2;
-        dst = P.v_pages + (info.v_at + (long long)(h - Hs) * P.vh) * 2;
-      }
-      const bool turns = h < Hs && s < (VW == 1 ? half : P.rot / (2 * VW));
-      if constexpr (VW == 1) {
-        // one pair of values
-        const unsigned short* a = reinterpret_cast<const unsigned short*>(src);
-        unsigned short* d = reinterpret_cast<unsigned short*>(dst);
-        const int j = turns && !INTER ? s : 2 * s;
-        const int j2 = turns && !INTER ? s + half : 2 * s + 1;
-        if (!turns) {
-          d[j] = a[j];
-          if (j2 < P.D) d[j2] = a[j2];
+
+#pragma unroll 1
+  for (int e0 = tid; e0 < n; e0 += kTasks * kThreads) {
+    if (e0 != tid) fetch(e0);
+#pragma unroll
+    for (int k = 0; k < kTasks; ++k) {
+      if (e0 + k * kThreads >= n) continue;
+      const Task t = task_of(e0 + k * kThreads);
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        if (r >= nrows || !s_ok[r]) continue;
+        char* dst;
+        if (t.h < P.Hq) {
+          dst = P.q_out + ((long long)(r0 + r) * P.o_row + (long long)t.h * P.o_head) * 2;
         } else {
-          const float2 x = Conv<T>::up((unsigned int)a[j] | ((unsigned int)a[j2] << 16));
-          const float2 c = turn[s];
-          const unsigned int y = Conv<T>::down(x.x * c.x - x.y * c.y, x.y * c.x + x.x * c.y);
-          d[j] = (unsigned short)y;
-          d[j2] = (unsigned short)(y >> 16);
+          const RowInfo info = s_row[r];
+          if (info.k_at < 0) continue;
+          dst = t.h < Hs ? P.k_pages + (info.k_at + (long long)(t.h - P.Hq) * P.kh) * 2
+                         : P.v_pages + (info.v_at + (long long)(t.h - Hs) * P.vh) * 2;
         }
-      } else if (!turns) {
-        const Vec<VW> x = load_vec<VW>(src + (size_t)s * VW * 4), y = load_vec<VW>(src + (size_t)s * VW * 4 + VW * 2);
-        store_vec<VW>(dst + (size_t)s * VW * 4, x);
-        store_vec<VW>(dst + (size_t)s * VW * 4 + VW * 2, y);
-      } else if (INTER) {
-        // two neighbouring vectors hold VW pairs
-        Vec<VW> x[2];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) x[m] = load_vec<VW>(src + (size_t)s * VW * 4 + m * VW * 2);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-#pragma unroll
-          for (int w = 0; w < VW / 2; ++w) {
-            const float2 a = Conv<T>::up(x[m].w[w]);
-            const float2 c = turn[s * VW + m * (VW / 2) + w];
-            x[m].w[w] = Conv<T>::down(a.x * c.x - a.y * c.y, a.y * c.x + a.x * c.y);
+        const float2* turn = s_turn + r * half;
+        Words<VW> u = w[k][r];
+        if constexpr (VW == 1) {
+          unsigned short* d = reinterpret_cast<unsigned short*>(dst);
+          if (t.turns) {
+            const float2 a = Conv<T>::up((unsigned int)u.x | ((unsigned int)u.y << 16)), c = turn[t.s];
+            const unsigned int y = Conv<T>::down(a.x * c.x - a.y * c.y, a.y * c.x + a.x * c.y);
+            u.x = (unsigned short)y;
+            u.y = (unsigned short)(y >> 16);
           }
-          store_vec<VW>(dst + (size_t)s * VW * 4 + m * VW * 2, x[m]);
-        }
-      } else {
-        Vec<VW> x = load_vec<VW>(src + (size_t)s * VW * 2), y = load_vec<VW>(src + ((size_t)half + s * VW) * 2);
+          d[t.j] = u.x;
+          if (t.j2 < P.D) d[t.j2] = u.y;
+        } else {
+          if (t.turns && INTER) {
 #pragma unroll
-        for (int w = 0; w < VW / 2; ++w) {
-          const float2 a = Conv<T>::up(x.w[w]), b = Conv<T>::up(y.w[w]);
-          const float2 c0 = turn[s * VW + 2 * w], c1 = turn[s * VW + 2 * w + 1];
-          x.w[w] = Conv<T>::down(a.x * c0.x - b.x * c0.y, a.y * c1.x - b.y * c1.y);
-          y.w[w] = Conv<T>::down(b.x * c0.x + a.x * c0.y, b.y * c1.x + a.y * c1.y);
+            for (int i = 0; i < VW / 2; ++i) {
+              const float2 a = Conv<T>::up(u.x.w[i]), b = Conv<T>::up(u.y.w[i]);
+              const float2 c0 = turn[t.s * VW + i], c1 = turn[t.s * VW + VW / 2 + i];
+              u.x.w[i] = Conv<T>::down(a.x * c0.x - a.y * c0.y, a.y * c0.x + a.x * c0.y);
+              u.y.w[i] = Conv<T>::down(b.x * c1.x - b.y * c1.y, b.y * c1.x + b.x * c1.y);
+            }
+          } else if (t.turns) {
+#pragma unroll
+            for (int i = 0; i < VW / 2; ++i) {
+              const float2 a = Conv<T>::up(u.x.w[i]), b = Conv<T>::up(u.y.w[i]);
+              const float2 c0 = turn[t.s * VW + 2 * i], c1 = turn[t.s * VW + 2 * i + 1];
+              u.x.w[i] = Conv<T>::down(a.x * c0.x - b.x * c0.y, a.y * c1.x - b.y * c1.y);
+              u.y.w[i] = Conv<T>::down(b.x * c0.x + a.x * c0.y, b.y * c1.x + a.y * c1.y);
+            }
+          }
+          store_vec<VW>(dst + t.j * 2, u.x);
+          store_vec<VW>(dst + t.j2 * 2, u.y);
         }
-        store_vec<VW>(dst + (size_t)s * VW * 2, x);
-        store_vec<VW>(dst + ((size_t)half + s * VW) * 2, y);
       }
     }
   }
 }
 
+template <typename T, int VW, bool INTER, int ROWS>
+int launch_rows(const AppendParams& P, cudaStream_t stream) {
+  const unsigned int grid = (unsigned int)((P.T + ROWS - 1) / ROWS);
+  append_kernel<T, VW, INTER, ROWS><<<grid, kThreads, (size_t)ROWS * (P.rot / 2) * sizeof(float2), stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
 template <typename T, int VW>
 int launch(const AppendParams& P, bool inter, cudaStream_t stream) {
-  const unsigned int grid = (unsigned int)((P.T + P.rows - 1) / P.rows);
-  const size_t smem = (size_t)P.rows * (P.rot / 2) * sizeof(float2);
-  if (inter)
-    append_kernel<T, VW, true><<<grid, kThreads, smem, stream>>>(P);
-  else
-    append_kernel<T, VW, false><<<grid, kThreads, smem, stream>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  // four rows a CTA where one row each would be more than two waves of CTAs
+  if (P.T >= kManyRows)
+    return inter ? launch_rows<T, VW, true, 4>(P, stream) : launch_rows<T, VW, false, 4>(P, stream);
+  return inter ? launch_rows<T, VW, true, 1>(P, stream) : launch_rows<T, VW, false, 1>(P, stream);
 }
 
 template <typename T>
@@ -319,7 +360,6 @@ extern "C" int spec_verify_kv_append(const void* q, const int64_t* q_strides, in
   P.num_pages = c.num_pages;
   P.page_size = c.page_size;
   P.max_pages = c.max_pages;
-  P.rows = P.T >= 2048 ? kMaxRows : 1;
   P.table = c.page_table;
   P.kv_len = c.kv_len;
   P.cu = cu_draft;
