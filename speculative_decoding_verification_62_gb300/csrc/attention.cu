@@ -94,9 +94,14 @@ struct AttnParams {
   float* lse;
   unsigned int* status;
   int* starts;         // [B + 1]: first tile of each request in list B, and the list's end
-  float* dense[2];     // own, prefix: rows of whole units [T * Hq][DP]
-  float* dense_lse[2];
-  float* slot;         // [kSlots][kRows][DP]
+  // Parts: whole units over own keys as rows [T * Hq][DP]; whole prefix units by
+  // block [Hk][blocks] and parts of units by slot [kSlots], both as [DP / 8][kRows][8]
+  // (a warp's lanes have a row each: their stores are one run of memory)
+  float* own;
+  float* own_lse;
+  float* whole;
+  float* whole_lse;
+  float* slot;
   float* slot_lse;
   unsigned long long wait_ns;
 };
@@ -901,14 +906,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       const size_t at = (size_t)(p.row0 + skip + tok) * P.Hq + (size_t)p.h * P.group + g;
       float* part = nullptr;
       float* part_lse = nullptr;
+      int jump = 8;  // from eight values of the row to the next
       if (!direct) {
-        if (whole) {
-          part = P.dense[p.prefix] + at * DP;
-          part_lse = P.dense_lse[p.prefix] + at;
+        if (whole && !p.prefix) {
+          part = P.own + at * DP;
+          part_lse = P.own_lse + at;
         } else {
-          const size_t r = (size_t)(part_base + (p.t0 == 0 ? (PAIR ? 2 : 1) : 0)) * kRows + row;
-          part = P.slot + r * DP;
-          part_lse = P.slot_lse + r;
+          const size_t tile = whole ? (size_t)p.h * (2 * P.pairs + P.odd) + p.row0 / P.tpq + (PAIR ? s : 0)
+                                    : (size_t)(part_base + (p.t0 == 0 ? (PAIR ? 2 : 1) : 0));
+          part = (whole ? P.whole : P.slot) + tile * kRows * DP + row * 8;
+          part_lse = (whole ? P.whole_lse : P.slot_lse) + tile * kRows + row;
+          jump = kRows * 8;
         }
       }
 #pragma unroll 1
@@ -935,7 +943,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
             }
           } else {
 #pragma unroll
-            for (int y = 0; y < 32; y += 8) store8(part + x + y, o + y);
+            for (int y = 0; y < 32; y += 8) store8(part + (x + y) / 8 * jump, o + y);
           }
         }
       }
@@ -1148,21 +1156,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct Unit {
   bool pair;
   int c0, count;   // first share, shares
-  int slot_row, stream, which;
-};
-// The running join of some of a row's parts: a lane holds W values.
-template <int W>
-struct Joined {
-  float o[W], m, l;
+  int slot_row, stream;
 };
 
-// WARPS warps a row: one where rows are many; four, each with every fourth part,
-// where few rows have many parts (one request of 131000 tokens: 38 parts).
-template <typename T, int DP, int WARPS>
+// A group of DP / 8 lanes a row, each with eight neighbouring values; or, where few
+// rows have many parts (MANY; one request of 131000 tokens: 38), a CTA a row, whose
+// groups share the row's parts and are joined at the end.
+template <typename T, int DP, bool MANY>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ AttnParams P, int ctas) {
-  constexpr int W = DP / 32, kAhead = 8;  // values a lane; rows of parts loaded at once
+  constexpr int kLanes = DP / 8, kGroups = 32 / kLanes;  // lanes of a group, groups of a warp
   __shared__ float s_o[4][DP], s_m[4], s_l[4];
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int in = lane % kLanes, group = lane / kLanes;
   unsigned int ignored = 0;
   const Req r = request(P, b, ignored);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's writes
@@ -1173,10 +1178,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
   // without a prefix, requests whose units all lie within one share are done
   if (P.prefix_len == 0 && first / L.per_b == (first + request_tiles(P, r) - 1) / L.per_b) return;
   const int rows = r.n * P.Hq;
-  constexpr int kPerCta = 4 / WARPS;
+  constexpr int kRowsCta = MANY ? 1 : 4 * kGroups;
+  const int x0 = blockIdx.y * kRowsCta + (MANY ? 0 : warp * kGroups + group);
 #pragma unroll 1
-  for (int x = blockIdx.y * kPerCta + (WARPS == 1 ? warp : 0); x < rows; x += gridDim.y * kPerCta) {
-    const int i = x / P.Hq, head = x - i * P.Hq;
+  for (int x = x0; x - (MANY ? 0 : group) < rows; x += gridDim.y * kRowsCta) {
+    const bool live = x < rows;
+    const int i = (live ? x : 0) / P.Hq, head = (live ? x : 0) - i * P.Hq;
     const int h = head / P.group, g = head - h * P.group;
     const size_t at = (size_t)(r.row0 + i) * P.Hq + head;
     const int rb = i / P.tpq;
@@ -1190,120 +1197,130 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     own.c0 = u0 / L.per_b;
     own.count = (u0 + tiles - 1) / L.per_b - own.c0 + 1;
     own.slot_row = (i - rb * P.tpq) * P.group + g;
-    own.stream = own.which = 0;
+    own.stream = 0;
     pre = own;
     pre.count = 0;
-    if (P.prefix_len == 0) {
-      if (own.count == 1) continue;  // written already
-    } else {
-      const int t = r.row0 + i, blk = t / P.tpq;
+    int blk = 0;
+    if (P.prefix_len > 0) {
+      const int t = r.row0 + i;
+      blk = t / P.tpq;
       pre.pair = blk < 2 * P.pairs;
       pre.slot_row = (t - blk * P.tpq) * P.group + g;
       pre.stream = blk & 1;
-      pre.which = 1;
       const int per = pre.pair ? L.per_a : L.per_b;
       const int t_unit = pre.pair ? P.pair_tiles : P.prefix_tiles;
       const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * t_unit;
       pre.c0 = v0 / per;
       pre.count = (v0 + t_unit - 1) / per - pre.c0 + 1;
     }
-    const int all = pre.count + own.count;
-    const int skip = WARPS == 1 ? 0 : warp, parts = (all - skip + WARPS - 1) / WARPS;  // of this warp
-    // 32 parts at a time: their sums by lane, then their rows, eight loads under way
-    Joined<W> J;
+    const bool done = P.prefix_len == 0 && own.count == 1;  // written already
+    const int parts = live && !done ? pre.count + own.count : 0;
+    // where part k lies: its first eight values, the way to the next eight, its sum
+    auto place = [&](int k, const float*& src, int& jump, const float*& lse) {
+      const Unit& u = k < pre.count ? pre : own;
+      const int j = k < pre.count ? k : k - pre.count;
+      if (u.count == 1 && k >= pre.count) {
+        src = P.own + at * DP;
+        lse = P.own_lse + at;
+        jump = 8;
+        return;
+      }
+      const int c = u.c0 + j;
+      const size_t tile =
+          u.count == 1 ? (size_t)h * (2 * P.pairs + P.odd) + blk
+                       : (size_t)(u.pair ? 4 * c + u.stream + 2 * (j == 0)
+                                         : 4 * (L.ctas_a + c / 2) + 2 * (c & 1) + (j == 0));
+      src = (u.count == 1 ? P.whole : P.slot) + tile * kRows * DP + u.slot_row * 8;
+      lse = (u.count == 1 ? P.whole_lse : P.slot_lse) + tile * kRows + u.slot_row;
+      jump = kRows * 8;
+    };
+    float o[8], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int y = 0; y < W; ++y) J.o[y] = 0.f;
-    J.m = -INFINITY;
-    J.l = 0.f;
+    for (int y = 0; y < 8; ++y) o[y] = 0.f;
+    constexpr int kAhead = 4, kStep = MANY ? 4 * kGroups : 1;
 #pragma unroll 1
-    for (int p0 = 0; p0 < parts; p0 += 32) {
-      const int k = (p0 + lane) * WARPS + skip;
-      const float* src = P.slot;
-      float lse2 = -INFINITY;
-      if (p0 + lane < parts) {
-        const Unit& u = k < pre.count ? pre : own;
-        const int j = k < pre.count ? k : k - pre.count;
-        if (u.count == 1) {
-          src = P.dense[u.which] + at * DP;
-          lse2 = P.dense_lse[u.which][at];
-        } else {
-          const int c = u.c0 + j;
-          const int id = u.pair ? 4 * c + u.stream + 2 * (j == 0) : 4 * (L.ctas_a + c / 2) + 2 * (c & 1) + (j == 0);
-          const size_t s = (size_t)id * kRows + u.slot_row;
-          src = P.slot + s * DP;
-          lse2 = P.slot_lse[s];
+    for (int k0 = MANY ? warp * kGroups + group : 0; k0 < parts; k0 += kAhead * kStep) {
+      float v[kAhead][8], e[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = k0 + j * kStep;
+        e[j] = -INFINITY;
+        if (k < parts) {
+          const float *src, *lse;
+          int jump;
+          place(k, src, jump, lse);
+          e[j] = *lse;
+          const float4 a = *reinterpret_cast<const float4*>(src + in * jump),
+                       c = *reinterpret_cast<const float4*>(src + in * jump + 4);
+          v[j][0] = a.x, v[j][1] = a.y, v[j][2] = a.z, v[j][3] = a.w;
+          v[j][4] = c.x, v[j][5] = c.y, v[j][6] = c.z, v[j][7] = c.w;
         }
       }
-      float top = lse2;  // (a NaN is dropped here, and kept by its weight)
+      float top = m;
 #pragma unroll
-      for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
-      top = fmaxf(top, J.m);
-      const float scale = J.m == -INFINITY ? 0.f : exp2f(J.m - top);
-      const float w = lse2 == -INFINITY ? 0.f : exp2f(lse2 - top);  // -inf: no key seen there
-      float sum = w;
+      for (int j = 0; j < kAhead; ++j) top = fmaxf(top, e[j]);  // (a NaN is dropped here, and kept by its weight)
+      const float scale = m == -INFINITY ? 0.f : exp2f(m - top);
+      l *= scale;
 #pragma unroll
-      for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
-      J.l = J.l * scale + sum;
-      J.m = top;
+      for (int y = 0; y < 8; ++y) o[y] *= scale;
+      m = top;
 #pragma unroll
-      for (int y = 0; y < W; ++y) J.o[y] *= scale;
-      const int n = parts - p0 < 32 ? parts - p0 : 32;
-#pragma unroll 1
-      for (int j0 = 0; j0 < n; j0 += kAhead) {
-        float v[kAhead][W], wj[kAhead];
+      for (int j = 0; j < kAhead; ++j) {
+        if (e[j] == -INFINITY) continue;  // no key seen there
+        const float w = exp2f(e[j] - top);
+        l += w;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-          const float* pj = reinterpret_cast<const float*>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), (j0 + j) & 31));
-          const bool in = j0 + j < n;
-          if (W == 4) {
-            const float4 q = in ? *reinterpret_cast<const float4*>(pj + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[j][0] = q.x, v[j][1] = q.y, v[j][2 % W] = q.z, v[j][3 % W] = q.w;
-          } else {
-            const float2 q = in ? *reinterpret_cast<const float2*>(pj + lane * 2) : make_float2(0.f, 0.f);
-            v[j][0] = q.x, v[j][1] = q.y;
-          }
-          if (!in) wj[j] = 0.f;
+        for (int y = 0; y < 8; ++y) o[y] += v[j][y] * w;
+      }
+    }
+    if (MANY) {
+      // the groups' joins, in a fixed order
+#pragma unroll
+      for (int d = kLanes; d < 32; d <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, d), l2 = __shfl_xor_sync(0xffffffffu, l, d);
+        const float top = fmaxf(m, m2);
+        const float f = m == -INFINITY ? (l != l ? 1.f : 0.f) : exp2f(m - top);
+        const float f2 = m2 == -INFINITY ? (l2 != l2 ? 1.f : 0.f) : exp2f(m2 - top);
+        l = l * f + l2 * f2;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const float o2 = __shfl_xor_sync(0xffffffffu, o[y], d);
+          o[y] = (f == 0.f ? 0.f : o[y] * f) + (f2 == 0.f ? 0.f : o2 * f2);
         }
+        m = top;
+      }
+      __syncthreads();
+      if (group == 0) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
+        for (int y = 0; y < 8; ++y) s_o[warp][in * 8 + y] = o[y];
+        if (in == 0) s_m[warp] = m, s_l[warp] = l;
+      }
+      __syncthreads();
+      if (warp == 0 && group == 0) {
+        m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        l = 0.f;
 #pragma unroll
-          for (int y = 0; y < W; ++y) J.o[y] += wj[j] == 0.f ? 0.f : v[j][y] * wj[j];
+        for (int y = 0; y < 8; ++y) o[y] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float f = s_m[k] == -INFINITY ? (s_l[k] != s_l[k] ? 1.f : 0.f) : exp2f(s_m[k] - m);
+          l += s_l[k] * f;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) o[y] += f == 0.f ? 0.f : s_o[k][in * 8 + y] * f;
+        }
       }
     }
-    if (WARPS > 1) {
-      // the warps' joins, in their order
-      __syncthreads();
-#pragma unroll
-      for (int y = 0; y < W; ++y) s_o[warp][lane * W + y] = J.o[y];
-      if (lane == 0) s_m[warp] = J.m, s_l[warp] = J.l;
-      __syncthreads();
-      if (warp != 0) continue;
-      float top = -INFINITY;
-#pragma unroll
-      for (int y = 0; y < WARPS; ++y) top = fmaxf(top, s_m[y]);
-      J.l = 0.f;
-#pragma unroll
-      for (int y = 0; y < W; ++y) J.o[y] = 0.f;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float f = s_m[k] == -INFINITY && s_l[k] == 0.f ? 0.f : exp2f(s_m[k] - top);
-        J.l += s_l[k] * f;
-#pragma unroll
-        for (int y = 0; y < W; ++y) J.o[y] += f == 0.f ? 0.f : s_o[k][lane * W + y] * f;
-      }
-      J.m = top;
+    if (!live || done || (MANY && (warp != 0 || group != 0))) continue;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    if (in * 8 < P.D) {
+      uint4 q;
+      q.x = Type<T>::pack(o[0] * inv, o[1] * inv);
+      q.y = Type<T>::pack(o[2] * inv, o[3] * inv);
+      q.z = Type<T>::pack(o[4] * inv, o[5] * inv);
+      q.w = Type<T>::pack(o[6] * inv, o[7] * inv);
+      *reinterpret_cast<uint4*>(P.out + (at * P.D + in * 8) * 2) = q;
     }
-    const float inv = J.l > 0.f || J.l != J.l ? 1.f / J.l : 0.f;
-    if (W == 4) {
-      if (lane * 4 < P.D)
-        *reinterpret_cast<uint2*>(P.out + (at * P.D + lane * 4) * 2) =
-            make_uint2(Type<T>::pack(J.o[0] * inv, J.o[1] * inv), Type<T>::pack(J.o[2 % W] * inv, J.o[3 % W] * inv));
-    } else if (lane * 2 < P.D) {
-      *reinterpret_cast<uint32_t*>(P.out + (at * P.D + lane * 2) * 2) = Type<T>::pack(J.o[0] * inv, J.o[1] * inv);
-    }
-    if (P.lse && lane == 0) P.lse[at] = (J.m + log2f(J.l)) * 0.693147180559945309f;
+    if (P.lse && in == 0) P.lse[at] = (m + log2f(l)) * 0.693147180559945309f;
   }
 }
 
@@ -1345,10 +1362,13 @@ bool encode(CUtensorMap* map, sv_dtype dtype, const void* base, const uint64_t (
 }
 
 struct AttnLayout {
-  size_t starts, dense[2], dense_lse[2], slot, slot_lse, total;
+  size_t starts, own, own_lse, whole, whole_lse, slot, slot_lse, total;
 };
 AttnLayout attn_layout(long long T, int Hq, int D) {
   const size_t dp = D <= 64 ? 64 : 128, rows = (size_t)T * Hq;
+  // blocks of the prefix in every grouping of the heads: a block holds at least
+  // kRows / 2 + 1 rows (kRows - group + 1 of a larger group) but the last of a key head
+  const size_t tiles = rows / (kRows / 2) + Hq;
   AttnLayout L;
   size_t at = 256;  // the status word
   auto take = [&](size_t bytes) {
@@ -1357,8 +1377,10 @@ AttnLayout attn_layout(long long T, int Hq, int D) {
     return a;
   };
   L.starts = take((size_t)(T + 1) * sizeof(int));
-  for (int i = 0; i < 2; ++i) L.dense[i] = take(rows * dp * 4);
-  for (int i = 0; i < 2; ++i) L.dense_lse[i] = take(rows * 4);
+  L.own = take(rows * dp * 4);
+  L.own_lse = take(rows * 4);
+  L.whole = take(tiles * kRows * dp * 4);
+  L.whole_lse = take(tiles * kRows * 4);
   L.slot = take((size_t)kSlots * kRows * dp * 4);
   L.slot_lse = take((size_t)kSlots * kRows * 4);
   L.total = at;
@@ -1387,11 +1409,12 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   if (grid <= 0) return SV_ERR_CUDA;
   attention_kernel<T, DP><<<grid, kThreads, Shape<DP, false>::smem, stream>>>(m, P);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  // The launch itself overlaps the attention kernel, whose end the CTAs wait
-  // for.  Four warps a row where all rows are at most four waves of CTAs.
+  // The launch itself overlaps the attention kernel, whose end the CTAs wait for.
+  // A CTA a row where the shares are more than eight times the units.
+  const bool many = 2ll * grid > 8ll * P.B * P.Hk;
   const long long rows = (long long)(P.G < P.T ? P.G + 1 : P.T) * P.Hq;
-  const bool few = (long long)P.T * P.Hq <= 4096;
-  const long long y = few ? rows : (rows + 3) / 4;
+  const int per_cta = many ? 1 : 4 * (32 / (DP / 8));
+  const long long y = (rows + per_cta - 1) / per_cta;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned int)P.B, (unsigned int)(y < 1024 ? y : 1024));
   cfg.blockDim = dim3(128);
@@ -1401,7 +1424,7 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few ? combine_kernel<T, DP, 4> : combine_kernel<T, DP, 1>, P, grid) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, many ? combine_kernel<T, DP, true> : combine_kernel<T, DP, false>, P, grid) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;
 }
@@ -1481,10 +1504,10 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   char* w = static_cast<char*>(workspace);
   P.status = reinterpret_cast<unsigned int*>(w);
   P.starts = reinterpret_cast<int*>(w + L.starts);
-  for (int i = 0; i < 2; ++i) {
-    P.dense[i] = reinterpret_cast<float*>(w + L.dense[i]);
-    P.dense_lse[i] = reinterpret_cast<float*>(w + L.dense_lse[i]);
-  }
+  P.own = reinterpret_cast<float*>(w + L.own);
+  P.own_lse = reinterpret_cast<float*>(w + L.own_lse);
+  P.whole = reinterpret_cast<float*>(w + L.whole);
+  P.whole_lse = reinterpret_cast<float*>(w + L.whole_lse);
   P.slot = reinterpret_cast<float*>(w + L.slot);
   P.slot_lse = reinterpret_cast<float*>(w + L.slot_lse);
   P.wait_ns = sv::wait_limit_ns();
