@@ -8,7 +8,6 @@ cannot be loaded or built, the first call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import threading
@@ -333,8 +332,9 @@ def spec_verify_greedy(target_logits, draft_tokens, gamma, out_tokens, num_accep
         raise SpecVerifyError(rc)
 
 
-# The calls below check their tensors with few Python steps: a small batch's kernel
-# takes 4 to 10 us, less than a careless wrapper.
+# The calls below check their tensors in few Python steps, in line: a small batch's
+# kernel takes 4 to 10 us, less than a careless wrapper.  What does not pass goes
+# through _arg, which says what is wrong.
 def _arg(t, name, dtype, shape, index):
     """Address of a contiguous tensor of that dtype and shape (None: any) on CUDA device `index`."""
     if isinstance(t, torch.Tensor):
@@ -353,20 +353,22 @@ def _index(t, name):
     return t.get_device()
 
 
-def _on(index):
-    """Makes `index` the current device for a launch; nothing to do in the usual case."""
-    if torch.cuda.current_device() == index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(index)
+# (the public ways take 1 us more)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1 us less than the public way
-
-
-def _stream_of(stream, index):
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+def _launch(call, index, stream, *args):
+    """The C call on the tensors' device, on `stream` or that device's current one."""
+    stream = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current() == index:
+        rc = call(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, stream)
+    if rc != 0:
+        raise SpecVerifyError(rc)
 
 
 @functools.lru_cache(maxsize=256)
@@ -374,63 +376,47 @@ def _two(a, b):
     return (ctypes.c_int64 * 2)(a, b)
 
 
-def _probs_args(target_probs, draft_probs, draft_shape, index):
-    """Addresses and type code of the rows."""
-    code = _dtype_code(target_probs)
-    tp = _arg(target_probs, "target_probs", target_probs.dtype, None, index)
-    dp = None
-    if draft_probs is not None:
-        dp = _arg(draft_probs, "draft_probs", target_probs.dtype, draft_shape, index)
-    return tp, dp, code
-
-
 def spec_verify_sample_probs(target_probs, draft_probs, draft_tokens, gamma, uniforms, out_tokens,
                              num_accepted, workspace, stream=None) -> None:
     """Sampling verify step on probabilities instead of logits; draft_probs None: the
     drafts were certain (looked up).  See include/spec_verify.h."""
-    lib = _lib or load_library()
     index = _index(target_probs, "target_probs")
+    dtype, i32 = target_probs.dtype, torch.int32
     B, G1, V = target_probs.shape
     G = G1 - 1
-    tp, dp, code = _probs_args(target_probs, draft_probs, (B, G, V), index)
-    i32 = torch.int32
-    with _on(index):
-        rc = lib.spec_verify_sample_probs(
-            tp, dp, code, B, G, V, _arg(draft_tokens, "draft_tokens", i32, (B, G), index),
+    _launch((_lib or load_library()).spec_verify_sample_probs, index, stream,
+            _arg(target_probs, "target_probs", dtype, None, index),
+            None if draft_probs is None else _arg(draft_probs, "draft_probs", dtype, (B, G, V), index),
+            SV_F32 if dtype is torch.float32 else _dtype_code(target_probs), B, G, V,
+            _arg(draft_tokens, "draft_tokens", i32, (B, G), index),
             _arg(gamma, "gamma", i32, (B,), index),
             _arg(uniforms, "uniforms", torch.float32, (B, G1), index),
             _arg(out_tokens, "out_tokens", i32, (B, G1), index),
             _arg(num_accepted, "num_accepted", i32, (B,), index),
-            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel(),
-            _stream_of(stream, index))
-    if rc != 0:
-        raise SpecVerifyError(rc)
+            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 
 
 def spec_verify_sample_probs_packed(target_probs, draft_probs, cu_draft, draft_tokens, uniforms,
                                     out_tokens, num_accepted, workspace, stream=None) -> None:
     """spec_verify_sample_probs on the packed layout; see include/spec_verify.h."""
-    lib = _lib or load_library()
     index = _index(target_probs, "target_probs")
+    dtype, i32 = target_probs.dtype, torch.int32
     B = cu_draft.numel() - 1
     total = draft_tokens.numel()
     rows, V = target_probs.shape
     G = out_tokens.shape[1] - 1
     if rows != total + B:
         raise ValueError("target_probs must have total_drafts + B rows")
-    tp, dp, code = _probs_args(target_probs, draft_probs, (total, V), index)
-    i32 = torch.int32
-    with _on(index):
-        rc = lib.spec_verify_sample_probs_packed(
-            tp, dp, code, B, G, V, _arg(cu_draft, "cu_draft", i32, (B + 1,), index), total,
+    _launch((_lib or load_library()).spec_verify_sample_probs_packed, index, stream,
+            _arg(target_probs, "target_probs", dtype, None, index),
+            None if draft_probs is None else _arg(draft_probs, "draft_probs", dtype, (total, V), index),
+            SV_F32 if dtype is torch.float32 else _dtype_code(target_probs), B, G, V,
+            _arg(cu_draft, "cu_draft", i32, (B + 1,), index), total,
             _arg(draft_tokens, "draft_tokens", i32, (total,), index),
             _arg(uniforms, "uniforms", torch.float32, (rows,), index),
             _arg(out_tokens, "out_tokens", i32, (B, G + 1), index),
             _arg(num_accepted, "num_accepted", i32, (B,), index),
-            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel(),
-            _stream_of(stream, index))
-    if rc != 0:
-        raise SpecVerifyError(rc)
+            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 
 
 class PagedCache:
@@ -480,7 +466,7 @@ class PagedCache:
         _dev(kv_len, "kv_len", torch.int32, (B,))
         self.k_pages, self.v_pages, self.page_table, self.kv_len = k_pages, v_pages, page_table, kv_len
         self.batch, self.kv_heads, self.head_dim, self.dtype = B, heads, dim, k_pages.dtype
-        self.page_size = page
+        self.page_size, self.scale = page, dim ** -0.5
         ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
         self.struct = _KvCache(
             k_pages.data_ptr(), v_pages.data_ptr(),
@@ -536,7 +522,6 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     """Append a step's keys and values to the paged cache and rotate its queries and keys;
     q and q_out may be None, freq (rope.fixed_point) None for no rotation.  See
     include/spec_verify.h."""
-    lib = _lib or load_library()
     index = cache.index
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
@@ -557,22 +542,17 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     if freq is not None:
         half = freq.numel()
         rot, fp = 2 * half, _arg(freq, "freq", torch.int64, (half,), index)
-    with _on(index):
-        rc = lib.spec_verify_kv_append(
+    _launch((_lib or load_library()).spec_verify_kv_append, index, stream,
             qp, qs, heads, kp, ks, vp, vs, op, os_, cache.ref, cu, rows - cache.batch, max_drafts, fp,
             rot, 1 if interleaved else 0, rope_scale,
             None if positions is None else _arg(positions, "positions", torch.int32, (rows,), index),
-            position_offset, _arg(workspace, "workspace", torch.uint8, None, index),
-            workspace.numel(), _stream_of(stream, index))
-    if rc != 0:
-        raise SpecVerifyError(rc)
+            position_offset, _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 
 
 def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix_table=None,
                           prefix_len=0, scale=None, draft_mask=None, lse=None, stream=None) -> None:
     """Attention of a step's rows over the paged cache (and a prefix that the batch shares);
     scale None: head_dim ** -0.5.  See include/spec_verify.h."""
-    lib = _lib or load_library()
     index = cache.index
     _index(q, "q")
     rows, heads = q.shape[0], q.shape[1]
@@ -587,16 +567,12 @@ def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix
         if draft_mask.dtype not in (torch.int32, torch.uint32):
             raise TypeError("draft_mask must be int32 or uint32 words")
         mask = _arg(draft_mask, "draft_mask", draft_mask.dtype, (rows,), index)
-    with _on(index):
-        rc = lib.spec_verify_attention(
+    _launch((_lib or load_library()).spec_verify_attention, index, stream,
             qp, qs, heads, cache.ref, pt, prefix_len, cu, rows - cache.batch, max_drafts,
-            cache.head_dim ** -0.5 if scale is None else scale, mask,
+            cache.scale if scale is None else scale, mask,
             _arg(out, "out", cache.dtype, (rows, heads, cache.head_dim), index),
             None if lse is None else _arg(lse, "lse", torch.float32, (rows, heads), index),
-            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel(),
-            _stream_of(stream, index))
-    if rc != 0:
-        raise SpecVerifyError(rc)
+            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 
 
 def spec_verify_status(workspace, stream=None) -> int:

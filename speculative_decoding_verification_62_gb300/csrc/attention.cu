@@ -1020,25 +1020,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicOr(P.status, (unsigned int)SV_STATUS_INTERNAL);
     return;
   }
-  // the requests' tiles, scanned; what else a CTA needs is set up meanwhile
-  unsigned int flags = 0;
-  const int chunk = (P.B + kThreads - 1) / kThreads;
-  const int b0 = tid * chunk < P.B ? tid * chunk : P.B;
-  const int b1 = b0 + chunk < P.B ? b0 + chunk : P.B;
-  Req r{0, 0, 0};  // the thread's last request: its only one up to 384 requests
-  int mine = 0;
+  // what needs no input is set up before the kernel ahead in the stream has ended
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&c->tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-#pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    r = request(P, b, flags);
-    mine += request_tiles(P, r);
-  }
-  if (tid == kThreads - 1) {
+  } else if (warp == 8 && lane < 4) {
+    const CUtensorMap* map = lane < 2 ? maps.q + lane : lane == 2 ? &maps.k : &maps.v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+  } else if (tid == kThreads - 1) {
     c->abort = 0;
     c->q_copied[0] = c->q_copied[1] = c->kv_copied[0] = c->kv_copied[1] = 0;
     for (int s = 0; s < 2; ++s) {
@@ -1053,6 +1044,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(smem_addr(&c->o_free[s]), 4);
       bar_init(smem_addr(&c->drain[s]), 1);
     }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the requests' tiles, scanned
+  unsigned int flags = 0;
+  const int chunk = (P.B + kThreads - 1) / kThreads;
+  const int b0 = tid * chunk < P.B ? tid * chunk : P.B;
+  const int b1 = b0 + chunk < P.B ? b0 + chunk : P.B;
+  Req r{0, 0, 0};  // the thread's last request: its only one up to 384 requests
+  int mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    r = request(P, b, flags);
+    mine += request_tiles(P, r);
   }
   int incl = mine;
 #pragma unroll
@@ -1407,23 +1411,25 @@ template <typename T, int DP>
 int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   const int grid = grid_size<T, DP>();
   if (grid <= 0) return SV_ERR_CUDA;
-  attention_kernel<T, DP><<<grid, kThreads, Shape<DP, false>::smem, stream>>>(m, P);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned int)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<DP, false>::smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  sv::overlap_launch(at[0]);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attention_kernel<T, DP>, m, P) != cudaSuccess) return SV_ERR_CUDA;
   // The launch itself overlaps the attention kernel, whose end the CTAs wait for.
   // A CTA a row where the shares are more than eight times the units.
   const bool many = 2ll * grid > 8ll * P.B * P.Hk;
   const long long rows = (long long)(P.G < P.T ? P.G + 1 : P.T) * P.Hq;
   const int per_cta = many ? 1 : 4 * (32 / (DP / 8));
   const long long y = (rows + per_cta - 1) / per_cta;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned int)P.B, (unsigned int)(y < 1024 ? y : 1024));
   cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, many ? combine_kernel<T, DP, true> : combine_kernel<T, DP, false>, P, grid) == cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;

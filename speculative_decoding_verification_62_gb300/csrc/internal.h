@@ -14,6 +14,13 @@ unsigned long long wait_limit_ns();
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Launches that may begin while the kernel before them in the stream ends; the
+// kernel waits for that one (griddepcontrol.wait) before it touches memory.
+inline void overlap_launch(cudaLaunchAttribute& a) {
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+}
+
 // The checks of a paged cache that the host can make.
 inline int check_cache(const sv_kv_cache& c) {
   if (c.dtype != SV_BF16 && c.dtype != SV_F16) return SV_ERR_SCALAR;

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
       }
     }
   };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   fetch(tid);
 
   if (tid < 32) {
@@ -289,8 +290,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
 template <typename T, int VW, bool INTER, int ROWS>
 int launch_rows(const AppendParams& P, cudaStream_t stream) {
   const unsigned int grid = (unsigned int)((P.T + ROWS - 1) / ROWS);
-  append_kernel<T, VW, INTER, ROWS><<<grid, kThreads, (size_t)ROWS * (P.rot / 2) * sizeof(float2), stream>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)ROWS * (P.rot / 2) * sizeof(float2);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  sv::overlap_launch(at[0]);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, append_kernel<T, VW, INTER, ROWS>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 template <typename T, int VW>

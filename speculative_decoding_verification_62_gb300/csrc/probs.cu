@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
   const int rank = C > 1 ? (int)cluster_rank() : 0;
   unsigned int flags = 0;
   if (C > 1) cluster_arrive();  // waited for before the first store to a peer
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // rows of this request
   int gb;
   size_t trow, drow;
@@ -456,13 +457,14 @@ int launch(ProbsParams P, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned int)P.B * (unsigned int)P.C);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
+  sv::overlap_launch(at[1]);
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned int)P.C;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, probs_kernel<EB, PK, VEC>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
