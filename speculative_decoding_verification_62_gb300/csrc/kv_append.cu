@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
       }
     }
   };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   fetch(tid);
 

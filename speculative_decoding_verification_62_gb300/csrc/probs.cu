@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
   const int rank = C > 1 ? (int)cluster_rank() : 0;
   unsigned int flags = 0;
   if (C > 1) cluster_arrive();  // waited for before the first store to a peer
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // rows of this request
   int gb;
