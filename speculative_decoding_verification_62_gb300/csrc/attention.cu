@@ -25,12 +25,12 @@
 // query tile in shared memory and 256 columns of tensor memory for S and O.
 // S = Q K^T and O += P V are tcgen05 products; P overwrites its S.
 // B reads keys from memory once and is bound by that: its streams are independent
-// (each with a copy warp and a ring of five 64-key slots), so that one stream's
+// (each with a copy warp and a ring of 64-key slots), so that one stream's
 // start and end of a unit hide behind the other's, and each has two score tiles,
 // so that the product of the next keys runs beside the softmax.
 // A is bound by the products: a product of 128 rows and 64 keys takes as long as
 // one of 128 keys, so its tiles have 128.  Each stream has one block of rows and
-// both read every key and value slot of one ring of five; one stream's softmax
+// both read every key and value slot of one ring; one stream's softmax
 // runs beside the other's products, and P goes over in halves.
 // Keys and values arrive by TMA, a page (at most 64 tokens) and 64 values a box,
 // with 128-byte swizzle; the layout of the page pool is only the tensor map's
@@ -74,7 +74,8 @@ struct Shape {
   static constexpr int q_half = kRows * 128;       // 64 values of every row
   static constexpr int tile_bytes = keys * DP * 2;
   static constexpr int half_bytes = keys * 128;
-  static constexpr int ring = 5 * kPairTile * DP * 2;
+  static constexpr int slots = DP == 64 ? 10 : 5;  // of a ring: A has one, B one a stream
+  static constexpr int ring = slots * kPairTile * DP * 2;
   static constexpr int smem = 2 * q_bytes + ring + kControl;
   static_assert(smem <= 227 * 1024, "shared memory");
 };
@@ -496,7 +497,7 @@ struct Walk {
 };
 
 struct Control {
-  uint64_t kv_full[10], kv_empty[10];
+  uint64_t kv_full[20], kv_empty[20];
   // of each stream
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], o_full[2], o_free[2], drain[2];
   uint32_t tmem;
@@ -507,17 +508,26 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kControl, "control block");
 
-// Barriers of a stream's ring entries (A: both streams', 0 to 4).
-template <bool PAIR>
-__device__ __forceinline__ uint32_t slot_of(int s, unsigned int e) {
-  return (PAIR ? 0u : s * 5u) + e % 5u;
-}
-__device__ __forceinline__ uint32_t turn_of(unsigned int e) {  // parity of the slot's use
-  return (e / 5u) & 1u;
-}
-// The order of a piece's tiles in the ring: keys one tile ahead of values.
-__device__ __forceinline__ int k_entry(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int v_entry(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+// A place in a ring of N slots.  A piece's tiles fill it as keys, values, keys, ..
+template <int N>
+struct Cursor {
+  uint32_t slot, turn;  // turn: parity of the slot's use
+  __device__ __forceinline__ void step(int k) {
+    slot += k;
+    if (slot >= (uint32_t)N) {
+      slot -= N;
+      turn ^= 1u;
+    }
+  }
+  __device__ __forceinline__ Cursor next() const {
+    Cursor c = *this;
+    c.step(1);
+    return c;
+  }
+  __device__ __forceinline__ Cursor previous() const {
+    return slot == 0 ? Cursor{(uint32_t)N - 1, turn ^ 1u} : Cursor{slot - 1, turn};
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Roles
@@ -535,28 +545,21 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
                                           const CUtensorMap* vmap) {
   using S = Shape<DP, PAIR>;
   const int lane = threadIdx.x & 31;
-  unsigned int flags = 0, base = 0, qn = 0, last = 0;
+  const int first = PAIR ? 0 : s * S::slots;  // slot of the ring's start
+  unsigned int flags = 0, qn = 0, copied = 0;
+  Cursor<S::slots> at{PAIR && s == 1 ? 1u : 0u, 0u};
   Piece p;
   bool ok = true;
 #pragma unroll 1
   while (ok && w.next(P, p)) {
     const int n = p.t1 - p.t0;
-    // a lane's page of tile i (a box is at most a page)
-    auto page_of = [&](int i) {
+    // a lane's page of tile i (a box is at most a page), as the table has it
+    const int32_t* table = p.prefix ? P.prefix_table : P.table + (size_t)p.b * P.max_pages;
+    auto look_up = [&](int i) {
       const int key = (p.t0 + i) * S::keys + lane * P.box_rows;
-      int id = 0;
-      if (lane * P.box_rows < S::keys && key < p.keys) {
-        id = __ldg(p.prefix ? P.prefix_table + (key >> P.page_shift)
-                            : P.table + (size_t)p.b * P.max_pages + (key >> P.page_shift));
-        if (id < 0 || id >= P.num_pages) {
-          flags |= SV_STATUS_BAD_PAGE;
-          id = P.num_pages;  // past the pool: the copy fills zeros
-        }
-      }
-      return id;
+      return i < n && lane * P.box_rows < S::keys && key < p.keys ? __ldg(table + (key >> P.page_shift)) : 0;
     };
-    // pages of the tile of the next entry and, in B, of the one before it
-    int at = 0, id = page_of(0), before = 0;
+    int ahead = look_up(0);
     if (!PAIR || s == 0) {
       // the block's query rows: [token][head of the group] in 128-byte rows
 #pragma unroll
@@ -575,42 +578,42 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
       ++qn;
     }
 #pragma unroll 1
-    for (int y = 0; ok && y < 2 * n; ++y) {
-      const bool is_v = y == 2 * n - 1 || (y > 0 && !(y & 1));
-      if (PAIR && is_v != (s == 1)) continue;
-      const int i = is_v ? (y == 2 * n - 1 ? n - 1 : y / 2 - 1) : (y + 1) / 2;
-      if (i > at) {
-        before = id;
-        id = page_of(i);
-        at = i;
+    for (int i = 0; ok && i < n; ++i) {
+      int id = ahead;
+      if (id < 0 || id >= P.num_pages) {
+        flags |= SV_STATUS_BAD_PAGE;
+        id = P.num_pages;  // past the pool: the copy fills zeros
       }
-      const int mine = i == at ? id : before;
-      const unsigned int e = base + y;
-      const uint32_t slot = slot_of<PAIR>(s, e);
-      int key = (p.t0 + i) * S::keys;
-      const int keys = p.keys - key < S::keys ? p.keys - key : S::keys;
-      const int boxes = (keys + P.box_rows - 1) / P.box_rows;
-      if (!(ok = warp_wait(&c->kv_empty[slot], turn_of(e) ^ 1, P, c))) break;
-      const uint32_t bar = smem_addr(&c->kv_full[slot]);
-      const CUtensorMap* map = is_v ? vmap : kmap;
-      uint32_t dst = ring + slot * S::tile_bytes;
-      if (elect_one()) bar_expect(bar, (uint32_t)(boxes * S::halves * 128 * P.box_rows));
+      ahead = look_up(i + 1);  // on its way while this tile's copies are issued
+      const int key0 = (p.t0 + i) * S::keys;
+      const int keys = p.keys - key0 < S::keys ? p.keys - key0 : S::keys;
 #pragma unroll 1
-      for (int x = 0; x < boxes; ++x, dst += P.box_rows * 128, key += P.box_rows) {
-        const int page = __shfl_sync(0xffffffffu, mine, x), in = key & (P.page_size - 1);
-        if (elect_one()) {
-          tma_load(dst, map, bar, 0, in, p.h, page);
-          if (S::halves == 2) tma_load(dst + S::half_bytes, map, bar, 64, in, p.h, page);
+      for (int v = PAIR ? s : 0; v < (PAIR ? s + 1 : 2); ++v) {  // keys, values
+        const uint32_t slot = first + at.slot;
+        if (!(ok = warp_wait(&c->kv_empty[slot], at.turn ^ 1, P, c))) break;
+        const uint32_t bar = smem_addr(&c->kv_full[slot]);
+        const CUtensorMap* map = v ? vmap : kmap;
+        uint32_t dst = ring + slot * S::tile_bytes;
+        if (elect_one()) bar_expect(bar, (uint32_t)(((keys + P.box_rows - 1) & -P.box_rows) * S::halves * 128));
+        int lane_of = 0;
+#pragma unroll 1
+        for (int x = 0; x < keys; x += P.box_rows, dst += P.box_rows * 128, ++lane_of) {
+          const int page = __shfl_sync(0xffffffffu, id, lane_of);
+          if (elect_one()) {
+            const int in = (key0 + x) & (P.page_size - 1);
+            tma_load(dst, map, bar, 0, in, p.h, page);
+            if (S::halves == 2) tma_load(dst + S::half_bytes, map, bar, 64, in, p.h, page);
+          }
         }
+        __syncwarp();
+        at.step(PAIR ? 2 : 1);
+        ++copied;
       }
-      __syncwarp();
-      last = e + 1;
     }
-    base += 2 * n;
   }
   if (lane == 0) {
     c->q_copied[s] = qn;
-    c->kv_copied[s] = last;
+    c->kv_copied[s] = copied;
   }
   const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && any) atomicOr(P.status, any);
@@ -628,37 +631,38 @@ __device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control
   constexpr uint32_t kPv = instr_desc(Type<T>::fmt, DP, true);
   constexpr int kAhead = PAIR ? 1 : 2;  // score tiles
   const uint32_t q = q_smem + s * S::q_bytes;
-  unsigned int base = 0, pieces = 0, tiles = 0;  // tiles: of the pieces so far
+  const int first = PAIR ? 0 : s * S::slots;  // slot of the ring's start
+  unsigned int pieces = 0, tk = 0, tv = 0;    // tiles of keys and of values so far
+  Cursor<S::slots> ck{0u, 0u}, cv{1u, 0u};
   Piece p;
   bool ok = true;
 #pragma unroll 1
   while (ok && w.next(P, p)) {
     const int n = p.t1 - p.t0;
     auto qk = [&](int i) {
-      const unsigned int e = base + k_entry(i), t = tiles + i;
-      const uint32_t slot = slot_of<PAIR>(s, e), buf = PAIR ? 0 : t & 1;
+      const uint32_t slot = first + ck.slot, buf = PAIR ? 0 : tk & 1;
       if (i == 0 && !(ok = wait(&c->q_full[s], pieces & 1))) return;
-      if (!(ok = wait(&c->kv_full[slot], turn_of(e)))) return;
-      {
-        const uint32_t b = ring + slot * S::tile_bytes;
+      if (!(ok = wait(&c->kv_full[slot], ck.turn))) return;
+      const uint32_t b = ring + slot * S::tile_bytes;
 #pragma unroll
-        for (int x = 0; x < S::halves; ++x)
-          mma_ss4(cols + buf * kTile, mat_desc(q + x * S::q_half, 16), mat_desc(b + x * S::half_bytes, 16), kQk, x > 0);
-        mma_commit(smem_addr(&c->s_full[s][buf]));  // (the softmax warps hand the keys' slot back)
-        if (i == n - 1) mma_commit(smem_addr(&c->q_empty[s]));
-      }
+      for (int x = 0; x < S::halves; ++x)
+        mma_ss4(cols + buf * kTile, mat_desc(q + x * S::q_half, 16), mat_desc(b + x * S::half_bytes, 16), kQk, x > 0);
+      mma_commit(smem_addr(&c->s_full[s][buf]));  // (the softmax warps hand the keys' slot back)
+      if (i == n - 1) mma_commit(smem_addr(&c->q_empty[s]));
+      ck.step(2);
+      ++tk;
     };
-    qk(0);
-    if (!PAIR && ok && n > 1) qk(1);
+    int ahead = 0;  // tiles whose scores are on their way
+#pragma unroll 1
+    for (; ok && ahead < kAhead && ahead < n; ++ahead) qk(ahead);
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
-      const unsigned int e = base + v_entry(i, n), t = tiles + i;
-      const uint32_t slot = slot_of<PAIR>(s, e);
+      const uint32_t slot = first + cv.slot, t = tv;
       if (i == 0 && pieces > 0 && !(ok = wait(&c->o_free[s], (pieces - 1) & 1))) break;
       int keys = p.keys - (p.t0 + i) * S::keys;
       keys = keys < S::keys ? keys : S::keys;
       const int steps = (keys + 15) / 16;
-      if (!(ok = wait(&c->kv_full[slot], turn_of(e)))) break;
+      if (!(ok = wait(&c->kv_full[slot], cv.turn))) break;
       const uint32_t d = cols + 2 * kTile;
       const uint64_t v = mat_desc(ring + slot * S::tile_bytes, S::half_bytes);
 #pragma unroll
@@ -681,10 +685,10 @@ __device__ __forceinline__ void matrix_role(const AttnParams& P, Walk w, Control
           }
         }
       }
+      cv.step(2);
+      ++tv;
       if (ok && i + kAhead < n) qk(i + kAhead);
     }
-    base += 2 * n;
-    tiles += n;
     ++pieces;
   }
 }
@@ -739,7 +743,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
   const float ninf = -INFINITY;
   const int tok = row / P.group, g = row - tok * P.group;
   using S = Shape<DP, PAIR>;
-  unsigned int tiles = 0, pieces = 0, base = 0;
+  const int first = PAIR ? 0 : s * S::slots;  // slot of the ring's start
+  unsigned int tiles = 0, pieces = 0;
+  Cursor<S::slots> at{0u, 0u};  // the tile's keys; its values come next
   Piece p;
   bool ok = true;
 #pragma unroll 1
@@ -774,8 +780,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       // came after it; in B its values' slot has been handed back (the slot's
       // next use cannot end before this tile's own product).
       if (!PAIR) {
-        const unsigned int e = base + v_entry(i - 1, n);
-        if (!(ok = warp_wait(&c->kv_empty[slot_of<PAIR>(s, e)], turn_of(e), P, c))) return;
+        const Cursor<S::slots> v = at.previous();
+        if (!(ok = warp_wait(&c->kv_empty[first + v.slot], v.turn, P, c))) return;
         fence_after();
       }
 #pragma unroll 1
@@ -794,10 +800,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
     // The value rows behind the last key of its 16 hold what memory held there, and
     // weights of 0 times NaN would be NaN: this warpgroup clears them before it
     // hands P over.  (In A both streams' write the same zeros.)
-    auto clear_tail = [&](int i, int keys) {
-      const unsigned int e = base + v_entry(i, n);
-      const uint32_t slot = slot_of<PAIR>(s, e);
-      if (!(ok = warp_wait(&c->kv_full[slot], turn_of(e), P, c))) return;
+    auto clear_tail = [&](int keys) {
+      const Cursor<S::slots> v = at.next();
+      const uint32_t slot = first + v.slot;
+      if (!(ok = warp_wait(&c->kv_full[slot], v.turn, P, c))) return;
       constexpr int kRow = S::halves * 8;  // 16-byte words of a row
 #pragma unroll 1
       for (int x = row; x < ((keys + 15) / 16 * 16 - keys) * kRow; x += 128) {
@@ -809,10 +815,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
     };
     const uint64_t sl2 = pair(P.sl2, P.sl2);
 #pragma unroll 1
-    for (int i = 0; i < n; ++i, ++tiles) {
+    for (int i = 0; i < n; ++i, ++tiles, at.step(2)) {
       const uint32_t buf = PAIR ? 0 : tiles & 1, s_col = s_cols + buf * kTile;
       if (!(ok = warp_wait(&c->s_full[s][buf], PAIR ? tiles & 1 : (tiles >> 1) & 1, P, c))) break;
-      if (threadIdx.x % 128 == 0) bar_arrive(smem_addr(&c->kv_empty[slot_of<PAIR>(s, base + k_entry(i))]));
+      if (threadIdx.x % 128 == 0) bar_arrive(smem_addr(&c->kv_empty[first + at.slot]));
       const int key0 = (p.t0 + i) * S::keys;
       const bool masked = key0 + S::keys > free;
       const int keys = p.keys - key0;
@@ -843,7 +849,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           const float neg = m == ninf ? 0.f : -m;
           sub = pair(neg, neg);
         }
-        if (tail) clear_tail(i, keys);
+        if (tail) clear_tail(keys);
         if (!ok) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -882,7 +888,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
           tmem_wait_store();
           fence_before();
         }
-        if (tail) clear_tail(i, keys);
+        if (tail) clear_tail(keys);
         if (!ok) break;
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&c->p_ready[s][buf]));
@@ -891,7 +897,6 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       unpair(pair_add(sum0, sum1), a, b);
       l += a + b;
     }
-    base += 2 * n;
     if (!ok) break;
     // the piece's rows, after its last product (a barrier of its own: parity
     // would not tell that product from the one two before it)
@@ -988,14 +993,16 @@ __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsig
         const unsigned int q = c->q_copied[PAIR ? 0 : x];
         if (q > 0 && (PAIR || x == s)) (void)bar_wait(smem_addr(&c->q_full[x]), (q - 1) & 1, kDrainNs, &ignored);
       }
-      // the last use of each slot that a copy was started for; in A the two
-      // warps' entries interleave: all up to the later one's last are waited
-      // for, an entry that was never started runs out
-      const unsigned int a = c->kv_copied[0], b = c->kv_copied[1];
-      const unsigned int end = PAIR ? (a > b ? a : b) : c->kv_copied[s];
+      // the copies started last, one a slot of the ring (A: every other entry is
+      // this warp's, in five slots of either ring size)
+      constexpr int kKept = PAIR ? 5 : S::slots;
+      const int first = PAIR ? 0 : s * S::slots, by = PAIR ? 2 : 1;
+      const int end = (int)c->kv_copied[s], from = end > kKept ? end - kKept : 0;
 #pragma unroll 1
-      for (unsigned int e = end > 5 ? end - 5 : 0; e < end; ++e)
-        (void)bar_wait(smem_addr(&c->kv_full[slot_of<PAIR>(s, e)]), turn_of(e), kDrainNs, &ignored);
+      for (int k = from; k < end; ++k) {
+        const int e = k * by + (PAIR ? s : 0);
+        (void)bar_wait(smem_addr(&c->kv_full[first + e % S::slots]), (e / S::slots) & 1, kDrainNs, &ignored);
+      }
     } else if (warp >= 8) {
       if (elect_one()) mma_commit(smem_addr(&c->drain[s]));
       __syncwarp();
@@ -1076,7 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const Plan L = make_plan(P, total, gridDim.x);
   const bool pair_cta = (int)blockIdx.x < L.ctas_a;
-  if (tid < 10) {
+  if (tid < 20) {
     bar_init(smem_addr(&c->kv_full[tid]), 1);
     bar_init(smem_addr(&c->kv_empty[tid]), pair_cta ? 2 : 1);
   }
