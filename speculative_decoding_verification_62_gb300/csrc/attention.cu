@@ -80,6 +80,31 @@ struct Shape {
   static_assert(smem <= 227 * 1024, "shared memory");
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: m = ceil(2^(31 + k) / d) with 2^k >= d
+// is off by less than 2^k / 2^(31 + k) of 1 / d, so n m / 2^(31 + k) exceeds n / d by
+// less than 1 / d.
+struct Divisor {
+  unsigned int d, k;
+  unsigned long long m;
+};
+inline Divisor divisor(int d) {
+  Divisor v{(unsigned int)d, 0u, 0ull};
+  while ((1ull << v.k) < (unsigned long long)d) ++v.k;
+  v.m = ((1ull << (31 + v.k)) + d - 1) / d;
+  return v;
+}
+__device__ __forceinline__ int divide(int n, const Divisor& v) {
+  return (int)(((unsigned long long)(unsigned int)n * v.m) >> (31 + v.k));
+}
+// n / d where the quotient is a small number (a share: at most 2 kMaxCtas): by a
+// rounded reciprocal and one correction.
+__device__ __forceinline__ int share_of(int n, int d, float inv) {
+  int q = (int)((float)n * inv);
+  const int r = n - q * d;
+  q += r < 0 ? -1 : r >= d ? 1 : 0;
+  return q;
+}
+
 struct AttnParams {
   int B, T, G, total, Hq, Hk, D, group, tpq, own_tok;
   int num_pages, page_size, page_shift, max_pages, box_rows;
@@ -87,6 +112,7 @@ struct AttnParams {
   const int32_t* kv_len;
   const int32_t* cu;
   const int32_t* prefix_table;
+  Divisor by_heads, by_group, by_tpq;        // Hq, group, tpq
   int prefix_len, prefix_tiles, pair_tiles;  // tiles of the prefix in list B and in list A
   int pairs, odd;                            // pairs of row blocks, and a single one
   const uint32_t* mask;
@@ -1186,18 +1212,21 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
   const Plan L = make_plan(P, P.starts[P.B], ctas);
   const int first = P.starts[b];
   if (L.per_b <= 0) return;
+  const float inv_a = 1.f / (float)(L.per_a > 0 ? L.per_a : 1), inv_b = 1.f / (float)L.per_b;
   // without a prefix, requests whose units all lie within one share are done
-  if (P.prefix_len == 0 && first / L.per_b == (first + request_tiles(P, r) - 1) / L.per_b) return;
+  if (P.prefix_len == 0 &&
+      share_of(first, L.per_b, inv_b) == share_of(first + request_tiles(P, r) - 1, L.per_b, inv_b))
+    return;
   const int rows = r.n * P.Hq;
   constexpr int kRowsCta = MANY ? 1 : 4 * kGroups;
   const int x0 = blockIdx.y * kRowsCta + (MANY ? 0 : warp * kGroups + group);
 #pragma unroll 1
   for (int x = x0; x - (MANY ? 0 : group) < rows; x += gridDim.y * kRowsCta) {
     const bool live = x < rows;
-    const int i = (live ? x : 0) / P.Hq, head = (live ? x : 0) - i * P.Hq;
-    const int h = head / P.group, g = head - h * P.group;
+    const int i = divide(live ? x : 0, P.by_heads), head = (live ? x : 0) - i * P.Hq;
+    const int h = divide(head, P.by_group), g = head - h * P.group;
     const size_t at = (size_t)(r.row0 + i) * P.Hq + head;
-    const int rb = i / P.tpq;
+    const int rb = divide(i, P.by_tpq);
     int u0 = first;
 #pragma unroll 1
     for (int y = 0; y < rb; ++y) u0 += tiles_of(block_keys(P, r, y)) * P.Hk;
@@ -1205,8 +1234,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     u0 += h * tiles;
     Unit own, pre;
     own.pair = false;
-    own.c0 = u0 / L.per_b;
-    own.count = (u0 + tiles - 1) / L.per_b - own.c0 + 1;
+    own.c0 = share_of(u0, L.per_b, inv_b);
+    own.count = share_of(u0 + tiles - 1, L.per_b, inv_b) - own.c0 + 1;
     own.slot_row = (i - rb * P.tpq) * P.group + g;
     own.stream = 0;
     pre = own;
@@ -1214,15 +1243,16 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     int blk = 0;
     if (P.prefix_len > 0) {
       const int t = r.row0 + i;
-      blk = t / P.tpq;
+      blk = divide(t, P.by_tpq);
       pre.pair = blk < 2 * P.pairs;
       pre.slot_row = (t - blk * P.tpq) * P.group + g;
       pre.stream = blk & 1;
       const int per = pre.pair ? L.per_a : L.per_b;
+      const float inv = pre.pair ? inv_a : inv_b;
       const int t_unit = pre.pair ? P.pair_tiles : P.prefix_tiles;
       const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * t_unit;
-      pre.c0 = v0 / per;
-      pre.count = (v0 + t_unit - 1) / per - pre.c0 + 1;
+      pre.c0 = share_of(v0, per, inv);
+      pre.count = share_of(v0 + t_unit - 1, per, inv) - pre.c0 + 1;
     }
     const bool done = P.prefix_len == 0 && own.count == 1;  // written already
     const int parts = live && !done ? pre.count + own.count : 0;
@@ -1248,7 +1278,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     float o[8], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int y = 0; y < 8; ++y) o[y] = 0.f;
-    constexpr int kAhead = 4, kStep = MANY ? 4 * kGroups : 1;
+    constexpr int kAhead = MANY ? 8 : 5, kStep = MANY ? 4 * kGroups : 1;
 #pragma unroll 1
     for (int k0 = MANY ? warp * kGroups + group : 0; k0 < parts; k0 += kAhead * kStep) {
       float v[kAhead][8], e[kAhead];
@@ -1487,6 +1517,9 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   P.D = c.head_dim;
   P.group = q_heads / c.kv_heads;
   P.tpq = kRows / P.group;
+  P.by_heads = divisor(P.Hq);
+  P.by_group = divisor(P.group);
+  P.by_tpq = divisor(P.tpq);
   P.own_tok = max_drafts < P.tpq ? max_drafts + 1 : P.tpq;
   P.num_pages = c.num_pages;
   P.page_size = c.page_size;
