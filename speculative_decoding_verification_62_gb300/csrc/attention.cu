@@ -170,16 +170,19 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // kernel's instructions have to stay in the cache.
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
                                            volatile int* abort) {
-  // ordinary waits end within these tries (a try suspends the warp for a while
-  // itself) and read no timer
+  // ordinary waits end within the first tries (a try suspends the warp for a while
+  // itself) and read no timer; a limit below 1 ms is looked at after every try
+  const int tries = wait_ns >= 1000000ull ? 64 : 1;
+  if (tries > 1) {
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i)
-    if (bar_try(bar, parity)) return true;
+    for (int i = 0; i < 256; ++i)
+      if (bar_try(bar, parity)) return true;
+  }
   const unsigned long long t0 = now_ns();
 #pragma unroll 1
   for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < tries; ++i)
       if (bar_try(bar, parity)) return true;
     if (*abort) return false;
     if (now_ns() - t0 > wait_ns) {
@@ -572,7 +575,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
   using S = Shape<DP, PAIR>;
   const int lane = threadIdx.x & 31;
   const int first = PAIR ? 0 : s * S::slots;  // slot of the ring's start
-  unsigned int flags = 0, qn = 0, copied = 0;
+  unsigned int flags = 0, qn = 0, copied = 0;  // query tiles of a stream, ring entries
   Cursor<S::slots> at{PAIR && s == 1 ? 1u : 0u, 0u};
   Piece p;
   bool ok = true;
@@ -600,6 +603,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
                      p.row0 + x * P.tpq);
         }
         __syncwarp();
+        if (lane == 0) c->q_copied[qs] = qn + 1;
       }
       ++qn;
     }
@@ -637,10 +641,7 @@ __device__ __forceinline__ void copy_role(const AttnParams& P, Walk w, Control* 
       }
     }
   }
-  if (lane == 0) {
-    c->q_copied[s] = qn;
-    c->kv_copied[s] = copied;
-  }
+  if (lane == 0) c->kv_copied[s] = copied;
   const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
   if (lane == 0 && any) atomicOr(P.status, any);
 }
@@ -1014,11 +1015,8 @@ __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsig
     // before shared and tensor memory are given back
     int ignored = 0;
     if (warp == 8 || warp == 10) {
-#pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        const unsigned int q = c->q_copied[PAIR ? 0 : x];
-        if (q > 0 && (PAIR || x == s)) (void)bar_wait(smem_addr(&c->q_full[x]), (q - 1) & 1, kDrainNs, &ignored);
-      }
+      if (c->q_copied[s] > 0)
+        (void)bar_wait(smem_addr(&c->q_full[s]), (c->q_copied[s] - 1) & 1, kDrainNs, &ignored);
       // the copies started last, one a slot of the ring (A: every other entry is
       // this warp's, in five slots of either ring size)
       constexpr int kKept = PAIR ? 5 : S::slots;

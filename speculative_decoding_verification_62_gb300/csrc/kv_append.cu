@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
       const int i = t - b - c0;
       RowInfo info{-1, -1};
       long long pos = 0;
-      if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 + P.B > P.T || i < 0 || i > c1 - c0) {
+      if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 > P.T - P.B || i < 0 || i > c1 - c0) {
         flags = SV_STATUS_BAD_GAMMA;
       } else {
         const long long slot = (long long)len + i;

@@ -116,6 +116,11 @@ CASES = {
     "split_long": ([20000], [3], 8, 1, 128, 64, "bf16", 0, "nhd"),
     "split_long_f16_64": ([9001, 17], [7, 2], 16, 2, 64, 16, "f16", 0, "nhd"),
     "many": ([(37 * b) % 400 for b in range(330)], [b % 4 for b in range(330)], 4, 2, 64, 16, "bf16", 0, "nhd"),
+    "more_requests_than_threads": ([(53 * b) % 300 for b in range(900)], [b % 3 for b in range(900)], 2, 1, 64, 32,
+                                   "f16", 0, "nhd"),
+    "more_requests_and_a_prefix": ([(53 * b) % 90 for b in range(401)], [b % 5 for b in range(401)], 8, 2, 128, 16,
+                                   "bf16", 200, "nhd"),
+    "long_among_short": ([30, 9000, 5, 0, 77], [1, 2, 0, 3, 4], 4, 4, 128, 64, "f16", 0, "nhd"),
     "prompt": ([0, 64], [399, 150], 4, 2, 128, 16, "bf16", 0, "nhd"),
     "prompt_group_3": ([5], [600], 3, 1, 64, 32, "f16", 0, "nhd"),
     "prefix_1": ([40, 0, 9], [2, 3, 0], 8, 2, 128, 16, "bf16", 1, "nhd"),
@@ -271,3 +276,36 @@ def test_a_dirty_workspace_and_a_larger_one():
     ws[:4] = 0
     out, _ = w.run(ws=ws)
     assert torch.equal(ref, out)
+
+
+def test_an_empty_batch_and_no_prefix_pages():
+    w = Batch([5], [0], 2, 1, 64, 16, "bf16", 0)
+    empty = binding.PagedCache(w.cache.k_pages, w.cache.v_pages, w.cache.page_table[:0],
+                               w.cache.kv_len[:0])
+    ws = binding.make_attention_workspace(1, 2, 64)
+    out = torch.full((0, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    binding.spec_verify_attention(w.q[:0], empty, w.cu[:1], 0, out, ws)
+    assert binding.spec_verify_status(ws) == 0
+
+
+def test_a_wait_that_runs_out_ends_the_call():
+    """With a limit of 1 ns a wait for a copy runs out: the call returns with the status
+    bit (or, where every copy was already there, complete), nothing hangs, and the next
+    call is right."""
+    import time
+    w = Batch([4000, 300, 9], [3, 0, 2], 8, 2, 128, 16, "bf16", 700)
+    ref, _ = w.run()
+    ws = binding.make_attention_workspace(w.T, w.Hq, w.D)
+    prev = binding.spec_verify_set_wait_limit(1)
+    try:
+        t0 = time.perf_counter()
+        w.run(ws=ws, status=None)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 20.0
+        bits = binding.spec_verify_status(ws)
+        assert set(binding.status_names(bits)) <= {"TIMEOUT"}
+        print("status", binding.status_names(bits))
+    finally:
+        binding.spec_verify_set_wait_limit(prev)
+    out, _ = w.run(ws=ws)
+    assert torch.equal(out, ref)
