@@ -63,8 +63,9 @@ constexpr int kMaxCtas = 160;   // CTAs at most (the slots of parts are sized fo
 constexpr int kSlots = 4 * kMaxCtas;  // parts: two a stream
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
 constexpr int kControl = 3072;  // barriers and small tables behind the tiles
-// Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs.
-constexpr int kCostA = 30, kCostB = 9;
+// Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs; and
+// of a unit's start and end, in tiles, which the lists count in front of its tiles.
+constexpr int kCostA = 30, kCostB = 9, kStartA = 3, kStartB = 1;
 
 template <int DP, bool PAIR>
 struct Shape {
@@ -120,7 +121,7 @@ struct AttnParams {
   char* out;
   float* lse;
   unsigned int* status;
-  int* starts;         // [B + 1]: first tile of each request in list B, and the list's end
+  int* starts;         // [B + 1]: where each request begins in list B, and the list's end
   // Parts: whole units over own keys as rows [T * Hq][DP]; whole prefix units by
   // block [Hk][blocks] and parts of units by slot [kSlots], both as [DP / 8][kRows][8]
   // (a warp's lanes have a row each: their stores are one run of memory)
@@ -414,24 +415,25 @@ __device__ __forceinline__ int block_keys(const AttnParams& P, const Req& r, int
   return r.kv + last;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
-// (the host refuses sizes whose lists could pass 2^30 tiles)
+// A request's length in list B: its units' tiles and starts.  (The host refuses sizes
+// whose lists could pass 2^30.)
 __device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) {
   if (r.n <= 0) return 0;
   int t = 0;
 #pragma unroll 1
-  for (int rb = 0; rb * P.tpq < r.n; ++rb) t += tiles_of(block_keys(P, r, rb));
+  for (int rb = 0; rb * P.tpq < r.n; ++rb) t += tiles_of(block_keys(P, r, rb)) + kStartB;
   return t * P.Hk;
 }
 
 // How the lists are dealt out.
 struct Plan {
-  int a, b;          // tiles of the lists
+  int a, b;          // lengths of the lists: tiles and starts
   int per_a, per_b;  // of a CTA's share of A, of a stream's share of B
   int ctas_a, ctas_b;
 };
 __device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int ctas) {
   Plan L;
-  L.a = P.Hk * P.pairs * P.pair_tiles;
+  L.a = P.Hk * P.pairs * (P.pair_tiles + kStartA);
   L.b = b_tiles;
   int na = 0;
   if (L.a > 0) {
@@ -446,8 +448,8 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int 
   L.per_b = L.ctas_b ? (L.b + 2 * L.ctas_b - 1) / (2 * L.ctas_b) : 0;
   return L;
 }
-// tiles of list B before the requests' own
-__device__ __forceinline__ int single_tiles(const AttnParams& P) { return P.Hk * P.odd * P.prefix_tiles; }
+// list B before the requests' own units
+__device__ __forceinline__ int single_tiles(const AttnParams& P) { return P.Hk * P.odd * (P.prefix_tiles + kStartB); }
 
 // A run of tiles of one unit.
 struct Piece {
@@ -467,7 +469,7 @@ struct Walk {
   bool pair, single;  // list A; the prefix's single block in list B
   int unit;           // prefix unit
   int b, rb, h;       // own unit
-  int off;            // first tile within the unit
+  int off;            // place within the unit: its start, then its tiles
   Req r;
 
   __device__ __forceinline__ void load_request(const AttnParams& P) {
@@ -507,10 +509,13 @@ struct Walk {
       p.keys = block_keys(P, r, rb);
       p.unit_t = tiles_of(p.keys);
     }
-    p.t0 = off;
-    p.t1 = left < p.unit_t - off ? off + left : p.unit_t;
-    left -= p.t1 - p.t0;
+    const int start = pair ? kStartA : kStartB, all = p.unit_t + start;
+    const int end = left < all - off ? off + left : all;
+    p.t0 = off > start ? off - start : 0;
+    p.t1 = end > start ? end - start : 0;
+    left -= end - off;
     off = 0;
+    if (p.t1 == p.t0) return false;  // the share ends in the unit's start
     if (p.prefix) {
       ++unit;
     } else if (++h == P.Hk) {
@@ -1129,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.unit = w.b = w.rb = w.h = w.off = 0;
       w.r = r;
       if (unit) {
-        const int t = pair_cta ? P.pair_tiles : P.prefix_tiles;
+        const int t = pair_cta ? P.pair_tiles + kStartA : P.prefix_tiles + kStartB;
         w.unit = g0 / t;
         w.off = g0 - w.unit * t;
       } else {
@@ -1144,7 +1149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (b1 - b0 > 1) w.r = request(P, w.b, ignored);
 #pragma unroll 1
         for (; w.rb * P.tpq < w.r.n; ++w.rb) {
-          const int t = tiles_of(block_keys(P, w.r, w.rb));
+          const int t = tiles_of(block_keys(P, w.r, w.rb)) + kStartB;
           if (rem < t * P.Hk) {
             w.h = rem / t;
             w.off = rem - w.h * t;
@@ -1227,9 +1232,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     const int rb = divide(i, P.by_tpq);
     int u0 = first;
 #pragma unroll 1
-    for (int y = 0; y < rb; ++y) u0 += tiles_of(block_keys(P, r, y)) * P.Hk;
+    for (int y = 0; y < rb; ++y) u0 += (tiles_of(block_keys(P, r, y)) + kStartB) * P.Hk;
     const int tiles = tiles_of(block_keys(P, r, rb));
-    u0 += h * tiles;
+    u0 += h * (tiles + kStartB) + kStartB;  // its first tile
     Unit own, pre;
     own.pair = false;
     own.c0 = share_of(u0, L.per_b, inv_b);
@@ -1248,7 +1253,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
       const int per = pre.pair ? L.per_a : L.per_b;
       const float inv = pre.pair ? inv_a : inv_b;
       const int t_unit = pre.pair ? P.pair_tiles : P.prefix_tiles;
-      const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * t_unit;
+      const int start = pre.pair ? kStartA : kStartB;
+      const int v0 = (pre.pair ? h * P.pairs + blk / 2 : h) * (t_unit + start) + start;
       pre.c0 = share_of(v0, per, inv);
       pre.count = share_of(v0 + t_unit - 1, per, inv) - pre.c0 + 1;
     }
@@ -1537,9 +1543,9 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
     P.odd = blocks & 1;
   }
   // tiles of the longest lists that the arguments allow, in 32 bits
-  const double reach = (double)c.max_pages * c.page_size / kTile + 1.0;
+  const double reach = (double)c.max_pages * c.page_size / kTile + 1.0 + kStartB;
   if (((double)rows / P.tpq + c.batch) * P.Hk * reach > (double)(1 << 30) ||
-      ((double)rows / P.tpq + 1.0) * P.Hk * P.prefix_tiles > (double)(1 << 30))
+      ((double)rows / P.tpq + 1.0) * P.Hk * ((double)P.prefix_tiles + kStartA) > (double)(1 << 30))
     return SV_ERR_SCALAR;
   P.mask = draft_mask;
   P.sl2 = scale * 1.44269504088896341f;
