@@ -65,7 +65,7 @@ constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits th
 constexpr int kControl = 3072;  // barriers and small tables behind the tiles
 // Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs; and
 // of a unit's start and end, in tiles, which the lists count in front of its tiles.
-constexpr int kCostA = 30, kCostB = 9, kStartA = 3, kStartB = 1;
+constexpr int kCostA = 40, kCostB = 9, kStartA = 3, kStartB = 1;
 
 template <int DP, bool PAIR>
 struct Shape {
@@ -97,8 +97,8 @@ inline Divisor divisor(int d) {
 __device__ __forceinline__ int divide(int n, const Divisor& v) {
   return (int)(((unsigned long long)(unsigned int)n * v.m) >> (31 + v.k));
 }
-// n / d where the quotient is a small number (a share: at most 2 kMaxCtas): by a
-// rounded reciprocal and one correction.
+// n / d where the quotient is a small number (a share: at most 2 kMaxCtas; a key
+// head: at most 65535): by a rounded reciprocal and one correction.
 __device__ __forceinline__ int share_of(int n, int d, float inv) {
   int q = (int)((float)n * inv);
   const int r = n - q * d;
@@ -167,9 +167,10 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 // Waits for a phase, at most wait_ns; false (and *abort set) when that ran out
-// or another warp of the CTA gave up.  The loop stands once in the code: the
-// kernel's instructions have to stay in the cache.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
+// or another warp of the CTA gave up.  Loops here and below are kept rolled: with
+// these waits unrolled the kernel had 304 KB of instructions and ran at half its
+// speed.  (Not a function of its own: registers are moved between warps.)
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, unsigned long long wait_ns,
                                            volatile int* abort) {
   // ordinary waits end within the first tries (a try suspends the warp for a while
   // itself) and read no timer; a limit below 1 ms is looked at after every try
@@ -1007,6 +1008,13 @@ __device__ __forceinline__ void run_roles(const AttnParams& P, Control* c, unsig
   const int s = warp < 8 ? warp >> 2 : (warp - 8) >> 1;
   const uint32_t q_smem = smem_addr(tiles), ring = q_smem + 2 * S::q_bytes;
   const Walk w = c->start[s];
+  // the launch's registers (384 threads x 168) where they are needed: 256 x 200 +
+  // 128 x 104 (a pair's 128 scores a thread: attn of 256 requests 257 -> 252 us; with
+  // 208 and 88 the copy and matrix warps spill: 301 us)
+  if (warp < 8)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp < 8)
     softmax_role<T, DP, PAIR>(P, w, c, s, 4 * blockIdx.x + (PAIR ? s : 2 * s), tiles + 2 * S::q_bytes);
   else if (!(warp & 1))
@@ -1151,7 +1159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; w.rb * P.tpq < w.r.n; ++w.rb) {
           const int t = tiles_of(block_keys(P, w.r, w.rb)) + kStartB;
           if (rem < t * P.Hk) {
-            w.h = rem / t;
+            w.h = share_of(rem, t, 1.f / (float)t);
             w.off = rem - w.h * t;
             break;
           }
