@@ -465,6 +465,7 @@ class PagedCache:
         B, width = page_table.shape
         _dev(kv_len, "kv_len", torch.int32, (B,))
         self.k_pages, self.v_pages, self.page_table, self.kv_len = k_pages, v_pages, page_table, kv_len
+        self.cu_shape = (B + 1,)
         self.batch, self.kv_heads, self.head_dim, self.dtype = B, heads, dim, k_pages.dtype
         self.page_size, self.scale = page, dim ** -0.5
         ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
@@ -494,10 +495,10 @@ def make_attention_workspace(total_rows: int, q_heads: int, head_dim: int,
     return ws
 
 
-def _heads(t, name, cache, rows, heads):
-    """Address and (row, head) strides of a [rows, heads, head_dim] view."""
+def _heads(t, name, cache, shape):
+    """Address and (row, head) strides of a [rows, heads, head_dim] view of that shape."""
     if (isinstance(t, torch.Tensor) and t.dtype is cache.dtype and t.get_device() == cache.index
-            and t.shape == (rows, heads, cache.head_dim)):
+            and t.shape == shape):
         row, head, one = t.stride()
         if one == 1:
             return t.data_ptr(), _two(row, head)
@@ -505,15 +506,15 @@ def _heads(t, name, cache, rows, heads):
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.index}")
     if t.dtype != cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
-    if tuple(t.shape) != (rows, heads, cache.head_dim):
-        raise ValueError(f"{name} must have shape {(rows, heads, cache.head_dim)}, got {tuple(t.shape)}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must have contiguous heads")
 
 
 def _cu_rows(cu_draft, cache, rows):
     if rows < cache.batch:
         raise ValueError(f"a step of {cache.batch} requests has at least as many rows, got {rows}")
-    return _arg(cu_draft, "cu_draft", torch.int32, (cache.batch + 1,), cache.index)
+    return _arg(cu_draft, "cu_draft", torch.int32, cache.cu_shape, cache.index)
 
 
 def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, workspace,
@@ -522,21 +523,22 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     """Append a step's keys and values to the paged cache and rotate its queries and keys;
     q and q_out may be None, freq (rope.fixed_point) None for no rotation.  See
     include/spec_verify.h."""
-    index = cache.index
+    index, dtype, dim = cache.index, cache.dtype, cache.head_dim
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     _index(k, "k")
     rows = k.shape[0]
     cu = _cu_rows(cu_draft, cache, rows)
-    kp, ks = _heads(k, "k", cache, rows, cache.kv_heads)
-    vp, vs = _heads(v, "v", cache, rows, cache.kv_heads)
+    kp, ks = _heads(k, "k", cache, (rows, cache.kv_heads, dim))
+    vp, vs = _heads(v, "v", cache, (rows, cache.kv_heads, dim))
     heads, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
         _index(q, "q")
         heads = q.shape[1]
-        qp, qs = _heads(q, "q", cache, rows, heads)
-        op, os_ = _heads(q_out, "q_out", cache, rows, heads)
-        if (rows > 1 and os_[0] < cache.head_dim) or (heads > 1 and os_[1] < cache.head_dim):
+        shape = (rows, heads, dim)
+        qp, qs = _heads(q, "q", cache, shape)
+        op, os_ = _heads(q_out, "q_out", cache, shape)
+        if (rows > 1 and os_[0] < dim) or (heads > 1 and os_[1] < dim):
             raise ValueError("q_out overlaps itself")
     rot, fp = 0, None
     if freq is not None:
@@ -557,20 +559,21 @@ def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix
     _index(q, "q")
     rows, heads = q.shape[0], q.shape[1]
     cu = _cu_rows(cu_draft, cache, rows)
-    qp, qs = _heads(q, "q", cache, rows, heads)
+    shape = (rows, heads, cache.head_dim)
+    qp, qs = _heads(q, "q", cache, shape)
     pt = mask = None
     if prefix_len > 0:
-        if prefix_table is None or prefix_table.numel() * cache.page_size < prefix_len:
+        if not isinstance(prefix_table, torch.Tensor) or prefix_table.numel() * cache.page_size < prefix_len:
             raise ValueError(f"prefix_table must hold {-(-prefix_len // cache.page_size)} pages")
         pt = _arg(prefix_table, "prefix_table", torch.int32, None, index)
     if draft_mask is not None:
-        if draft_mask.dtype not in (torch.int32, torch.uint32):
+        if getattr(draft_mask, "dtype", None) not in (torch.int32, torch.uint32):
             raise TypeError("draft_mask must be int32 or uint32 words")
         mask = _arg(draft_mask, "draft_mask", draft_mask.dtype, (rows,), index)
     _launch((_lib or load_library()).spec_verify_attention, index, stream,
             qp, qs, heads, cache.ref, pt, prefix_len, cu, rows - cache.batch, max_drafts,
             cache.scale if scale is None else scale, mask,
-            _arg(out, "out", cache.dtype, (rows, heads, cache.head_dim), index),
+            _arg(out, "out", cache.dtype, shape, index),
             None if lse is None else _arg(lse, "lse", torch.float32, (rows, heads), index),
             _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 

@@ -476,6 +476,7 @@ int verify_probs(const void* target, const void* draft, sv_dtype dtype, int B, i
   if (B < 0 || G < 0 || G > SV_MAX_GAMMA || V < 1 || V > SV_MAX_VOCAB || total < 0)
     return SV_ERR_SCALAR;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_SCALAR;
+  if (B == 0) return SV_OK;
   if (!target || !uniforms || !out || !accepted || !ws || (packed ? !cu : !gamma)) return SV_ERR_NULL;
   if ((packed ? total > 0 : G > 0) && !tokens) return SV_ERR_NULL;
   const size_t eb = dtype == SV_BF16 ? 2 : 4;
@@ -484,7 +485,6 @@ int verify_probs(const void* target, const void* draft, sv_dtype dtype, int B, i
       !sv::aligned(gamma, 4) || !sv::aligned(cu, 4) || !sv::aligned(uniforms, 4) ||
       !sv::aligned(out, 4) || !sv::aligned(accepted, 4) || !sv::aligned(ws, 256))
     return SV_ERR_ALIGN;
-  if (B == 0) return SV_OK;
   ProbsParams P;
   P.target = static_cast<const char*>(target);
   P.draft = static_cast<const char*>(draft);

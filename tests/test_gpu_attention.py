@@ -288,6 +288,29 @@ def test_an_empty_batch_and_no_prefix_pages():
     assert binding.spec_verify_status(ws) == 0
 
 
+def test_refused_tensors():
+    w = Batch([50, 60], [3, 1], 8, 2, 64, 16, "bf16", 40)
+    ws = binding.make_attention_workspace(w.T, 8, 64)
+    out = torch.empty((w.T, 8, 64), dtype=w.dtype, device="cuda")
+    call = binding.spec_verify_attention
+    with pytest.raises(TypeError):
+        call(w.q.half(), w.cache, w.cu, 3, out, ws)
+    with pytest.raises(TypeError):
+        call(w.q, w.cache, w.cu, 3, out, ws, draft_mask=torch.zeros(w.T, device="cuda"))
+    for kw in (dict(prefix_len=40), dict(prefix_table=w.prefix_table[:1], prefix_len=40),
+               dict(lse=torch.zeros((w.T, 4), device="cuda")), dict(draft_mask=torch.zeros(3, dtype=torch.int32).cuda())):
+        with pytest.raises(ValueError):
+            call(w.q, w.cache, w.cu, 3, out, ws, **kw)
+    for kw, code in ((dict(scale=0.0), -1), (dict(max_drafts=-1), -1), (dict(workspace=ws[:512]), -4)):
+        a = dict(max_drafts=3, workspace=ws)
+        a.update({k: v for k, v in kw.items() if k in a})
+        with pytest.raises(binding.SpecVerifyError) as e:
+            call(w.q, w.cache, w.cu, a["max_drafts"], out, a["workspace"], scale=kw.get("scale"))
+        assert e.value.code == code
+    with pytest.raises(binding.SpecVerifyError):  # heads of a query read 16 bytes at a time
+        call(torch.zeros((w.T, 8, 68), dtype=w.dtype, device="cuda")[..., :64], w.cache, w.cu, 3, out, ws)
+
+
 def test_a_wait_that_runs_out_ends_the_call():
     """With a limit of 1 ns a wait for a copy runs out: the call returns with the status
     bit (or, where every copy was already there, complete), nothing hangs, and the next

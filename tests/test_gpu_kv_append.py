@@ -210,3 +210,32 @@ def test_graph_replay_at_another_length():
     torch.cuda.synchronize()
     check(out, want[0], float(q.abs().max()), dtype)
     check(cache.k_pages, want[1], float(k.abs().max()), dtype)
+
+
+def test_refused_tensors():
+    lens, gam, dtype = [20, 3], [3, 5], torch.bfloat16
+    q, k, v, cu, cache, _ = setup(lens, gam, 4, 2, 64, 16, dtype, 9)
+    fx = rope.fixed_point(rope.frequencies(64)).cuda()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    out = torch.empty((10, 4, 64), dtype=dtype, device="cuda")
+    call = binding.spec_verify_kv_append
+    for args in ((q.half(), k, v, cache, cu, 5, fx, out, ws), (q, k, v, cache, cu.long(), 5, fx, out, ws),
+                 (q, k, v, cache, cu, 5, fx.int(), out, ws), (q, k.cpu(), v, cache, cu, 5, fx, out, ws)):
+        with pytest.raises(TypeError):
+            call(*args)
+    for args in ((q, k[:, :1], v, cache, cu, 5, fx, out, ws), (q, k, v, cache, cu, 5, fx, None, ws),
+                 (q, k, v, cache, cu, 5, fx, out[:1].expand(10, 4, 64), ws), (q, k, v, cache, cu[:2], 5, fx, out, ws),
+                 (q[:1], k[:1], v[:1], cache, cu, 5, fx, out[:1], ws)):
+        with pytest.raises(ValueError):
+            call(*args)
+    with pytest.raises(binding.SpecVerifyError):
+        call(q, k, v, cache, cu, -1, fx, out, ws)
+    pool = torch.zeros((4, 16, 2, 64), dtype=dtype, device="cuda")
+    table, n = torch.zeros((2, 4), dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for bad in ((pool[:, :15], pool[:, :15], table, n), (pool, pool[:2], table, n), (pool, pool, table[:1], n),
+                (pool, pool, table.long(), n), (pool[:1].expand(4, 16, 2, 64), pool, table, n),
+                (pool[..., :60], pool[..., :60], table, n)):
+        with pytest.raises((ValueError, TypeError)):
+            binding.PagedCache(*bad)
+    with pytest.raises(TypeError):
+        binding.PagedCache(pool.float(), pool.float(), table, n)

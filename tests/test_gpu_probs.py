@@ -209,6 +209,31 @@ def test_large_vocabulary_many_requests():
     assert (out.reshape(n, 4, 3) == ref).all() and (acc.reshape(n, 4) == ra).all()
 
 
+def test_no_requests_is_a_noop():
+    z = torch.zeros
+    ws = binding.make_workspace(1, 2, 50)
+    out, acc = z((0, 3), dtype=torch.int32, device="cuda"), z((0,), dtype=torch.int32, device="cuda")
+    binding.spec_verify_sample_probs(z((0, 3, 50), device="cuda"), z((0, 2, 50), device="cuda"),
+                                     z((0, 2), dtype=torch.int32, device="cuda"), acc.clone(),
+                                     z((0, 3), device="cuda"), out, acc, ws)
+    assert binding.spec_verify_status(ws) == 0
+
+
+def test_refused_tensors():
+    t, d, tok, gam, u = (x.cuda() for x in make(2, 2, 40, "f32", 1))
+    v = binding.Verifier(2, 2, 40)
+    for bad in (dict(t=t.half()), dict(d=d.bfloat16()), dict(u=u.double()), dict(tok=tok.long()), dict(u=u.cpu())):
+        a = dict(t=t, d=d, tok=tok, gam=gam, u=u)
+        a.update(bad)
+        with pytest.raises(TypeError):
+            v.sample_probs(a["t"], a["d"], a["tok"], a["gam"], a["u"])
+    for bad in (dict(t=t[:, :, ::2]), dict(d=d[:, :1]), dict(gam=gam[:1])):
+        a = dict(t=t, d=d, tok=tok, gam=gam, u=u)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            v.sample_probs(a["t"], a["d"], a["tok"], a["gam"], a["u"])
+
+
 def test_side_stream_and_graph():
     t, d, tok, gam, u = (x.cuda() for x in make(20, 3, 3000, "f32", 33, gamma="ragged"))
     v = binding.Verifier(20, 3, 3000)
