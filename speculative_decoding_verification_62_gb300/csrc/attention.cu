@@ -65,7 +65,7 @@ constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits th
 constexpr int kControl = 3072;  // barriers and small tables behind the tiles
 // Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs; and
 // of a unit's start and end, in tiles, which the lists count in front of its tiles.
-constexpr int kCostA = 40, kCostB = 9, kStartA = 3, kStartB = 1;
+constexpr int kCostA = 36, kCostB = 9, kStartA = 3, kStartB = 2;
 
 template <int DP, bool PAIR>
 struct Shape {
