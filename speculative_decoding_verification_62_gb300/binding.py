@@ -332,9 +332,9 @@ def spec_verify_greedy(target_logits, draft_tokens, gamma, out_tokens, num_accep
         raise SpecVerifyError(rc)
 
 
-# The calls below check their tensors in few Python steps, in line: a small batch's
-# kernel takes 4 to 10 us, less than a careless wrapper.  What does not pass goes
-# through _arg, which says what is wrong.
+# The calls below check their tensors in one expression: a small batch's kernel takes 4 to
+# 10 us, less than a careless wrapper.  What does not pass goes through _arg, tensor by
+# tensor, which says what is wrong.
 def _arg(t, name, dtype, shape, index):
     """Address of a contiguous tensor of that dtype and shape (None: any) on CUDA device `index`."""
     if isinstance(t, torch.Tensor):
@@ -376,47 +376,67 @@ def _two(a, b):
     return (ctypes.c_int64 * 2)(a, b)
 
 
+def _probs(target, draft, d_shape, first, f_name, f_shape, tokens, k_shape, uniforms,
+           u_shape, out, o_shape, accepted, B, workspace, index):
+    """Checks the tensors of the two calls below; the addresses of rows, and the type code."""
+    i32, dtype = torch.int32, target.dtype
+    try:
+        fine = (tokens.dtype is i32 and first.dtype is i32 and out.dtype is i32
+                and accepted.dtype is i32 and uniforms.dtype is torch.float32
+                and workspace.dtype is torch.uint8 and tokens.shape == k_shape
+                and first.shape == f_shape and out.shape == o_shape and accepted.shape == (B,)
+                and uniforms.shape == u_shape and target.is_contiguous() and tokens.is_contiguous()
+                and first.is_contiguous() and out.is_contiguous() and accepted.is_contiguous()
+                and uniforms.is_contiguous() and workspace.is_contiguous()
+                and tokens.get_device() == index and first.get_device() == index
+                and out.get_device() == index and accepted.get_device() == index
+                and uniforms.get_device() == index and workspace.get_device() == index)
+    except AttributeError:
+        fine = False
+    if not fine:
+        _arg(target, "target_probs", dtype, None, index)
+        _arg(first, f_name, i32, f_shape, index)
+        _arg(tokens, "draft_tokens", i32, k_shape, index)
+        _arg(uniforms, "uniforms", torch.float32, u_shape, index)
+        _arg(out, "out_tokens", i32, o_shape, index)
+        _arg(accepted, "num_accepted", i32, (B,), index)
+        _arg(workspace, "workspace", torch.uint8, None, index)
+    return (target.data_ptr(), None if draft is None else _arg(draft, "draft_probs", dtype, d_shape, index),
+            SV_F32 if dtype is torch.float32 else _dtype_code(target))
+
+
 def spec_verify_sample_probs(target_probs, draft_probs, draft_tokens, gamma, uniforms, out_tokens,
                              num_accepted, workspace, stream=None) -> None:
     """Sampling verify step on probabilities instead of logits; draft_probs None: the
     drafts were certain (looked up).  See include/spec_verify.h."""
     index = _index(target_probs, "target_probs")
-    dtype, i32 = target_probs.dtype, torch.int32
     B, G1, V = target_probs.shape
     G = G1 - 1
-    _launch((_lib or load_library()).spec_verify_sample_probs, index, stream,
-            _arg(target_probs, "target_probs", dtype, None, index),
-            None if draft_probs is None else _arg(draft_probs, "draft_probs", dtype, (B, G, V), index),
-            SV_F32 if dtype is torch.float32 else _dtype_code(target_probs), B, G, V,
-            _arg(draft_tokens, "draft_tokens", i32, (B, G), index),
-            _arg(gamma, "gamma", i32, (B,), index),
-            _arg(uniforms, "uniforms", torch.float32, (B, G1), index),
-            _arg(out_tokens, "out_tokens", i32, (B, G1), index),
-            _arg(num_accepted, "num_accepted", i32, (B,), index),
-            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
+    rows = (B, G1)
+    tp, dp, code = _probs(target_probs, draft_probs, (B, G, V), gamma, "gamma", (B,),
+                          draft_tokens, (B, G), uniforms, rows, out_tokens, rows, num_accepted, B,
+                          workspace, index)
+    _launch((_lib or load_library()).spec_verify_sample_probs, index, stream, tp, dp, code, B, G, V,
+            draft_tokens.data_ptr(), gamma.data_ptr(), uniforms.data_ptr(), out_tokens.data_ptr(),
+            num_accepted.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def spec_verify_sample_probs_packed(target_probs, draft_probs, cu_draft, draft_tokens, uniforms,
                                     out_tokens, num_accepted, workspace, stream=None) -> None:
     """spec_verify_sample_probs on the packed layout; see include/spec_verify.h."""
     index = _index(target_probs, "target_probs")
-    dtype, i32 = target_probs.dtype, torch.int32
     B = cu_draft.numel() - 1
     total = draft_tokens.numel()
     rows, V = target_probs.shape
     G = out_tokens.shape[1] - 1
     if rows != total + B:
         raise ValueError("target_probs must have total_drafts + B rows")
-    _launch((_lib or load_library()).spec_verify_sample_probs_packed, index, stream,
-            _arg(target_probs, "target_probs", dtype, None, index),
-            None if draft_probs is None else _arg(draft_probs, "draft_probs", dtype, (total, V), index),
-            SV_F32 if dtype is torch.float32 else _dtype_code(target_probs), B, G, V,
-            _arg(cu_draft, "cu_draft", i32, (B + 1,), index), total,
-            _arg(draft_tokens, "draft_tokens", i32, (total,), index),
-            _arg(uniforms, "uniforms", torch.float32, (rows,), index),
-            _arg(out_tokens, "out_tokens", i32, (B, G + 1), index),
-            _arg(num_accepted, "num_accepted", i32, (B,), index),
-            _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
+    tp, dp, code = _probs(target_probs, draft_probs, (total, V), cu_draft, "cu_draft", (B + 1,),
+                          draft_tokens, (total,), uniforms, (rows,), out_tokens, (B, G + 1),
+                          num_accepted, B, workspace, index)
+    _launch((_lib or load_library()).spec_verify_sample_probs_packed, index, stream, tp, dp, code, B,
+            G, V, cu_draft.data_ptr(), total, draft_tokens.data_ptr(), uniforms.data_ptr(),
+            out_tokens.data_ptr(), num_accepted.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 class PagedCache:
@@ -529,24 +549,32 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     _index(k, "k")
     rows = k.shape[0]
     cu = _cu_rows(cu_draft, cache, rows)
-    kp, ks = _heads(k, "k", cache, (rows, cache.kv_heads, dim))
-    vp, vs = _heads(v, "v", cache, (rows, cache.kv_heads, dim))
+    shape = (rows, cache.kv_heads, dim)
+    ks, vs = k.stride(), v.stride()
+    if not (k.shape == shape and v.shape == shape and k.dtype is dtype and v.dtype is dtype
+            and k.get_device() == index and v.get_device() == index and ks[2] == 1 and vs[2] == 1):
+        _heads(k, "k", cache, shape)
+        _heads(v, "v", cache, shape)
     heads, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
-        _index(q, "q")
         heads = q.shape[1]
         shape = (rows, heads, dim)
-        qp, qs = _heads(q, "q", cache, shape)
-        op, os_ = _heads(q_out, "q_out", cache, shape)
+        qs, os_ = q.stride(), q_out.stride()
+        if not (q.shape == shape and q_out.shape == shape and q.dtype is dtype and q_out.dtype is dtype
+                and q.get_device() == index and q_out.get_device() == index and qs[2] == 1
+                and os_[2] == 1):
+            _heads(q, "q", cache, shape)
+            _heads(q_out, "q_out", cache, shape)
         if (rows > 1 and os_[0] < dim) or (heads > 1 and os_[1] < dim):
             raise ValueError("q_out overlaps itself")
+        qp, qs, op, os_ = q.data_ptr(), _two(qs[0], qs[1]), q_out.data_ptr(), _two(os_[0], os_[1])
     rot, fp = 0, None
     if freq is not None:
         half = freq.numel()
         rot, fp = 2 * half, _arg(freq, "freq", torch.int64, (half,), index)
     _launch((_lib or load_library()).spec_verify_kv_append, index, stream,
-            qp, qs, heads, kp, ks, vp, vs, op, os_, cache.ref, cu, rows - cache.batch, max_drafts, fp,
-            rot, 1 if interleaved else 0, rope_scale,
+            qp, qs, heads, k.data_ptr(), _two(ks[0], ks[1]), v.data_ptr(), _two(vs[0], vs[1]), op, os_,
+            cache.ref, cu, rows - cache.batch, max_drafts, fp, rot, 1 if interleaved else 0, rope_scale,
             None if positions is None else _arg(positions, "positions", torch.int32, (rows,), index),
             position_offset, _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 
