@@ -337,7 +337,8 @@ size_t spec_verify_attention_workspace_size(int total_rows, int q_heads, int hea
  * other rows of the step too.  Requests with inconsistent cu_draft entries
  * (SV_STATUS_BAD_GAMMA) or lengths (SV_STATUS_BAD_LENGTH: kv_len[b] + gamma_b + 1
  * tokens past the page table) are skipped, their rows of out and lse left as they
- * were.  Scores, sums and parts are 32 bits; weights are rounded to the cache's
+ * were; entries that name the same rows so often that the step's list of keys passes
+ * 2^30 tiles leave out every request (SV_STATUS_BAD_GAMMA).  Scores, sums and parts are 32 bits; weights are rounded to the cache's
  * type for the product with the values.  Results repeat bit for bit.
  */
 int spec_verify_attention(const void *q, const int64_t *q_strides, int q_heads,

@@ -423,8 +423,14 @@ __device__ __forceinline__ int block_keys(const AttnParams& P, const Req& r, int
   return r.kv + last;
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
-// A request's length in list B: its units' tiles and starts.  (The host refuses sizes
-// whose lists could pass 2^30.)
+// The host refuses sizes whose lists could reach kMaxList where requests have rows of
+// their own; inconsistent cu_draft entries (0, n, 0, n, ..) name the same rows again and
+// again, so lengths are summed up to that and no further.
+constexpr int kMaxList = 1 << 30;
+__device__ __forceinline__ int list_add(int a, int b) {
+  return (int)min((unsigned int)a + (unsigned int)b, (unsigned int)kMaxList);
+}
+// A request's length in list B: its units' tiles and starts (below kMaxList).
 __device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) {
   if (r.n <= 0) return 0;
   int t = 0;
@@ -1107,23 +1113,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     r = request(P, b, flags);
-    mine += request_tiles(P, r);
+    mine = list_add(mine, request_tiles(P, r));
   }
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    if (lane >= o) incl = list_add(incl, v);
   }
   if (lane == 31) c->scan[warp] = incl;
   __syncthreads();
   const int singles = single_tiles(P);
-  int excl = singles + incl - mine, total = singles;
+  int excl = list_add(singles, incl - mine), total = singles;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
     const int v = c->scan[i];
-    if (i < warp) excl += v;
-    total += v;
+    if (i < warp) excl = list_add(excl, v);
+    total = list_add(total, v);
+  }
+  const bool over = total >= kMaxList;  // no request's rows are worked on
+  if (over) {
+    total = singles;
+    flags |= SV_STATUS_BAD_GAMMA;
   }
   const Plan L = make_plan(P, total, gridDim.x);
   const bool pair_cta = (int)blockIdx.x < L.ctas_a;
@@ -1179,14 +1190,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0) {
     int at = excl;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1 && !over; ++b) {
       P.starts[b] = at;
       if (b + 1 < b1) {
         unsigned int ignored = 0;
         at += request_tiles(P, request(P, b, ignored));
       }
     }
-    if (tid == 0) P.starts[P.B] = total;
+    if (tid == 0) P.starts[P.B] = over ? -1 : total;
     if (flags) atomicOr(P.status, flags);
   }
   fence_before();
@@ -1226,8 +1237,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
   unsigned int ignored = 0;
   const Req r = request(P, b, ignored);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's writes
-  if (r.n <= 0) return;
-  const Plan L = make_plan(P, P.starts[P.B], ctas);
+  const int list = P.starts[P.B];
+  if (r.n <= 0 || list < 0) return;
+  const Plan L = make_plan(P, list, ctas);
   const int first = P.starts[b];
   if (L.per_b <= 0) return;
   const float inv_a = 1.f / (float)(L.per_a > 0 ? L.per_a : 1), inv_b = 1.f / (float)L.per_b;
@@ -1557,10 +1569,11 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
     P.pairs = blocks / 2;
     P.odd = blocks & 1;
   }
-  // tiles of the longest lists that the arguments allow, in 32 bits
+  // the longest lists that the arguments allow (the prefix's single block stands in B)
   const double reach = (double)c.max_pages * c.page_size / kTile + 1.0 + kStartB;
-  if (((double)rows / P.tpq + c.batch) * P.Hk * reach > (double)(1 << 30) ||
-      ((double)rows / P.tpq + 1.0) * P.Hk * ((double)P.prefix_tiles + kStartA) > (double)(1 << 30))
+  const double prefix = P.Hk * ((double)P.prefix_tiles + kStartA);
+  if (((double)rows / P.tpq + c.batch) * P.Hk * reach + prefix >= (double)kMaxList ||
+      ((double)rows / P.tpq + 1.0) * prefix >= (double)kMaxList)
     return SV_ERR_SCALAR;
   P.mask = draft_mask;
   P.sl2 = scale * 1.44269504088896341f;

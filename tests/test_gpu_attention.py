@@ -237,6 +237,29 @@ def test_bad_requests_are_left_out():
     w.check(out, lse, only=[1, 2])
 
 
+def test_rows_named_again_and_again_are_left_out():
+    # entries 0, n, 0, n, ..: every other request is consistent by itself, together their
+    # keys pass any list (1000 requests of 157 blocks of half a million tiles)
+    B, n, page, width = 2000, 20000, 4096, 7000
+    pools = [torch.zeros((1, page, 1, 8), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    table = torch.zeros((B, width), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), page * width - n - 1, dtype=torch.int32, device="cuda")
+    cache = binding.PagedCache(*pools, table, lens)
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = n
+    q = torch.zeros((n + B, 1, 8), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((n + B, 1), 7.0, device="cuda")
+    ws = binding.make_attention_workspace(n + B, 1, 8)
+    binding.spec_verify_attention(q, cache, cu, n, out, ws, lse=lse)
+    assert binding.spec_verify_status(ws) == 1
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+    # the workspace serves the next call
+    few = binding.PagedCache(*pools, table[:1], lens[:1] * 0)
+    one = torch.empty((1, 1, 8), dtype=torch.bfloat16, device="cuda")
+    binding.spec_verify_attention(q[:1], few, cu[::2][:2].contiguous(), 0, one, ws)
+    assert not one.any()
+
+
 def test_two_workspaces_two_streams_and_graphs():
     a = Batch([3000, 20, 500], [3, 0, 2], 8, 2, 128, 16, "bf16", 300, seed=2)
     b = Batch([40, 2000], [1, 5], 6, 6, 64, 32, "f16", 0, seed=3)
