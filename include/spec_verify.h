@@ -317,7 +317,8 @@ size_t spec_verify_attention_workspace_size(int total_rows, int q_heads, int hea
  *                    head; query head h reads key head h / (q_heads / kv_heads)
  *   prefix_table     device int32, ceil(prefix_len / page_size) pages that every
  *                    request reads before its own, with prefix_len (HOST) tokens;
- *                    read once for the whole batch
+ *                    read once for the whole batch.  A prefix, and a request's own
+ *                    tokens with the step's, hold at most 2^31 - 4097 tokens
  *   draft_mask       optional device uint32 [total_drafts + batch], max_drafts <=
  *                    SV_MAX_GAMMA: bit j of a row's word says whether it sees row j of
  *                    its request's step (tree drafts), in place of j <= i; bits from

@@ -66,6 +66,7 @@ constexpr int kRows = 128;      // rows a block
 constexpr int kTile = 64;       // keys a tile of list B, and a box
 constexpr int kPairTile = 128;  // keys a tile of list A
 constexpr int kThreads = 384;   // warps 0-3, 4-7: softmax; 8, 10: copies; 9, 11: products
+constexpr int kMaxKeys = INT32_MAX - 4096;  // keys of a request: the last tile's places fit 32 bits
 constexpr int kMaxCtas = 160;   // CTAs at most (the slots of parts are sized for this)
 constexpr int kSlots = 4 * kMaxCtas;  // parts: two a stream
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
@@ -120,6 +121,7 @@ struct AttnParams {
   const int32_t* kv_len;
   const int32_t* cu;
   const int32_t* prefix_table;
+  int max_keys;  // of a request
   Divisor by_heads, by_group, by_tpq;        // Hq, group, tpq
   int prefix_len, prefix_tiles, pair_tiles;  // tiles of the prefix in list B and in list A
   int pairs, odd;                            // pairs of row blocks, and a single one
@@ -410,7 +412,7 @@ __device__ __forceinline__ Req request(const AttnParams& P, int b, unsigned int&
   Req r{0, 0, 0};
   if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 > P.total) {
     flags |= SV_STATUS_BAD_GAMMA;
-  } else if (kv < 0 || (long long)kv + (c1 - c0) + 1 > (long long)P.max_pages * P.page_size) {
+  } else if (kv < 0 || (long long)kv + (c1 - c0) + 1 > P.max_keys) {
     flags |= SV_STATUS_BAD_LENGTH;
   } else {
     r = Req{c0 + b, c1 - c0 + 1, kv};
@@ -1524,7 +1526,8 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   int rc = sv::check_cache(c);
   if (rc) return rc;
   const long long rows = (long long)total_drafts + c.batch;
-  if (total_drafts < 0 || max_drafts < 0 || rows > INT32_MAX || prefix_len < 0 || q_heads < 1 ||
+  if (total_drafts < 0 || max_drafts < 0 || rows > INT32_MAX || prefix_len < 0 ||
+      prefix_len > kMaxKeys || q_heads < 1 ||
       q_heads > 65535 || q_heads % c.kv_heads || q_heads / c.kv_heads > kRows || !(scale > 0.f) ||
       !std::isfinite(scale * 1.44269504f) || (draft_mask && max_drafts > SV_MAX_GAMMA))
     return SV_ERR_SCALAR;
@@ -1561,6 +1564,8 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
   P.kv_len = c.kv_len;
   P.cu = cu_draft;
   P.prefix_table = prefix_table;
+  const long long room = (long long)c.max_pages * c.page_size;
+  P.max_keys = room < kMaxKeys ? (int)room : kMaxKeys;
   P.prefix_len = prefix_len;
   P.prefix_tiles = (prefix_len + kTile - 1) / kTile;
   P.pair_tiles = (prefix_len + kPairTile - 1) / kPairTile;

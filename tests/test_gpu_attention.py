@@ -260,6 +260,30 @@ def test_rows_named_again_and_again_are_left_out():
     assert not one.any()
 
 
+def test_the_longest_request():
+    # 2^31 - 4097 keys, all in one page: every score 0, every value 0.5.  A stream's sum of
+    # weights (7 million) and of values stays below 2^24 half units: exact.
+    most, page = 2 ** 31 - 4097, 4096
+    k = torch.zeros((1, page, 1, 8), dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, 0.5)
+    table = torch.zeros((1, 2 ** 31 // page), dtype=torch.int32, device="cuda")
+    lens = torch.tensor([most - 1], dtype=torch.int32, device="cuda")
+    cache = binding.PagedCache(k, v, table, lens)
+    cu = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = torch.ones((1, 1, 8), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((1, 1), 7.0, device="cuda")
+    ws = binding.make_attention_workspace(1, 1, 8)
+    binding.spec_verify_attention(q, cache, cu, 0, out, ws, lse=lse)
+    assert binding.spec_verify_status(ws) == 0
+    assert bool((out == 0.5).all())
+    assert abs(float(lse) - math.log(most)) < 22 * 2.0 ** -22  # the join's and logarithm's roundings
+    out.fill_(7.0)
+    lens.add_(1)  # one more is refused
+    binding.spec_verify_attention(q, cache, cu, 0, out, ws, lse=lse)
+    assert binding.spec_verify_status(ws) == 512
+    assert bool((out == 7.0).all())
+
+
 def test_two_workspaces_two_streams_and_graphs():
     a = Batch([3000, 20, 500], [3, 0, 2], 8, 2, 128, 16, "bf16", 300, seed=2)
     b = Batch([40, 2000], [1, 5], 6, 6, 64, 32, "f16", 0, seed=3)

@@ -121,6 +121,13 @@ def test_attention_refusals():
     assert attention(cache(batch=0)) == 0
 
 
+def test_attention_refuses_prefixes_whose_places_pass_32_bits():
+    # the most goes on to the next check
+    for plen in (2 ** 31 - 4096, 2 ** 31 - 1):
+        assert attention(plen=plen) == -1
+    assert attention(plen=2 ** 31 - 4097, ws_bytes=0) == -4
+
+
 def test_attention_workspace_size():
     size = binding.load_library().spec_verify_attention_workspace_size
     assert size(1, 1, 8) > 0 and size(8, 4, 64) % 256 == 0
