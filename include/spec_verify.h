@@ -325,7 +325,8 @@ size_t spec_verify_attention_workspace_size(int total_rows, int q_heads, int hea
  *                    gamma_b + 1 on are ignored.  Tokens before the step are always
  *                    seen.
  *   scale            positive
- *   out              [total_drafts + batch][q_heads][head_dim], dense, 16-byte aligned
+ *   out              [total_drafts + batch][q_heads][head_dim], dense, 16-byte aligned;
+ *                    not within q's reach (SV_ERR_ALIGN)
  *   lse              optional float32 [total_drafts + batch][q_heads]: the natural log
  *                    of the sum of weights
  *   workspace        zero its first 4 bytes before the first use; the rest is

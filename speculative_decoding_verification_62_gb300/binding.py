@@ -582,7 +582,7 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
 def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix_table=None,
                           prefix_len=0, scale=None, draft_mask=None, lse=None, stream=None) -> None:
     """Attention of a step's rows over the paged cache (and a prefix that the batch shares);
-    scale None: head_dim ** -0.5.  See include/spec_verify.h."""
+    scale None: head_dim ** -0.5; out may not lie within q.  See include/spec_verify.h."""
     index = cache.index
     _index(q, "q")
     rows, heads = q.shape[0], q.shape[1]

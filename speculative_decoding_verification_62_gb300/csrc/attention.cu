@@ -1541,6 +1541,12 @@ int spec_verify_attention(const void* q, const int64_t* q_strides, int q_heads,
     return SV_ERR_ALIGN;
   const AttnLayout L = attn_layout(rows, q_heads, c.head_dim);
   if (ws_bytes < L.total) return SV_ERR_WORKSPACE;
+  // every row's output is written while other rows' queries may still be read
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q), oa = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t q_end = qa + 2 * ((uint64_t)(rows - 1) * (uint64_t)q_strides[0] +
+                                    (uint64_t)(q_heads - 1) * (uint64_t)q_strides[1] + (uint64_t)c.head_dim);
+  const uintptr_t o_end = oa + 2 * (uint64_t)rows * (uint64_t)q_heads * (uint64_t)c.head_dim;
+  if (qa < o_end && oa < q_end) return SV_ERR_ALIGN;
   AttnParams P = {};
   P.B = c.batch;
   P.T = (int)rows;

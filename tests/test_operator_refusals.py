@@ -128,6 +128,13 @@ def test_attention_refuses_prefixes_whose_places_pass_32_bits():
     assert attention(plen=2 ** 31 - 4097, ws_bytes=0) == -4
 
 
+def test_attention_refuses_an_output_within_the_queries():
+    # 8 rows of 4 heads of 64, 256 a row: 4096 bytes of q and of out; wider q rows reach further
+    for out in (0x100000, 0x100ff0, 0xff010):
+        assert attention(out=ptr(out)) == -3, hex(out)
+    assert attention(out=ptr(0x101000), qs=(ctypes.c_int64 * 2)(512, 64)) == -3
+
+
 def test_attention_workspace_size():
     size = binding.load_library().spec_verify_attention_workspace_size
     assert size(1, 1, 8) > 0 and size(8, 4, 64) % 256 == 0
