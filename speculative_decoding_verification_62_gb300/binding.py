@@ -446,9 +446,14 @@ class PagedCache:
     last dimension contiguous, the others of any stride that is a multiple of 8: a pool
     stored [page, head, token, value] is passed as its transpose(1, 2)), page_table
     [batch, max_pages] int32 and kv_len [batch] int32.  The tensors stay the caller's: they
-    are used in place, and kv_len is advanced by commit() alone.  Pages or rows of the
-    pools may not overlap one another.
+    are used in place (their contents may change between calls, the attributes may not be
+    assigned), and kv_len is advanced by commit() alone.  Pages or rows of the pools may
+    not overlap one another.
     """
+    k_pages = property(lambda self: self._tensors[0])
+    v_pages = property(lambda self: self._tensors[1])
+    page_table = property(lambda self: self._tensors[2])
+    kv_len = property(lambda self: self._tensors[3])
 
     def __init__(self, k_pages, v_pages, page_table, kv_len):
         self.index = _index(k_pages, "k_pages")
@@ -484,7 +489,7 @@ class PagedCache:
             raise ValueError("page_table must be a contiguous int32 [batch, max_pages]")
         B, width = page_table.shape
         _dev(kv_len, "kv_len", torch.int32, (B,))
-        self.k_pages, self.v_pages, self.page_table, self.kv_len = k_pages, v_pages, page_table, kv_len
+        self._tensors = (k_pages, v_pages, page_table, kv_len)
         self.cu_shape = (B + 1,)
         self.batch, self.kv_heads, self.head_dim, self.dtype = B, heads, dim, k_pages.dtype
         self.page_size, self.scale = page, dim ** -0.5

@@ -12,6 +12,18 @@ from speculative_decoding_verification_62_gb300 import binding, rope
 pytestmark = pytest.mark.gpu
 
 
+def test_a_cache_keeps_its_tensors():
+    pools = [torch.zeros((2, 16, 1, 8), dtype=torch.float16, device="cuda") for _ in range(2)]
+    table, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((3, 2), (3,)))
+    cache = binding.PagedCache(*pools, table, lens)
+    # the calls hold the addresses: another tensor takes another PagedCache
+    for name, t in (("k_pages", pools[1]), ("v_pages", pools[0]), ("page_table", table + 1), ("kv_len", lens + 1)):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, t)
+    cache.commit(torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"))
+    assert cache.kv_len is lens and lens.tolist() == [1, 2, 3]
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("prefix", [0, 75])
 def test_steps_against_the_whole_history(prefix, dtype):
