@@ -10,13 +10,19 @@
 // turns, grows to 2^-34 turns at position 2^31).  The turn goes to 32-bit
 // floats as a fraction in [-1/2, 1/2), and cos and sin are taken of that.
 //
-// Bound: q, k and v are read once and written once.  Few rows: latency (the
-// page look-up depends on the request look-up).  A CTA handles four rows (one
-// where there are few): their angles are formed once, in shared memory, and serve
-// every head.  A thread's first values are under way before the look-ups, and the
-// rows of a task are read together.  Measured (GB300): one row 3.6 us; 256 requests'
-// steps 9.2 us (29 MB, 3.1 TB/s); prompts of 12 requests, 24 + 6 + 6 heads of 96 in
-// fp16, 69.8 us (318 MB, 4.6 TB/s: 67 % of a copy; instruction issue 40 %).
+// Bound: q, k and v are read once and written once; a CTA's chain of look-ups
+// (request, length, page), angles and stores is hidden by its first values, which are
+// under way before the look-ups, and by the other CTAs of its SM.  The angles of a row
+// are formed once, in shared memory, and serve every head.  Hence many small CTAs:
+// - up to 608 rows (four CTAs an SM, one wave) a CTA of 256 threads a row;
+// - up to 2047 rows 128 threads a row, eight CTAs an SM, three reads a thread under
+//   way: 1174 rows 9.3 -> 7.4 us (256 threads -> 128), 618 rows 6.3 (two rows a CTA: 7.4),
+//   1920 rows 13.0 (14.0);
+// - from there two rows a CTA of 128 threads, twelve CTAs an SM: 23018 rows 59 us, one
+//   row a CTA of 128 threads 68, four rows 69, two rows of 256 threads 64.
+// Measured (GB300): one row 3.5 us; 256 requests' steps 7.4 us (29 MB, 3.9 TB/s);
+// prompts of 12 requests, 24 + 6 + 6 heads of 96 in fp16, 59.2 us (318 MB, 5.4 TB/s: 79 %
+// of a copy).
 #include "../../include/spec_verify.h"
 #include "internal.h"
 
@@ -25,8 +31,8 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kManyRows = 2048;  // from here on four rows a CTA
+constexpr int kFewRows = 608;    // up to here 256 threads a row
+constexpr int kManyRows = 2048;  // from here on two rows a CTA
 
 struct AppendParams {
   const char* q;
@@ -127,8 +133,9 @@ struct Words<1> {
   unsigned short x, y;
 };
 
-template <typename T, int VW, bool INTER, int ROWS>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
+template <typename T, int VW, bool INTER, int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : ROWS == 1 ? 8 : 12) append_kernel(AppendParams P) {
+  constexpr int kThreads = THREADS;
   extern __shared__ float2 s_turn[];  // [ROWS][rot / 2] cos, sin
   __shared__ RowInfo s_row[ROWS];
   __shared__ long long s_pos[ROWS];
@@ -140,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
   const int per_head = VW == 1 ? (P.D + 1) / 2 : P.D / (2 * VW);
   const int Hs = P.Hq + P.Hk;  // heads that turn
   const int n = (Hs + P.Hk) * per_head;
-  constexpr int kTasks = ROWS == 1 ? 2 : 1;  // under way together
+  constexpr int kTasks = ROWS > 1 ? 1 : THREADS == 256 ? 2 : 3;  // under way together
 
   // of a task: its head, the values that it moves (elements of the head)
   struct Task {
@@ -290,27 +297,31 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams P) {
   }
 }
 
-template <typename T, int VW, bool INTER, int ROWS>
+template <typename T, int VW, bool INTER, int ROWS, int THREADS>
 int launch_rows(const AppendParams& P, cudaStream_t stream) {
   const unsigned int grid = (unsigned int)((P.T + ROWS - 1) / ROWS);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = (size_t)ROWS * (P.rot / 2) * sizeof(float2);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   sv::overlap_launch(at[0]);
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<T, VW, INTER, ROWS>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, append_kernel<T, VW, INTER, ROWS, THREADS>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <typename T, int VW, bool INTER>
+int launch_order(const AppendParams& P, cudaStream_t stream) {
+  if (P.T <= kFewRows) return launch_rows<T, VW, INTER, 1, 256>(P, stream);
+  if (P.T < kManyRows) return launch_rows<T, VW, INTER, 1, 128>(P, stream);
+  return launch_rows<T, VW, INTER, 2, 128>(P, stream);
 }
 
 template <typename T, int VW>
 int launch(const AppendParams& P, bool inter, cudaStream_t stream) {
-  // four rows a CTA where one row each would be more than two waves of CTAs
-  if (P.T >= kManyRows)
-    return inter ? launch_rows<T, VW, true, 4>(P, stream) : launch_rows<T, VW, false, 4>(P, stream);
-  return inter ? launch_rows<T, VW, true, 1>(P, stream) : launch_rows<T, VW, false, 1>(P, stream);
+  return inter ? launch_order<T, VW, true>(P, stream) : launch_order<T, VW, false>(P, stream);
 }
 
 template <typename T>

@@ -105,6 +105,25 @@ def test_against_the_definition(case, fused):
     assert torch.equal(cache.v_pages.double(), want[2])
 
 
+@pytest.mark.parametrize("rows", [608, 609, 1217, 2047, 2048, 2049])
+@pytest.mark.parametrize("D, rot, inter", [(128, 128, False), (64, 32, True), (72, 20, False)])
+def test_around_the_borders_of_the_forms(rows, D, rot, inter):
+    # one long request among short ones, so that the last rows' requests differ
+    lens, gam = [5] * 25 + [70] + [31] * 25, [3] * 25 + [rows - 201] + [3] * 25
+    q, k, v, cu, cache, table = setup(lens, gam, 5, 1, D, 32, torch.bfloat16, 9)
+    assert q.shape[0] == rows
+    freq = rope.frequencies(rot, 10000.0)
+    want = expect(q, k, v, cu, cache, table, lens, gam, freq, inter)
+    q_out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    binding.spec_verify_kv_append(q, k, v, cache, cu, max(gam), rope.fixed_point(freq).cuda(), q_out, ws,
+                                  interleaved=inter)
+    assert binding.spec_verify_status(ws) == 0
+    check(q_out, want[0], float(q.abs().max()), torch.bfloat16)
+    check(cache.k_pages, want[1], float(k.abs().max()), torch.bfloat16)
+    assert torch.equal(cache.v_pages.double(), want[2])
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_unaligned_inputs_take_the_pair_path(inter):
     """q and k views that start 2 bytes off a 16-byte boundary."""
