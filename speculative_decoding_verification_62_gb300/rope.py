@@ -46,7 +46,7 @@ def frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", fact
             return n * math.log(trained_len / (2.0 * math.pi * turns)) / math.log(base)
 
         lo = max(math.floor(pair_of(beta_fast)), 0)
-        hi = min(math.ceil(pair_of(beta_slow)), n - 1)
+        hi = math.ceil(pair_of(beta_slow))  # behind the last pair where that one turns more often
         ramp = ((torch.arange(n, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         return f * (1.0 - ramp) + f / factor * ramp
     raise ValueError(f"unknown scaling {scaling!r}")

@@ -188,3 +188,23 @@ def test_frequencies():
     for bad in (torch.tensor([math.inf]), torch.ones(2, 2)):
         with pytest.raises(ValueError):
             rope.fixed_point(bad)
+
+
+@pytest.mark.parametrize("rot, base, factor, trained", [(128, 10000.0, 4.0, 131072), (64, 10000.0, 8.0, 131072),
+                                                         (128, 500000.0, 16.0, 1 << 23), (64, 10000.0, 8.0, 1 << 30),
+                                                         (128, 10000.0, 4.0, 4096), (32, 10000.0, 2.0, 40)])
+def test_by_parts_where_every_pair_turns_often(rot, base, factor, trained):
+    """Beyond trained_len = 2 pi base beta_slow the ramp ends behind the last pair: a pair
+    that turns more than beta_slow times is never divided by the whole factor."""
+    f0, f = rope.frequencies(rot, base), rope.frequencies(rot, base, "by_parts", factor, trained)
+    turns = f0 * trained / (2 * math.pi)
+    part = (1 - f / f0) / (1 - 1 / factor)  # the ramp: 0 stays, 1 takes the whole factor
+    assert bool((part[turns >= 32.0].abs() < 1e-12).all())
+    assert bool((part[turns > 1.0] < 1 - 1e-6).all())
+    assert bool(((part[turns <= 1.0] - 1).abs() < 1e-12).all())
+    # linear between the pairs (whole numbers) that turn at least 32 times and at most once
+    per_pair = math.log(base) * 2 / rot
+    lo = max(0, math.floor(math.log(trained / (2 * math.pi * 32.0)) / per_pair))
+    hi = math.ceil(math.log(trained / (2 * math.pi)) / per_pair)
+    for i in range(rot // 2):
+        assert math.isclose(part[i], min(max((i - lo) / (hi - lo), 0.0), 1.0), rel_tol=1e-9, abs_tol=1e-9)
