@@ -379,3 +379,24 @@ def test_a_wait_that_runs_out_ends_the_call():
         binding.spec_verify_set_wait_limit(prev)
     out, _ = w.run(ws=ws)
     assert torch.equal(out, ref)
+
+
+def test_the_wait_limit_ends_a_call_with_its_status():
+    """With a limit of 1 ns the first wait for a copy from memory runs out in every CTA:
+    the call ends with the status bit, and the next call is right."""
+    import time
+    w = Batch([4000, 300, 9], [3, 0, 2], 8, 2, 128, 16, "bf16", 700)
+    ref, _ = w.run()
+    ws = binding.make_attention_workspace(w.T, w.Hq, w.D)
+    for _ in range(3):
+        prev = binding.spec_verify_set_wait_limit(1)
+        try:
+            t0 = time.perf_counter()
+            w.run(ws=ws, status=None)
+            bits = binding.spec_verify_status(ws)
+            assert time.perf_counter() - t0 < 20.0
+        finally:
+            binding.spec_verify_set_wait_limit(prev)
+        assert binding.status_names(bits) == ["TIMEOUT"]
+        out, _ = w.run(ws=ws)
+        assert torch.equal(out, ref)
