@@ -324,7 +324,8 @@ size_t spec_verify_attention_workspace_size(int total_rows, int q_heads, int hea
  *                    its request's step (tree drafts), in place of j <= i; bits from
  *                    gamma_b + 1 on are ignored.  Tokens before the step are always
  *                    seen.
- *   scale            positive
+ *   scale            positive; a score scale q . k stays below 2^27 in magnitude (or is
+ *                    infinite)
  *   out              [total_drafts + batch][q_heads][head_dim], dense, 16-byte aligned;
  *                    not within q's reach (SV_ERR_ALIGN)
  *   lse              optional float32 [total_drafts + batch][q_heads]: the natural log
@@ -341,7 +342,8 @@ size_t spec_verify_attention_workspace_size(int total_rows, int q_heads, int hea
  * tokens past the page table) are skipped, their rows of out and lse left as they
  * were; entries that name the same rows so often that the step's list of keys passes
  * 2^30 tiles leave out every request (SV_STATUS_BAD_GAMMA).  Scores, sums and parts are 32 bits; weights are rounded to the cache's
- * type for the product with the values.  Results repeat bit for bit.
+ * type for the product with the values (half a step of each weight; in fp16, of a
+ * weight below 2^-21 of the largest, 2^-32 of the largest).  Results repeat bit for bit.
  */
 int spec_verify_attention(const void *q, const int64_t *q_strides, int q_heads,
                           const sv_kv_cache *cache, const int32_t *prefix_table, int prefix_len,

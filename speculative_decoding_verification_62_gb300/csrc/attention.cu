@@ -37,11 +37,16 @@
 // strides.
 //
 // S and the sums are 32 bits.  P is rounded to the cache's 16-bit type for the
-// product (at most half a step of a weight, below the rounding of the output's
-// own type where weights are spread); the sum of weights uses the unrounded
-// ones.  The running maximum moves only when it grows by more than 8 (a factor
-// of 256 in P, harmless in 32 bits and in the range of fp16), which makes the
-// rescaling of O rare.
+// product: each weight is off by at most half a step of that type, so the output by
+// at most what the rounding of an output of its magnitude takes (relative to the sum
+// of the weighted magnitudes of the values); the sum of weights uses the unrounded
+// ones.  m is the running maximum less a shift, and moves only when the maximum
+// has grown by more than 8 since (a factor of 256 in P), which makes the rescaling of O
+// rare.  The shift is 0 in bf16, whose weights have the range of 32 bits, and 7 in fp16:
+// weights then reach 2^15 (fp16 ends at 65504), the largest of a part is 2^7 at
+// least, and those below the normal numbers, 2^-14, are off by 2^-25: 2^-32 of the
+// largest each.  (Without the shift, weights below 2^-25 of the largest were lost: 65536
+// keys of 2^-25 each after one that is 1 are 0.16 % of an output.)
 //
 // Measured (GB300, with the join): one request's 131000 keys of 8 heads, 64 query heads
 // of 128, 97.8 us (537 MB, 5.5 TB/s; 88 us and 6.1 TB/s without the join); 256 requests
@@ -380,6 +385,7 @@ struct Type;
 template <>
 struct Type<__nv_bfloat16> {
   static constexpr uint32_t fmt = 1;
+  static constexpr float shift = 0.f;  // log2 of the largest weight where the maximum just moved
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&r);
@@ -388,6 +394,7 @@ struct Type<__nv_bfloat16> {
 template <>
 struct Type<__half> {
   static constexpr uint32_t fmt = 0;
+  static constexpr float shift = 7.f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     __half2 r = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&r);
@@ -814,14 +821,19 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
       word = P.mask[p.row0 + tok];
       if (p.keys - p.kv < 32) word &= (1u << (p.keys - p.kv)) - 1u;  // rows of the step
     }
-    float m = ninf, l = 0.f;  // running maximum (times scale log2 e) and sum
-    // Moves the maximum to the new scores' where that grows by more than 8.
-    auto settle = [&](int i, float top) {
+    float m = ninf, l = 0.f;  // running maximum (times scale log2 e) less the shift, and sum
+    // Moves the maximum to the new scores' (largest: `best`) where it has grown by more
+    // than 8.  It is rounded up, and the growth is the exponent that `best` gets below, so
+    // that no weight passes 2^(8 + shift), however large the scores are; the rounding lowers
+    // a row's weights by one step of the maximum at most (16 below 2^28, which fp16 bears).
+    auto settle = [&](int i, float best) {
+      const float top = __fmaf_ru(best, P.sl2, -Type<T>::shift);
       if (i == 0) {
         m = top;
         return;
       }
-      const bool grow = top > m + 8.f || (m == ninf && top > ninf);
+      // (also from -inf; not where both are infinite or one is NaN)
+      const bool grow = fmaf(best, P.sl2, -m) > 8.f + Type<T>::shift;
       if (!__any_sync(0xffffffffu, grow)) return;
       const float f = grow ? (m == ninf ? 0.f : exp2_fast(m - top)) : 1.f;
       // O is at rest once the last tile's product is done.  In A S of this tile
@@ -893,7 +905,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
               mx[ch] = max32(v + 32 * ch);
             }
           }
-          settle(i, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * P.sl2);
+          settle(i, max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]));
           const float neg = m == ninf ? 0.f : -m;
           sub = pair(neg, neg);
         }
@@ -926,7 +938,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& P, Walk w, Contro
             hide(v + 32, seen(key0 + 32, limit, by_word, word, p.kv));
             mx0 = max32(v), mx1 = max32(v + 32);
           }
-          settle(i, fmaxf(mx0, mx1) * P.sl2);
+          settle(i, fmaxf(mx0, mx1));
           if (!ok) break;
           const float neg = m == ninf ? 0.f : -m;
           const uint64_t sub = pair(neg, neg);

@@ -400,3 +400,99 @@ def test_the_wait_limit_ends_a_call_with_its_status():
         assert binding.status_names(bits) == ["TIMEOUT"]
         out, _ = w.run(ws=ws)
         assert torch.equal(out, ref)
+
+
+def sink_tolerance(o, lse, spread, size, keys, D, vmax, dtype):
+    """tolerance() without its term for narrow fp16 weights, and that term as the kernel's
+    shift leaves it: the largest weight of a part is 2^7 at least, so a weight below the
+    normal numbers, off by 2^-25, is off by 2^-32 of it."""
+    _, tl = tolerance(o, lse, spread, size, keys, D, vmax, dtype)
+    u, d = torch.finfo(dtype).eps / 2, tl - 2.0 ** -22 * (1.0 + lse.abs())
+    tol = (u + 2 * d[..., None]) * 1.01 * spread + u * 1.01 * o.abs() + 1e-30
+    if dtype == torch.float16:
+        tol = tol + keys * 2.0 ** -32 * vmax + 2.0 ** -25
+    return tol, tl
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D, group", [(64, 2), (128, 1)])
+@pytest.mark.parametrize("sink", [0, 40001, 65535])
+@pytest.mark.parametrize("shared", [False, True])
+def test_one_large_weight_before_many_small_ones(shared, sink, D, group, dtype):
+    """A key 17.5 above all others: each of the others weighs 2^-25 of it, all together 0.16
+    percent.  So many units that every one lies in one or two shares: 400 requests that
+    read the same pages, or 160 pairs of row blocks over a prefix."""
+    dt, page, L = DT[dtype], 64, 65536
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k = (torch.randn((L // page, page, 1, D), generator=g, device="cuda") * 0.05).to(dt)
+    v = (torch.randn((L // page, page, 1, D), generator=g, device="cuda") + 1.0).to(dt)
+    k[..., 0] = 0.0
+    at = sink // page, sink % page
+    k[at], v[at] = 0.0, 0.25
+    k[at][0, 0] = 17.5 * D ** 0.5
+    B = 160 * 2 * (128 // group) if shared else 400
+    pages = torch.arange(L // page, dtype=torch.int32, device="cuda")
+    if shared:  # a request has one key of its own: the first of the last page
+        table = torch.full((B, 1), L // page - 1, dtype=torch.int32, device="cuda")
+        cache = binding.PagedCache(k, v, table, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    else:
+        cache = binding.PagedCache(k, v, pages.expand(B, -1).contiguous(),
+                                   torch.full((B,), L - 1, dtype=torch.int32, device="cuda"))
+    q = torch.zeros((B, group, D), dtype=dt, device="cuda")
+    q[..., 0] = 1.0
+    q[..., 1] = torch.rand((B, group), generator=g, device="cuda").to(dt)
+    out, lse = torch.empty_like(q), torch.empty((B, group), device="cuda")
+    ws = binding.make_attention_workspace(B, group, D)
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    binding.spec_verify_attention(q, cache, cu, 0, out, ws, lse=lse, prefix_table=pages if shared else None,
+                                  prefix_len=L if shared else 0)
+    assert binding.spec_verify_status(ws) == 0
+    rows = torch.tensor([0, 1, B // 2, B - 1], device="cuda")
+    kk, vv = k.double().view(L, 1, D), v.double().view(L, 1, D)
+    if shared:
+        kk, vv = torch.cat([kk, kk[L - page:L - page + 1]]), torch.cat([vv, vv[L - page:L - page + 1]])
+    seen = torch.ones((4, kk.shape[0]), dtype=torch.bool, device="cuda")
+    o, l, spread, size = attend(q[rows].double(), kk, vv, seen, D ** -0.5)
+    tol, tl = sink_tolerance(o, l, spread, size, kk.shape[0], D, float(vv.abs().max()), dt)
+    err = (out[rows].double() - o).abs()
+    assert not (err > tol).any() and not torch.isnan(err).any(), float((err / tol).max())
+    assert not ((lse[rows].double() - l).abs() > tl).any()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("power", [16, 20, 24, 27])
+def test_scores_whose_own_rounding_is_large(power, dtype):
+    """Scores up to 2^power, rising along the keys in steps of 2^(power - 9) for three keys
+    each, whose scores differ by 0 or 1.  2^27 is what the call allows: the running maximum
+    (times log2 e, below 2^28) then has steps of 16 at most, and rounded up by less than one
+    step it leaves the largest weight, 2^7 less that, above 2^-9 and off by 2^-16 of itself at
+    most; with steps of 32 it would be lost in fp16.  The products are exact in 24 bits and the scale a power of two, so that the
+    weights of the keys around the largest score are good to their rounding all the same."""
+    w = Batch([1000, 700], [2, 1], 4, 2, 64, 16, dtype, 0, seed=power)
+    g = torch.Generator(device="cuda").manual_seed(power)
+    scale = 2.0 ** (power - 16)
+    for b in range(2):
+        n = w.k[b].shape[0]
+        t = torch.arange(n, device="cuda")
+        w.k[b].zero_()
+        w.k[b][:, :, 0] = 128.0 + (t // 3 % 64)[:, None]
+        w.k[b][:, :, 1] = 8.0 * (t // 192)[:, None]
+        if power <= 24:  # a 2^-8 is the last bit of the products
+            w.k[b][:, :, 2] = torch.randint(0, 2, (n, 2), generator=g, device="cuda").double() / scale
+        w.cache.k_pages[w.cache.page_table[b].long()[t // 16], t % 16] = w.k[b].to(w.dtype)
+    w.q.zero_()
+    w.q[:, :, 0], w.q[:, :, 1], w.q[:, :, 2] = 128.0, 1024.0, 1.0
+    out, lse = w.run(scale=scale)
+    u, row = torch.finfo(w.dtype).eps / 2, 0
+    for b, (n, x) in enumerate(zip(w.lens, w.gam)):
+        rows = slice(row, row + x + 1)
+        row += x + 1
+        seen = torch.arange(n + x + 1, device="cuda")[None, :] <= n + torch.arange(x + 1, device="cuda")[:, None]
+        o, l, spread, _ = attend(w.q[rows].double(), w.k[b], w.v[b], seen, scale)
+        assert 2.0 ** (power - 1) < float(l.min()) and float(l.max()) < 2.0 ** power
+        # scores that differ by 1 are off by 2^-22 of that, weights by 2^-17 as in
+        # tolerance(); what lies a step of 128 scale or more below has no weight
+        tol = (u + 2.0 ** -16 + (2.0 ** -15 if dtype == "f16" and power == 27 else 0)) * 1.01 * spread
+        tol = tol + u * 1.01 * o.abs() + 2.0 ** -25
+        assert not ((out[rows].double() - o).abs() > tol).any() and torch.isfinite(out[rows]).all()
+        assert not ((lse[rows].double() - l).abs() > 2.0 ** -21 * l.abs()).any()
