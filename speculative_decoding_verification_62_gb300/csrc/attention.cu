@@ -1423,8 +1423,7 @@ EncodeFn encoder() {
   void* f = found.load(std::memory_order_acquire);
   if (!f) {
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
+    if (sv::code_of(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q)) ||
         q != cudaDriverEntryPointSuccess)
       return nullptr;
     found.store(f, std::memory_order_release);
@@ -1477,12 +1476,12 @@ template <typename T, int DP>
 int grid_size() {
   static std::atomic<int> cached{0};
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (sv::code_of(cudaGetDevice(&dev))) return 0;
   const int c0 = cached.load(std::memory_order_relaxed);
   if ((c0 >> 16) == dev + 1) return c0 & 0xffff;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaFuncSetAttribute(attention_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Shape<DP, false>::smem) != cudaSuccess)
+  if (sv::code_of(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) ||
+      sv::code_of(cudaFuncSetAttribute(attention_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Shape<DP, false>::smem)))
     return 0;
   sms = sms < kMaxCtas ? sms : kMaxCtas;
   cached.store(((dev + 1) << 16) | sms, std::memory_order_relaxed);
@@ -1502,7 +1501,8 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   sv::overlap_launch(at[0]);
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attention_kernel<T, DP>, m, P) != cudaSuccess) return SV_ERR_CUDA;
+  const int rc = sv::code_of(cudaLaunchKernelEx(&cfg, attention_kernel<T, DP>, m, P));
+  if (rc) return rc;
   // The launch itself overlaps the attention kernel, whose end the CTAs wait for.
   // A CTA a row where the shares are more than eight times the units.
   const bool many = 2ll * grid > 8ll * P.B * P.Hk;
@@ -1512,9 +1512,8 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned int)P.B, (unsigned int)(y < 1024 ? y : 1024));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, many ? combine_kernel<T, DP, true> : combine_kernel<T, DP, false>, P, grid) == cudaSuccess
-             ? SV_OK
-             : SV_ERR_CUDA;
+  return sv::code_of(
+      cudaLaunchKernelEx(&cfg, many ? combine_kernel<T, DP, true> : combine_kernel<T, DP, false>, P, grid));
 }
 
 }  // namespace

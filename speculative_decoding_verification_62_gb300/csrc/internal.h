@@ -14,6 +14,14 @@ unsigned long long wait_limit_ns();
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// The code of a runtime call.  A failure is also kept by the runtime as this thread's
+// last error: it is cleared, so that no later call takes it for its own launch's.
+inline int code_of(cudaError_t e) {
+  if (e == cudaSuccess) return SV_OK;
+  (void)cudaGetLastError();
+  return SV_ERR_CUDA;
+}
+
 // Launches that may begin while the kernel before them in the stream ends; the
 // kernel waits for that one (griddepcontrol.wait) before it touches memory.
 inline void overlap_launch(cudaLaunchAttribute& a) {

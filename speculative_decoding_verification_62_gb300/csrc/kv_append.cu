@@ -309,7 +309,7 @@ int launch_rows(const AppendParams& P, cudaStream_t stream) {
   sv::overlap_launch(at[0]);
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<T, VW, INTER, ROWS, THREADS>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return sv::code_of(cudaLaunchKernelEx(&cfg, append_kernel<T, VW, INTER, ROWS, THREADS>, P));
 }
 
 template <typename T, int VW, bool INTER>

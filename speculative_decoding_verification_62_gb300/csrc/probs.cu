@@ -442,12 +442,12 @@ __global__ void __launch_bounds__(kThreads, 2) probs_kernel(ProbsParams P) {
 int cluster_for(int B) {
   static std::atomic<int> cached{0};
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (sv::code_of(cudaGetDevice(&dev))) return 0;
   const int c0 = cached.load(std::memory_order_relaxed);
   if ((c0 >> 16) == dev + 1) {
     sms = c0 & 0xffff;
   } else {
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (sv::code_of(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev))) return 0;
     cached.store(((dev + 1) << 16) | sms, std::memory_order_relaxed);
   }
   int C = kMaxCluster;
@@ -471,7 +471,7 @@ int launch(ProbsParams P, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, probs_kernel<EB, PK, VEC>, P) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return sv::code_of(cudaLaunchKernelEx(&cfg, probs_kernel<EB, PK, VEC>, P));
 }
 
 int verify_probs(const void* target, const void* draft, sv_dtype dtype, int B, int G, int V,

@@ -4297,8 +4297,7 @@ int launch_cluster(const Params& P, int C, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, cluster_kernel<EB, MODE, PK>, P) != cudaSuccess) return SV_ERR_CUDA;
-  return SV_OK;
+  return sv::code_of(cudaLaunchKernelEx(&cfg, cluster_kernel<EB, MODE, PK>, P));
 }
 
 struct Route {
@@ -4404,9 +4403,7 @@ int launch_stream(const Params& P, int C, int Q, cudaStream_t stream) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, stream_kernel<EB, MODE, PK, S::nw, S::nb, CPS>, P) != cudaSuccess)
-    return SV_ERR_CUDA;
-  return SV_OK;
+  return sv::code_of(cudaLaunchKernelEx(&cfg, stream_kernel<EB, MODE, PK, S::nw, S::nb, CPS>, P));
 }
 
 template <int EB, int MODE, bool PK>
@@ -4524,11 +4521,11 @@ namespace {
 
 int noalloc_scratch(void** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SV_ERR_CUDA;
+  if (sv::code_of(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return SV_ERR_CUDA;
   std::lock_guard<std::mutex> guard(g_noalloc_mu);
   if (!g_noalloc_ptr[dev]) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, sv_noalloc_scratch) != cudaSuccess || !p) return SV_ERR_CUDA;
+    if (sv::code_of(cudaGetSymbolAddress(&p, sv_noalloc_scratch)) || !p) return SV_ERR_CUDA;
     g_noalloc_ptr[dev] = p;
   }
   *out = g_noalloc_ptr[dev];
@@ -4677,7 +4674,7 @@ int spec_verify_sample_noalloc(const void* target_logits, const void* draft_logi
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // counters, arrival counts and decision records start at zero for every call
-  if (cudaMemsetAsync(ws, 0, L.stats, s) != cudaSuccess) return SV_ERR_CUDA;
+  if (sv::code_of(cudaMemsetAsync(ws, 0, L.stats, s))) return SV_ERR_CUDA;
   return dtype == SV_BF16 ? launch<2, MODE_SAMPLE, false>(P, s)
                           : launch<4, MODE_SAMPLE, false>(P, s);
 }
@@ -4686,11 +4683,9 @@ int spec_verify_status(void* workspace, sv_stream_t stream, uint32_t* status_hos
   if (!workspace || !status_host) return SV_ERR_NULL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // The status word sits at offset 0 of every workspace layout.
-  if (cudaMemcpyAsync(status_host, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost, s) !=
-      cudaSuccess)
-    return SV_ERR_CUDA;
-  if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s) != cudaSuccess) return SV_ERR_CUDA;
-  return cudaStreamSynchronize(s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  int rc = sv::code_of(cudaMemcpyAsync(status_host, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost, s));
+  if (!rc) rc = sv::code_of(cudaMemsetAsync(workspace, 0, sizeof(uint32_t), s));
+  return rc ? rc : sv::code_of(cudaStreamSynchronize(s));
 }
 
 const char* spec_verify_strerror(int code) {
