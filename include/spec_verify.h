@@ -274,9 +274,13 @@ typedef struct {
  * Appends a step's keys and values, and rotates its queries: row cu_draft[b] + b +
  * i (i <= gamma_b) of request b goes to token kv_len[b] + i.
  *   q            [total_drafts + batch][q_heads][head_dim], q_strides (HOST, row and
- *                head, elements); q_out likewise (q_out may be q; otherwise the two
- *                may not overlap).  q_heads 0: no queries, q and q_out may be NULL.
- *   k, v         [total_drafts + batch][kv_heads][head_dim] with k_strides, v_strides
+ *                head, elements); q_out likewise.  q_heads 0: no queries, q and q_out
+ *                may be NULL.  q_out may not overlap itself (SV_ERR_SCALAR), nor k, v
+ *                or, unless it is q with its strides, q (SV_ERR_ALIGN): their reaches
+ *                are apart, or they are slices of one tensor with one row stride (or
+ *                head stride), apart within it
+ *   k, v         [total_drafts + batch][kv_heads][head_dim] with k_strides, v_strides;
+ *                not within the slots that the call writes
  *   max_drafts   the largest gamma_b; any length (a prompt of n tokens is gamma_b =
  *                n - 1)
  *   freq         device int64 [rot_dim / 2]: pair j turns by freq[j] 2^-64 turns a

@@ -546,8 +546,8 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
                           interleaved=False, rope_scale=1.0, positions=None, position_offset=0,
                           stream=None) -> None:
     """Append a step's keys and values to the paged cache and rotate its queries and keys;
-    q and q_out may be None, freq (rope.fixed_point) None for no rotation.  See
-    include/spec_verify.h."""
+    q and q_out may be None, freq (rope.fixed_point) None for no rotation.  q_out is q
+    itself or overlaps none of q, k and v.  See include/spec_verify.h."""
     index, dtype, dim = cache.index, cache.dtype, cache.head_dim
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
@@ -570,7 +570,10 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
                 and os_[2] == 1):
             _heads(q, "q", cache, shape)
             _heads(q_out, "q_out", cache, shape)
-        if (rows > 1 and os_[0] < dim) or (heads > 1 and os_[1] < dim):
+        row, head = os_[0], os_[1]
+        if ((rows > 1 and row < dim) or (heads > 1 and head < dim)
+                or (rows > 1 and heads > 1 and row < (heads - 1) * head + dim
+                    and head < (rows - 1) * row + dim)):
             raise ValueError("q_out overlaps itself")
         qp, qs, op, os_ = q.data_ptr(), _two(qs[0], qs[1]), q_out.data_ptr(), _two(os_[0], os_[1])
     rot, fp = 0, None

@@ -331,6 +331,54 @@ int launch_width(const AppendParams& P, int vw, bool inter, cudaStream_t stream)
   return launch<T, 1>(P, inter, stream);
 }
 
+// ---------------------------------------------------------------------------
+// Host side: CTAs read and write their rows in no order, so q_out may not reach what
+// another row still reads, nor itself.
+// ---------------------------------------------------------------------------
+using Wide = __int128;  // offsets in bytes, at any stride
+Wide size_of(long long s) { return s < 0 ? -(Wide)s : (Wide)s; }
+
+// [n[0]][n[1]][dim] values of 2 bytes, strides in elements (dimension 0: rows, 1: heads)
+struct View {
+  Wide at;
+  long long n[2], stride[2];
+  int dim;
+  Wide inner(int d) const {  // bytes from the first to behind the last value along dimension d
+    return (Wide)(n[d] - 1) * size_of(stride[d]) * 2 + dim * 2;
+  }
+  Wide first(int d) const {  // the lowest address along dimension d
+    return at + (stride[d] < 0 ? (Wide)(n[d] - 1) * stride[d] * 2 : (Wide)0);
+  }
+};
+View view(const void* p, const int64_t* strides, long long rows, long long heads, int dim) {
+  return View{(Wide)reinterpret_cast<uintptr_t>(p), {rows, heads}, {strides[0], strides[1]}, dim};
+}
+bool overlaps_itself(const View& v) {
+  const int in = v.n[0] == 1 || (v.n[1] > 1 && size_of(v.stride[1]) <= size_of(v.stride[0])) ? 1 : 0;
+  const int out = 1 - in;
+  return (v.n[in] > 1 && size_of(v.stride[in]) < v.dim) ||
+         (v.n[out] > 1 && size_of(v.stride[out]) * 2 < v.inner(in));
+}
+// Whether two views are known to share no value: their reaches are apart, or they are
+// slices of one tensor (the q, k and v parts of a projection's rows): one stride along
+// rows or along heads, and windows within it that are apart.
+bool apart(const View& a, const View& b) {
+  auto low = [](const View& v) { return v.first(0) + v.first(1) - v.at; };
+  auto high = [&](const View& v) { return low(v) + v.inner(0) + v.inner(1) - v.dim * 2; };
+  if (high(a) <= low(b) || high(b) <= low(a)) return true;
+  for (int d = 0; d < 2; ++d) {
+    const Wide step = size_of(a.stride[d]) * 2;
+    if (a.stride[d] != b.stride[d] || a.inner(1 - d) > step || b.inner(1 - d) > step) continue;
+    const Wide by = ((b.first(1 - d) - a.first(1 - d)) % step + step) % step;
+    if (by >= a.inner(1 - d) && by + b.inner(1 - d) <= step) return true;
+  }
+  return false;
+}
+bool same(const View& a, const View& b) {
+  return a.at == b.at && (a.n[0] == 1 || a.stride[0] == b.stride[0]) &&
+         (a.n[1] == 1 || a.stride[1] == b.stride[1]);
+}
+
 }  // namespace
 
 extern "C" int spec_verify_kv_append(const void* q, const int64_t* q_strides, int q_heads,
@@ -358,6 +406,16 @@ extern "C" int spec_verify_kv_append(const void* q, const int64_t* q_strides, in
       !sv::aligned(workspace, 256))
     return SV_ERR_ALIGN;
   if (c.batch == 0) return SV_OK;
+  if (q_heads > 0) {
+    const long long rows = (long long)total_drafts + c.batch;
+    const View o = view(q_out, q_out_strides, rows, q_heads, c.head_dim);
+    const View in = view(q, q_strides, rows, q_heads, c.head_dim);
+    if (overlaps_itself(o)) return SV_ERR_SCALAR;
+    if ((!same(o, in) && !apart(o, in)) ||
+        !apart(o, view(k, k_strides, rows, c.kv_heads, c.head_dim)) ||
+        !apart(o, view(v, v_strides, rows, c.kv_heads, c.head_dim)))
+      return SV_ERR_ALIGN;
+  }
   AppendParams P = {};
   P.q = static_cast<const char*>(q);
   P.k = static_cast<const char*>(k);

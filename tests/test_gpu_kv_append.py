@@ -258,3 +258,35 @@ def test_refused_tensors():
             binding.PagedCache(*bad)
     with pytest.raises(TypeError):
         binding.PagedCache(pool.float(), pool.float(), table, n)
+
+
+@pytest.mark.parametrize("lens, gam", [([20, 3], [3, 5]), ([17], [0])])
+def test_queries_turned_in_place_beside_their_keys_and_values(lens, gam):
+    """q, k, v and q_out are slices of one projection's rows."""
+    freq = rope.frequencies(64)
+    fx, ws = rope.fixed_point(freq).cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for place in ("q", "beside", "heads"):
+        q, k, v, cu, cache, table = setup(lens, gam, 4, 2, 64, 16, torch.bfloat16, 12)
+        T = q.shape[0]
+        wide = torch.cat([q, k, v, torch.full_like(q, 9.0)], 1)
+        if place == "heads":  # stored [head, row, value]
+            wide = wide.transpose(0, 1).contiguous().transpose(0, 1)
+        before = wide.clone()
+        q, k, v = wide[:, :4], wide[:, 4:6], wide[:, 6:8]
+        out = q if place == "q" else wide[:, 8:]
+        want = expect(before[:, :4], before[:, 4:6], before[:, 6:8], cu, cache, table, lens, gam, freq, False)
+        binding.spec_verify_kv_append(q, k, v, cache, cu, max(gam), fx, out, ws)
+        check(out, want[0], float(q.abs().max()), torch.bfloat16)
+        check(cache.k_pages, want[1], float(k.abs().max()), torch.bfloat16)
+        assert torch.equal(cache.v_pages.double(), want[2])
+        keep = slice(4, 8) if place == "q" else slice(0, 8)
+        assert torch.equal(wide[:, keep], before[:, keep]) and binding.spec_verify_status(ws) == 0
+        # a slice that reaches into the keys, or the queries one head on
+        for bad in ([wide[:, 2:6], wide[:, 5:9], wide[:, 1:5]] if T > 1 else [wide[:, 2:6], wide[:, 1:5]]):
+            with pytest.raises(binding.SpecVerifyError) as e:
+                binding.spec_verify_kv_append(q, k, v, cache, cu, max(gam), fx, bad, ws)
+            assert e.value.code == -3
+        twice = torch.zeros((T + 3) * 64, dtype=torch.bfloat16, device="cuda").as_strided((T, 4, 64), (64, 64, 1))
+        if T > 1:
+            with pytest.raises(ValueError):
+                binding.spec_verify_kv_append(q, k, v, cache, cu, max(gam), fx, twice, ws)

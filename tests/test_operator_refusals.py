@@ -208,3 +208,26 @@ def test_by_parts_where_every_pair_turns_often(rot, base, factor, trained):
     hi = math.ceil(math.log(trained / (2 * math.pi)) / per_pair)
     for i in range(rot // 2):
         assert math.isclose(part[i], min(max((i - lo) / (hi - lo), 0.0), 1.0), rel_tol=1e-9, abs_tol=1e-9)
+
+
+def test_append_refuses_a_q_out_within_its_inputs():
+    """8 rows of 4 heads of 64 (k and v: 2 heads); all of these calls end on the host."""
+    def two(*s):
+        return (ctypes.c_int64 * 2)(*s)
+    # rows of 8 heads: q, k, v at 0, 512 and 768 bytes
+    fused = dict(q=ptr(0x100000), qs=two(512, 64), k=ptr(0x100200), ks=two(512, 64), v=ptr(0x100300), vs=two(512, 64))
+    far = dict(q=ptr(0x500000), qs=two(256, 64), k=ptr(0x600000), ks=two(128, 64), v=ptr(0x700000), vs=two(128, 64))
+    # q_out on itself: row 0's head 1 is row 1's head 0; heads or rows closer than a head
+    for s in (two(64, 64), two(192, 64), two(256, 32), two(32, 256), two(0, 64), two(256, 0), two(64, 448),
+              two(-64, 64), two(-192, 64)):
+        assert append(**far, o=ptr(0x800000), os=s) == -1, tuple(s)
+    # within q, shifted or with other strides
+    for base, at, s in ((fused, 0x100002, two(512, 64)), (fused, 0x100080, two(512, 64)), (fused, 0x100000, two(256, 64)),
+                        (far, 0x500080, two(256, 64)), (far, 0x500000, two(512, 64)), (far, 0x4ff800, two(256, 64)),
+                        (far, 0x500e00, two(-256, 64)), (far, 0x500000, two(64, 512))):
+        assert append(**base, o=ptr(at), os=s) == -3, (hex(at), tuple(s))
+    # within k or v: a window of the rows that reaches into theirs (also around the row's end)
+    for at in (0x100100, 0x100180, 0x100200, 0x100280, 0x100300, 0x100380):
+        assert append(**fused, o=ptr(at), os=two(512, 64)) == -3, hex(at)
+    for at in (0x600000, 0x6003f0, 0x5ffe02, 0x700000):
+        assert append(**far, o=ptr(at), os=two(256, 64)) == -3, hex(at)
