@@ -448,7 +448,9 @@ __device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) 
   return t * P.Hk;
 }
 
-// How the lists are dealt out.
+// How the lists are dealt out.  Both kernels work it out, in whole numbers: a sum of floats
+// may be contracted one way in one and another way in the other, and the join would then
+// look for a part in a place next to its own (lists past 2^24 tiles).
 struct Plan {
   int a, b;          // lengths of the lists: tiles and starts
   int per_a, per_b;  // of a CTA's share of A, of a stream's share of B
@@ -460,8 +462,8 @@ __device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int 
   L.b = b_tiles;
   int na = 0;
   if (L.a > 0) {
-    const float wa = (float)L.a * kCostA, wb = (float)L.b * kCostB;
-    na = (int)(ctas * (wa / (wa + wb)) + 0.5f);
+    const unsigned long long wa = (unsigned long long)L.a * kCostA, all = wa + (unsigned long long)L.b * kCostB;
+    na = (int)((2 * ctas * wa + all) / (2 * all));  // rounded to the nearest
     na = na < 1 ? 1 : na;
     if (L.b > 0 && na > ctas - 1) na = ctas - 1;
   }

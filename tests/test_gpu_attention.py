@@ -496,3 +496,24 @@ def test_scores_whose_own_rounding_is_large(power, dtype):
         tol = tol + u * 1.01 * o.abs() + 2.0 ** -25
         assert not ((out[rows].double() - o).abs() > tol).any() and torch.isfinite(out[rows]).all()
         assert not ((lse[rows].double() - l).abs() > 2.0 ** -21 * l.abs()).any()
+
+
+def test_long_lists_at_a_border_of_their_shares():
+    """380 blocks of requests behind 6.5 million shared tokens, 27648 tokens each: lists of
+    9.7 and 21.1 million tiles, whose share of the CTAs lies within a rounding of 32 bits of
+    98.5 of 152.  All keys stand in one page, every score is 0 and every value 0.5; the log
+    of the sum of weights counts the keys that the join found."""
+    page, B, own, prefix = 4096, 380 * 128, 432 * 64, 51136 * 128
+    k = torch.zeros((1, page, 1, 8), dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, 0.5)
+    cache = binding.PagedCache(k, v, torch.zeros((B, -(-own // page)), dtype=torch.int32, device="cuda"),
+                               torch.full((B,), own - 1, dtype=torch.int32, device="cuda"))
+    q = torch.zeros((B, 1, 8), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((B, 1), 7.0, device="cuda")
+    ws = binding.make_attention_workspace(B, 1, 8)
+    binding.spec_verify_attention(q, cache, torch.zeros(B + 1, dtype=torch.int32, device="cuda"), 0, out, ws, lse=lse,
+                                  prefix_table=torch.zeros(prefix // page, dtype=torch.int32, device="cuda"),
+                                  prefix_len=prefix)
+    assert binding.spec_verify_status(ws) == 0
+    assert bool((out == 0.5).all())
+    assert float((lse.double() - math.log(prefix + own)).abs().max()) < 20 * 2.0 ** -22
