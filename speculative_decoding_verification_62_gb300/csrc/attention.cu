@@ -439,13 +439,39 @@ constexpr int kMaxList = 1 << 30;
 __device__ __forceinline__ int list_add(int a, int b) {
   return (int)min((unsigned int)a + (unsigned int)b, (unsigned int)kMaxList);
 }
+// Of a key head, the tiles and starts of a request's first `blocks` row blocks, none of
+// them its last: the sum over i of ceil((kv + (i + 1) tpq) / 64).  A sum of n terms
+// floor((a i + b) / m) is its whole parts, n (n - 1) / 2 times a / m and n times b / m,
+// and what is left counts the whole numbers below a line, which are the same counted by
+// rows: n' = (a n + b) / m terms with a and m exchanged, Euclid's steps on (tpq, 64).
+// One or two for groups of 1, 2, 4, 8 heads, eight at most.  The sum is below kMaxList, so is every
+// product.  (With a loop over the blocks the join of a prompt's rows was quadratic.)
+__device__ __forceinline__ int blocks_before(const AttnParams& P, const Req& r, int blocks) {
+  if (blocks == 0) return 0;
+  if (P.mask) return blocks * (tiles_of(r.kv + r.n) + kStartB);  // a word may name any row
+  unsigned int n = blocks, a = P.tpq, b = (unsigned int)r.kv + P.tpq + kTile - 1, m = kTile, sum = 0;
+#pragma unroll 1
+  for (;;) {
+    const unsigned int qa = a / m, qb = b / m;
+    if (qa > 0) sum += (n & 1 ? n * ((n - 1) / 2) : (n / 2) * (n - 1)) * qa;
+    sum += n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const unsigned int top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top - n * m;
+    const unsigned int t = a;
+    a = m;
+    m = t;
+  }
+  return (int)sum + blocks * kStartB;
+}
 // A request's length in list B: its units' tiles and starts (below kMaxList).
 __device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) {
   if (r.n <= 0) return 0;
-  int t = 0;
-#pragma unroll 1
-  for (int rb = 0; rb * P.tpq < r.n; ++rb) t += tiles_of(block_keys(P, r, rb)) + kStartB;
-  return t * P.Hk;
+  const int last = r.n <= P.tpq ? 0 : (r.n - 1) / P.tpq;
+  return (blocks_before(P, r, last) + tiles_of(r.kv + r.n) + kStartB) * P.Hk;
 }
 
 // How the lists are dealt out.  Both kernels work it out, in whole numbers: a sum of floats
@@ -1189,16 +1215,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           rem -= t;
         }
         if (b1 - b0 > 1) w.r = request(P, w.b, ignored);
+        // the last block that begins at or before `rem`
+        int above = w.r.n <= P.tpq ? 1 : (w.r.n - 1) / P.tpq + 1;
 #pragma unroll 1
-        for (; w.rb * P.tpq < w.r.n; ++w.rb) {
-          const int t = tiles_of(block_keys(P, w.r, w.rb)) + kStartB;
-          if (rem < t * P.Hk) {
-            w.h = share_of(rem, t, 1.f / (float)t);
-            w.off = rem - w.h * t;
-            break;
-          }
-          rem -= t * P.Hk;
+        while (above - w.rb > 1) {
+          const int mid = (w.rb + above) / 2;
+          if (blocks_before(P, w.r, mid) * P.Hk <= rem)
+            w.rb = mid;
+          else
+            above = mid;
         }
+        rem -= blocks_before(P, w.r, w.rb) * P.Hk;
+        const int t = tiles_of(block_keys(P, w.r, w.rb)) + kStartB;
+        w.h = share_of(rem, t, 1.f / (float)t);
+        w.off = rem - w.h * t;
       }
       c->start[s] = w;
     }
@@ -1273,9 +1303,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
     const int h = divide(head, P.by_group), g = head - h * P.group;
     const size_t at = (size_t)(r.row0 + i) * P.Hq + head;
     const int rb = divide(i, P.by_tpq);
-    int u0 = first;
-#pragma unroll 1
-    for (int y = 0; y < rb; ++y) u0 += (tiles_of(block_keys(P, r, y)) + kStartB) * P.Hk;
+    int u0 = first + blocks_before(P, r, rb) * P.Hk;
     const int tiles = tiles_of(block_keys(P, r, rb));
     u0 += h * (tiles + kStartB) + kStartB;  // its first tile
     Unit own, pre;

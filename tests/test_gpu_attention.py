@@ -517,3 +517,35 @@ def test_long_lists_at_a_border_of_their_shares():
     assert binding.spec_verify_status(ws) == 0
     assert bool((out == 0.5).all())
     assert float((lse.double() - math.log(prefix + own)).abs().max()) < 20 * 2.0 ** -22
+
+
+PROMPTS = {
+    # lens, gamma, Hq, Hk, D, page, dtype, prefix: row blocks of 128 / group tokens each
+    "blocks_of_32": ([0, 70], [2499, 3], 4, 1, 64, 64, "bf16", 0),
+    "blocks_of_16": ([1000, 3, 0], [1500, 0, 777], 8, 1, 64, 32, "f16", 0),
+    "blocks_of_42": ([129, 5], [2600, 900], 3, 1, 64, 64, "bf16", 0),
+    "blocks_of_25": ([0, 31, 500], [1234, 1700, 2], 10, 2, 128, 64, "f16", 0),
+    "blocks_of_18_and_a_prefix": ([0, 64, 63], [700, 1300, 5], 7, 1, 64, 16, "bf16", 300),
+    "blocks_of_1": ([40, 0], [130, 70], 96, 1, 64, 16, "bf16", 0),
+    "blocks_of_128": ([1, 2], [6001, 1], 1, 1, 64, 64, "f16", 0),
+}
+
+
+@pytest.mark.parametrize("name", list(PROMPTS))
+def test_prompts_of_many_row_blocks(name):
+    lens, gam, Hq, Hk, D, page, dt, prefix = PROMPTS[name]
+    w = Batch(lens, gam, Hq, Hk, D, page, dt, prefix)
+    out, lse = w.run()
+    w.check(out, lse)
+    again, lse2 = w.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("Hq, D", [(96, 64), (20, 128)])
+def test_draft_masks_over_row_blocks(Hq, D):
+    """Steps of 32 rows in blocks of 1 and of 6: a word of a first block may name a row of the last."""
+    w = Batch([0, 100, 63, 64], [31, 31, 30, 5], Hq, 1, D, 16, "bf16")
+    g = torch.Generator().manual_seed(8)
+    mask = torch.randint(-2 ** 31, 2 ** 31 - 1, (w.T,), generator=g, dtype=torch.int64).int().cuda()
+    out, lse = w.run(mask=mask)
+    w.check(out, lse, mask=mask.long() & 0xffffffff)
