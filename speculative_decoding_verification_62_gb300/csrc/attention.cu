@@ -1389,6 +1389,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
         for (int y = 0; y < 8; ++y) o[y] += v[j][y] * w;
       }
     }
+    if (MANY && done) continue;  // (one row a CTA: all of it)
     if (MANY) {
       // the groups' joins, in a fixed order
 #pragma unroll
@@ -1534,9 +1535,15 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   const int rc = sv::code_of(cudaLaunchKernelEx(&cfg, attention_kernel<T, DP>, m, P));
   if (rc) return rc;
   // The launch itself overlaps the attention kernel, whose end the CTAs wait for.
-  // A CTA a row where the shares are more than eight times the units.
-  const bool many = 2ll * grid > 8ll * P.B * P.Hk;
-  const long long rows = (long long)(P.G < P.T ? P.G + 1 : P.T) * P.Hq;
+  // A CTA a row where the shares are more than eight times the units (counted at their most:
+  // a row block has a unit a key head).  By a CTA a row and by lane groups, 304 shares: one
+  // request of 131000 tokens, 8 rows (8 units) 98 and 117 us; four of 30000 (32 units) 91
+  // and 93; 64 rows behind 30000 tokens (16 units) 55 both; 256 rows (64 units) 148 and 125;
+  // a prompt of 2500 rows (632 units) 254 and 95.
+  const long long longest = P.G < P.T ? P.G + 1 : P.T;
+  const long long by_longest = (longest + P.tpq - 1) / P.tpq * P.B, by_rows = P.T / P.tpq + (long long)P.B;
+  const bool many = 2ll * grid > 8 * P.Hk * (by_longest < by_rows ? by_longest : by_rows);
+  const long long rows = longest * P.Hq;
   const int per_cta = many ? 1 : 4 * (32 / (DP / 8));
   const long long y = (rows + per_cta - 1) / per_cta;
   cfg.gridDim = dim3((unsigned int)P.B, (unsigned int)(y < 1024 ? y : 1024));
