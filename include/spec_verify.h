@@ -294,7 +294,9 @@ typedef struct {
  *   workspace    for the status word only: any of this library's, at least 4 bytes
  * The rotation is computed in 32 bits and rounded once.  A request whose cu_draft
  * entries are inconsistent (as in the packed calls, or a length above max_drafts)
- * is skipped (SV_STATUS_BAD_GAMMA); a row past the page table
+ * is skipped (SV_STATUS_BAD_GAMMA).  total_drafts may exceed cu_draft[batch], here and in
+ * spec_verify_attention: the rows behind the last request's are neither stored nor
+ * rotated (a captured step of fixed size).  A row past the page table
  * (SV_STATUS_BAD_LENGTH) or on a page outside the pool (SV_STATUS_BAD_PAGE) is not
  * stored, its query is still rotated.  No other element of the pools is written.
  */

@@ -205,8 +205,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : ROWS == 1 ? 8 : 
       const int i = t - b - c0;
       RowInfo info{-1, -1};
       long long pos = 0;
-      if (c0 < 0 || c1 < c0 || c1 - c0 > P.G || c1 > P.T - P.B || i < 0 || i > c1 - c0) {
-        flags = SV_STATUS_BAD_GAMMA;
+      const bool fits = c0 >= 0 && c1 >= c0 && c1 - c0 <= P.G && c1 <= P.T - P.B;
+      const bool row = fits && i >= 0 && i <= c1 - c0;
+      if (!row) {
+        // (rows behind a consistent last request: a step of fewer rows than the call's)
+        if (!fits || i < 0 || b + 1 < P.B) flags = SV_STATUS_BAD_GAMMA;
       } else {
         const long long slot = (long long)len + i;
         if (len < 0 || slot >= (long long)P.max_pages * P.page_size) {
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : ROWS == 1 ? 8 : 
       }
       s_row[lane] = info;
       s_pos[lane] = pos;
-      s_ok[lane] = flags != SV_STATUS_BAD_GAMMA;
+      s_ok[lane] = row;
     }
     const unsigned int any = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0 && any) atomicOr(P.status, any);

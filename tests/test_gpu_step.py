@@ -113,3 +113,84 @@ def test_steps_against_the_whole_history(prefix, dtype):
             total_accepted += a
         assert cache.kv_len.tolist() == [len(h) - 1 for h in history]
     assert total_accepted > 0
+
+
+@pytest.mark.parametrize("prefix", [0, 75])
+def test_a_captured_step_of_fixed_size_leaves_the_rows_behind_it(prefix):
+    """The append, the attention and the verification captured once for 24 rows and replayed
+    for steps of fewer: the rows behind the last request (NaN) are neither read into others
+    nor written, and no call takes them for an error."""
+    B, T, G, Hq, Hk, D, V, page = 4, 24, 8, 8, 2, 64, 50, 16
+    dtype, g = torch.bfloat16, torch.Generator().manual_seed(3)
+    lens = [20, 0, 33, 7]
+    need = [-(-(n + G + 1) // page) for n in lens]
+    pre = -(-prefix // page)
+    perm = torch.randperm(sum(need) + pre, generator=g).int()
+    table, at = torch.full((B, max(need)), -1, dtype=torch.int32), pre
+    for b, n in enumerate(need):
+        table[b, :n], at = perm[at:at + n], at + n
+    pools = [torch.randn((len(perm), page, Hk, D), generator=g).to(dtype).cuda() for _ in range(2)]
+    cache = binding.PagedCache(*pools, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    prefix_table = perm[:pre].cuda()
+    freq = rope.frequencies(D)
+    fx = rope.fixed_point(freq).cuda()
+    nan = float("nan")
+    qkv = torch.full((T, Hq + 2 * Hk, D), nan, dtype=dtype, device="cuda")
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+    p = torch.full((T, V), nan, device="cuda")
+    tok, u = torch.full((T - B,), -9, dtype=torch.int32, device="cuda"), torch.full((T,), nan, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    ws, ver = binding.make_attention_workspace(T, Hq, D), binding.Verifier(B, G, V)
+    q_rot, out, lse = torch.empty_like(q), torch.empty((T, Hq, D), dtype=dtype, device="cuda"), torch.empty((T, Hq), device="cuda")
+    q_rot = q_rot.contiguous()
+
+    def step():
+        binding.spec_verify_kv_append(q, k, v, cache, cu, G, fx, q_rot, ws, position_offset=prefix)
+        binding.spec_verify_attention(q_rot, cache, cu, G, out, ws, prefix_table=prefix_table, prefix_len=prefix, lse=lse)
+        ver.sample_probs_packed(p, None, cu, tok, u)
+
+    def load(gam):
+        n = sum(gam) + B
+        qkv.fill_(nan), p.fill_(nan), tok.fill_(-9), u.fill_(nan)
+        qkv[:n] = torch.randn((n, Hq + 2 * Hk, D), generator=g).to(dtype)
+        p[:n] = torch.softmax(torch.randn((n, V), generator=g), -1)
+        tok[:n - B] = torch.randint(0, V, (n - B,), generator=g, dtype=torch.int32)
+        u[:n] = torch.rand((n,), generator=g)
+        cu.copy_(torch.tensor([0] + list(np.cumsum(gam)), dtype=torch.int32))
+        for x in (q_rot, out, lse):
+            x.fill_(7.0)
+        return n
+    load([5, 5, 5, 5])
+    step()  # (modules are loaded before the capture)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for gam in ([0, 0, 0, 0], [5, 5, 5, 5], [2, 0, 3, 1], [0, 0, 0, 8], [8, 1, 0, 0]):
+        n = load(gam)
+        want = rotate(k[:n].double(), torch.cat([torch.arange(x + 1) + m + prefix for x, m in zip(gam, lens)]).cuda(),
+                      freq.cuda(), False)
+        graph.replay()
+        assert binding.spec_verify_status(ws) == 0 and binding.spec_verify_status(ver.workspace) == 0
+        for x in (q_rot, out, lse):
+            assert bool((x[n:] == 7.0).all()) and not torch.isnan(x[:n]).any()
+        tokens, acc = ver.out_tokens.cpu().numpy(), ver.num_accepted.cpu().numpy()
+        row = 0
+        for b in range(B):
+            m = gam[b] + 1
+            rows = slice(row, row + m)
+            slots = torch.arange(lens[b] + m).cuda()
+            ids = table[b].cuda().long()[slots // page]
+            keys, vals = (x[ids, slots % page].double() for x in pools)
+            assert (keys[lens[b]:] - want[rows]).abs().max() < 2.0 ** -8 * 1.1 * want.abs().max()
+            if prefix:
+                s = torch.arange(prefix).cuda()
+                keys, vals = (torch.cat([x[prefix_table.long()[s // page], s % page].double(), y])
+                              for x, y in zip(pools, (keys, vals)))
+            seen = torch.arange(len(keys)).cuda()[None] <= prefix + lens[b] + torch.arange(m).cuda()[:, None]
+            o, l, spread, size = attend(q_rot[rows].double(), keys, vals, seen, D ** -0.5)
+            tol, _ = tolerance(o, l, spread, size, len(keys), D, float(vals.abs().max()), dtype)
+            assert not ((out[rows].double() - o).abs() > tol).any()
+            a, z = probs_request(p[rows].double().cpu().numpy(), None, tok[row - b:row - b + gam[b]].tolist(),
+                                 u[rows].cpu().numpy(), float(u[rows][-1]))
+            assert acc[b] == a and tokens[b, a] == z
+            row += m
