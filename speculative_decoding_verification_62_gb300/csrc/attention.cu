@@ -135,7 +135,7 @@ struct AttnParams {
   char* out;
   float* lse;
   unsigned int* status;
-  int* starts;         // [B + 1]: where each request begins in list B, and the list's end
+  int* starts;         // [B + 2]: where each request begins in list B, the list's end, the CTAs of list A
   // Parts: whole units over own keys as rows [T * Hq][DP]; whole prefix units by
   // block [Hk][blocks] and parts of units by slot [kSlots], both as [DP / 8][kRows][8]
   // (a warp's lanes have a row each: their stores are one run of memory)
@@ -439,17 +439,22 @@ constexpr int kMaxList = 1 << 30;
 __device__ __forceinline__ int list_add(int a, int b) {
   return (int)min((unsigned int)a + (unsigned int)b, (unsigned int)kMaxList);
 }
-// Of a key head, the tiles and starts of a request's first `blocks` row blocks, none of
-// them its last: the sum over i of ceil((kv + (i + 1) tpq) / 64).  A sum of n terms
-// floor((a i + b) / m) is its whole parts, n (n - 1) / 2 times a / m and n times b / m,
-// and what is left counts the whole numbers below a line, which are the same counted by
-// rows: n' = (a n + b) / m terms with a and m exchanged, Euclid's steps on (tpq, 64).
-// One or two for groups of 1, 2, 4, 8 heads, eight at most.  The sum is below kMaxList, so is every
-// product.  (With a loop over the blocks the join of a prompt's rows was quadratic.)
-__device__ __forceinline__ int blocks_before(const AttnParams& P, const Req& r, int blocks) {
-  if (blocks == 0) return 0;
-  if (P.mask) return blocks * (tiles_of(r.kv + r.n) + kStartB);  // a word may name any row
-  unsigned int n = blocks, a = P.tpq, b = (unsigned int)r.kv + P.tpq + kTile - 1, m = kTile, sum = 0;
+// Of a key head, the tiles of a request's first `blocks` row blocks, none of them its last:
+// the sum over i of ceil((kv + (i + 1) tpq) / 64).  A sum of n terms floor((a i + b) / m) is
+// its whole parts, n (n - 1) / 2 times a / m and n times b / m, and what is left counts
+// the whole numbers below a line, which are the same counted by rows: (a n + b) / m terms
+// with a and m exchanged, Euclid's steps on (tpq, 64).  One or two for groups of 1, 2, 4, 8
+// heads, eight at most.  The sum is below kMaxList, so is every product.  (With a loop over
+// the blocks the join of a prompt's rows was quadratic.  A function of its own: inlined at its
+// six places it lengthened the code before the roles, which cost calls of single blocks 3
+// to 7 %.)
+__device__ __noinline__ int blocks_sum(int kv, int tpq, int blocks) {
+  unsigned int n = blocks, a = tpq, b = (unsigned int)kv + tpq + kTile - 1, m = kTile, sum = 0;
+  if (blocks <= 4) {  // sooner done one by one
+#pragma unroll 1
+    for (; n > 0; --n, b += a) sum += b / kTile;
+    return (int)sum;
+  }
 #pragma unroll 1
   for (;;) {
     const unsigned int qa = a / m, qb = b / m;
@@ -465,34 +470,43 @@ __device__ __forceinline__ int blocks_before(const AttnParams& P, const Req& r, 
     a = m;
     m = t;
   }
-  return (int)sum + blocks * kStartB;
+  return (int)sum;
+}
+// ... and their starts
+__device__ __forceinline__ int blocks_before(const AttnParams& P, const Req& r, int blocks) {
+  if (blocks == 0) return 0;
+  // (with mask words a row may see any row of its step)
+  return P.mask ? blocks * (tiles_of(r.kv + r.n) + kStartB) : blocks_sum(r.kv, P.tpq, blocks) + blocks * kStartB;
 }
 // A request's length in list B: its units' tiles and starts (below kMaxList).
 __device__ __forceinline__ int request_tiles(const AttnParams& P, const Req& r) {
   if (r.n <= 0) return 0;
-  const int last = r.n <= P.tpq ? 0 : (r.n - 1) / P.tpq;
-  return (blocks_before(P, r, last) + tiles_of(r.kv + r.n) + kStartB) * P.Hk;
+  int t = tiles_of(r.kv + r.n) + kStartB;
+  if (r.n > P.tpq) t += blocks_before(P, r, (r.n - 1) / P.tpq);
+  return t * P.Hk;
 }
 
-// How the lists are dealt out.  Both kernels work it out, in whole numbers: a sum of floats
-// may be contracted one way in one and another way in the other, and the join would then
-// look for a part in a place next to its own (lists past 2^24 tiles).
+// How the lists are dealt out.
 struct Plan {
   int a, b;          // lengths of the lists: tiles and starts
   int per_a, per_b;  // of a CTA's share of A, of a stream's share of B
   int ctas_a, ctas_b;
 };
-__device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int ctas) {
+// The CTAs of list A, by the lists' weights.  Only the attention kernel works this out,
+// and the join reads it: the sum of floats may be contracted in two ways, which differ by a
+// CTA for some lists past 2^24 tiles.
+__device__ __forceinline__ int pair_ctas(int a, int b, int ctas) {
+  if (a == 0) return 0;
+  const float wa = (float)a * kCostA, wb = (float)b * kCostB;
+  int na = (int)(ctas * (wa / (wa + wb)) + 0.5f);
+  na = na < 1 ? 1 : na;
+  return b > 0 && na > ctas - 1 ? ctas - 1 : na;
+}
+__device__ __forceinline__ int pair_list(const AttnParams& P) { return P.Hk * P.pairs * (P.pair_tiles + kStartA); }
+__device__ __forceinline__ Plan make_plan(const AttnParams& P, int b_tiles, int ctas, int na) {
   Plan L;
-  L.a = P.Hk * P.pairs * (P.pair_tiles + kStartA);
+  L.a = pair_list(P);
   L.b = b_tiles;
-  int na = 0;
-  if (L.a > 0) {
-    const unsigned long long wa = (unsigned long long)L.a * kCostA, all = wa + (unsigned long long)L.b * kCostB;
-    na = (int)((2 * ctas * wa + all) / (2 * all));  // rounded to the nearest
-    na = na < 1 ? 1 : na;
-    if (L.b > 0 && na > ctas - 1) na = ctas - 1;
-  }
   L.ctas_a = na;
   L.ctas_b = ctas - na;
   L.per_a = na ? (L.a + na - 1) / na : 0;
@@ -1178,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     total = singles;
     flags |= SV_STATUS_BAD_GAMMA;
   }
-  const Plan L = make_plan(P, total, gridDim.x);
+  const Plan L = make_plan(P, total, gridDim.x, pair_ctas(pair_list(P), total, gridDim.x));
   const bool pair_cta = (int)blockIdx.x < L.ctas_a;
   if (tid < 20) {
     bar_init(smem_addr(&c->kv_full[tid]), 1);
@@ -1215,17 +1229,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           rem -= t;
         }
         if (b1 - b0 > 1) w.r = request(P, w.b, ignored);
-        // the last block that begins at or before `rem`
-        int above = w.r.n <= P.tpq ? 1 : (w.r.n - 1) / P.tpq + 1;
+        if (w.r.n > P.tpq) {
+          // the last block that begins at or before `rem`
+          int above = (w.r.n - 1) / P.tpq + 1;
 #pragma unroll 1
-        while (above - w.rb > 1) {
-          const int mid = (w.rb + above) / 2;
-          if (blocks_before(P, w.r, mid) * P.Hk <= rem)
-            w.rb = mid;
-          else
-            above = mid;
+          while (above - w.rb > 1) {
+            const int mid = (w.rb + above) / 2;
+            if (blocks_before(P, w.r, mid) * P.Hk <= rem)
+              w.rb = mid;
+            else
+              above = mid;
+          }
+          rem -= blocks_before(P, w.r, w.rb) * P.Hk;
         }
-        rem -= blocks_before(P, w.r, w.rb) * P.Hk;
         const int t = tiles_of(block_keys(P, w.r, w.rb)) + kStartB;
         w.h = share_of(rem, t, 1.f / (float)t);
         w.off = rem - w.h * t;
@@ -1243,7 +1259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         at += request_tiles(P, request(P, b, ignored));
       }
     }
-    if (tid == 0) P.starts[P.B] = over ? -1 : total;
+    if (tid == 0) {
+      P.starts[P.B] = over ? -1 : total;
+      P.starts[P.B + 1] = L.ctas_a;
+    }
     if (flags) atomicOr(P.status, flags);
   }
   fence_before();
@@ -1285,7 +1304,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ At
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's writes
   const int list = P.starts[P.B];
   if (r.n <= 0 || list < 0) return;
-  const Plan L = make_plan(P, list, ctas);
+  const Plan L = make_plan(P, list, ctas, P.starts[P.B + 1]);
   const int first = P.starts[b];
   if (L.per_b <= 0) return;
   const float inv_a = 1.f / (float)(L.per_a > 0 ? L.per_a : 1), inv_b = 1.f / (float)L.per_b;
@@ -1492,7 +1511,7 @@ AttnLayout attn_layout(long long T, int Hq, int D) {
     at += sv::align256(bytes);
     return a;
   };
-  L.starts = take((size_t)(T + 1) * sizeof(int));
+  L.starts = take((size_t)(T + 2) * sizeof(int));
   L.own = take(rows * dp * 4);
   L.own_lse = take(rows * 4);
   L.whole = take(tiles * kRows * dp * 4);
@@ -1536,13 +1555,16 @@ int launch(const Maps& m, const AttnParams& P, cudaStream_t stream) {
   if (rc) return rc;
   // The launch itself overlaps the attention kernel, whose end the CTAs wait for.
   // A CTA a row where the shares are more than eight times the units (counted at their most:
-  // a row block has a unit a key head).  By a CTA a row and by lane groups, 304 shares: one
-  // request of 131000 tokens, 8 rows (8 units) 98 and 117 us; four of 30000 (32 units) 91
-  // and 93; 64 rows behind 30000 tokens (16 units) 55 both; 256 rows (64 units) 148 and 125;
-  // a prompt of 2500 rows (632 units) 254 and 95.
+  // a row block has a unit a key head) and the rows no more than 16 an SM.
+  // By a CTA a row and by lane groups, 304 shares: one request of 131000 tokens and 8 rows of
+  // 64 heads (8 units, 512 rows and heads) 98 and 117 us; four of 30000 tokens (32, 1024)
+  // 91 and 93; 64 rows of 32 heads behind 30000 tokens (16, 2048) 55 both, 128 rows
+  // (32, 4096) 91 and 79; a prompt of 128 rows (32, 4096) 25 and 17, of 2500 (632, 80000)
+  // 254 and 95.
   const long long longest = P.G < P.T ? P.G + 1 : P.T;
   const long long by_longest = (longest + P.tpq - 1) / P.tpq * P.B, by_rows = P.T / P.tpq + (long long)P.B;
-  const bool many = 2ll * grid > 8 * P.Hk * (by_longest < by_rows ? by_longest : by_rows);
+  const bool many = 2ll * grid > 8 * P.Hk * (by_longest < by_rows ? by_longest : by_rows) &&
+                    (long long)P.T * P.Hq <= 16ll * grid;
   const long long rows = longest * P.Hq;
   const int per_cta = many ? 1 : 4 * (32 / (DP / 8));
   const long long y = (rows + per_cta - 1) / per_cta;
