@@ -528,6 +528,9 @@ PROMPTS = {
     "blocks_of_18_and_a_prefix": ([0, 64, 63], [700, 1300, 5], 7, 1, 64, 16, "bf16", 300),
     "blocks_of_1": ([40, 0], [130, 70], 96, 1, 64, 16, "bf16", 0),
     "blocks_of_128": ([1, 2], [6001, 1], 1, 1, 64, 64, "f16", 0),
+    "few_rows_of_a_long_request": ([9000], [40], 8, 1, 64, 64, "f16", 0),  # joined by a CTA a row
+    "six_blocks_of_a_long_request": ([20011], [90], 8, 1, 128, 16, "bf16", 0),
+    "nine_blocks_of_two_requests": ([7000, 12000], [50, 8], 18, 1, 64, 32, "bf16", 100),
 }
 
 
