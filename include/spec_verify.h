@@ -214,9 +214,12 @@ int spec_verify_draw(const void *logits, sv_dtype dtype, int B, int V, const flo
  * draw as in steps 2 and 3.  Rows need not sum to 1: a draw uses its weights'
  * own total.  Of a request, the calls read p and q at the drafts, row k of
  * target_probs and, after a rejection, row k of draft_probs.  The tests are
- * exact; the draw's weights are rounded to whole multiples of 2^-47, summed
- * exactly, and compared with u times the total exactly.  A residual whose
- * weights are all 0 draws from p_k; a row of zeros draws V - 1 and sets
+ * exact; the draw's weights are rounded by less than 2^-46 (p or p - q to a multiple
+ * of 2^-46, so that one below 2^-47 counts as 0; the rounding error of p - q to one
+ * of 2^-47), summed exactly, and compared with u times the total exactly:
+ * a row should not sum to much less than 1 (where n entries sum to 2^-20, the
+ * roundings move a boundary by about 2^-28 sqrt(n) of the total).  A residual
+ * whose weights are all 0 draws from p_k; a row of zeros draws V - 1 and sets
  * SV_STATUS_BAD_PROB.  An entry that is no probability (negative, NaN, above 1)
  * sets that bit where it is read and counts as 0 (above 1: as 1).
  * The other arguments, the layouts, the workspace (status word only), errors and

@@ -8,11 +8,11 @@
 //
 // The test is exact: u q is a product of two 24-bit numbers, formed in double.
 // The draw is exact up to the weights' grain: each weight is a whole multiple of
-// 2^-47, found by additions alone (weight() below), and weights are summed as
-// integers, so that no sum depends on an order; u w_total is compared after a
+// 2^-47 (of 2^-46 without q), found by additions alone (weight() below), and weights are
+// summed as integers, so that no sum depends on an order; u w_total is compared after a
 // 128-bit product.  Weights below 2^-22 are rounded (by at most 2^-47, and by
-// 2^-48 where p and q differ much), and the roundings of n entries move a boundary
-// by about 2^-48 sqrt(n): a uniform lands on the other side of one of V boundaries
+// 2^-48 more where p - q itself is rounded), and the roundings of n entries move a
+// boundary by about 2^-48 sqrt(n): a uniform lands on the other side of one of V boundaries
 // with a chance of about V sqrt(V) 2^-48 (2^-23 at V = 128256, if all entries
 // were that small).  Sums saturate at 2^63 = 65536 (a row sums to about 1).
 //
@@ -20,11 +20,11 @@
 // other reads are gathers.  A cluster of C CTAs shares a request, each warp a
 // contiguous range of the row.  The owner of the target re-reads only the
 // range of the warp that holds it, from L2.  Measured (GB300): 512 requests over
-// 128256 entries of bf16 59.6 us (197 MB, 3.3 TB/s; instruction issue 54 %, integer
-// pipe 46 %), 64 requests over 128256 of fp32 19.0 us (58 MB), one request 5.7 us:
-// latency, a chain of gathers, sums, exchange and walk.  Staging by asynchronous
-// copies (66 us), a second set of registers (64 us) and three CTAs an SM (87 us) were
-// slower at 512 requests.
+// 128256 entries of bf16, 350 of them with a refused draft, 59.5 us (222 MB, 3.7 TB/s;
+// instruction issue 54 %, integer pipe 46 %), 64 requests over 152064 of fp32, 50
+// refused, 19.0 us (70 MB), one request 5.7 us: latency, a chain of gathers, sums,
+// exchange and walk.  Staging by asynchronous copies (66 us), a second set of registers
+// (64 us) and three CTAs an SM (87 us) were slower at 512 requests.
 #include "../../include/spec_verify.h"
 #include "internal.h"
 

@@ -277,3 +277,22 @@ def test_more_than_the_logits_path_and_the_same_decisions():
     assert torch.equal(a[1][clear], b[1][clear])
     # a draw differs only where u lies within the fp32 rounding of a boundary
     assert (a[0][clear] != b[0][clear]).any(-1).sum() <= 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_that_sum_to_little_or_much(dtype):
+    """A draw goes by its weights' own total; weights below 2^-47 count as 0 (the rest of
+    a weight is added to 1.5 2^-23, whose last bit is 2^-46)."""
+    S = {n: b for b, n in binding.STATUS_BITS.items()}
+    w = torch.tensor([0.25, 0.0, 0.125, 0.5, 0.125, 0.0], dtype=DT[dtype])
+    us = [0.0, 0.24, 0.25, 0.374, 0.375, 0.874, 0.875, 0.999]
+    want = [0, 0, 2, 2, 3, 3, 4, 4]
+    tok, gam = torch.zeros((8, 0), dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    for power in (-43, -20, 1):  # (2^-43 of 0.125 is one step)
+        out, _ = run((w * 2.0 ** power).repeat(8, 1, 1), None, tok, gam, torch.tensor(us)[:, None])
+        assert out[:, 0].tolist() == want
+    # many entries of 1: their sum is exact
+    out, _ = run(torch.ones((8, 1, 60000), dtype=DT[dtype]), None, tok, gam, torch.tensor(us)[:, None])
+    assert out[:, 0].tolist() == [int(np.floor(np.float32(u).astype(np.float64) * 60000)) for u in us]
+    out, _ = run((w * 2.0 ** -60).repeat(8, 1, 1), None, tok, gam, torch.tensor(us)[:, None], status=S["BAD_PROB"])
+    assert (out[:, 0] == 5).all()
