@@ -49,11 +49,11 @@
 // keys of 2^-25 each after one that is 1 are 0.16 % of an output.)
 //
 // Measured (GB300, with the join): one request's 131000 keys of 8 heads, 64 query heads
-// of 128, 97.8 us (537 MB, 5.5 TB/s; 88 us and 6.1 TB/s without the join); 256 requests
-// behind 8192 shared tokens 249 us (551 TFLOP/s); 37 requests in 16-token pages 45 us,
-// bound by the issue of 2 KB boxes; one request of 600 tokens 11.9 us, 4 of them the
-// join.  128-key tiles in B cost 37 requests of D = 64 58 -> 72 us, a prefetch of the
-// next keys into L2 the long request 98 -> 116.
+// of 128, 97.8 us (537 MB, 5.5 TB/s; 87.8 us and 6.1 TB/s without the join); 256 requests
+// behind 8192 shared tokens 246 us (557 TFLOP/s); 37 requests in 16-token pages 45 us,
+// bound by the issue of 2 KB boxes; one request of 600 tokens 11.8 us, 4.0 of them the
+// join; a prompt of 2500 rows 96 us (533 TFLOP/s; 67 without the join), of 32768 rows 6.6 ms
+// (1330 TFLOP/s).
 #include "../../include/spec_verify.h"
 #include "internal.h"
 

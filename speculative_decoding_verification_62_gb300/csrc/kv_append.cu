@@ -16,12 +16,15 @@
 // are formed once, in shared memory, and serve every head.  Hence many small CTAs:
 // - up to 608 rows (four CTAs an SM, one wave) a CTA of 256 threads a row;
 // - up to 2047 rows 128 threads a row, eight CTAs an SM, three reads a thread under
-//   way: 1174 rows 9.3 -> 7.4 us (256 threads -> 128), 618 rows 6.3 (two rows a CTA: 7.4),
-//   1920 rows 13.0 (14.0);
+//   way: 618 rows 6.3 us (two rows a CTA: 7.4), 1174 rows 7.4 (10.0), 1920 rows 13.0 (14.0).
+//   This is the best form up to one wave, eight CTAs an SM (1216 rows on 152).  Past it forms
+//   that are not built in were faster: 1260 rows 10.8 us, with two reads under way 8.8;
+//   1330 rows 10.5 and 8.4; 1646 rows 11.5, with one read and twelve CTAs 9.6; 1920 rows
+//   13.0, with one read and sixteen CTAs 11.6 (and 2377 rows, two a CTA, 15.2 and 13.2);
 // - from there two rows a CTA of 128 threads, twelve CTAs an SM: 23018 rows 59 us, one
 //   row a CTA of 128 threads 68, four rows 69, two rows of 256 threads 64.
 // Measured (GB300): one row 3.5 us; 256 requests' steps 7.4 us (29 MB, 3.9 TB/s);
-// prompts of 12 requests, 24 + 6 + 6 heads of 96 in fp16, 59.2 us (318 MB, 5.4 TB/s: 79 %
+// prompts of 12 requests, 24 + 6 + 6 heads of 96 in fp16, 59.4 us (318 MB, 5.4 TB/s: 79 %
 // of a copy).
 #include "../../include/spec_verify.h"
 #include "internal.h"
