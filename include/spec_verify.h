@@ -68,7 +68,12 @@ extern "C" {
 /* A CUDA stream (cudaStream_t); NULL means the legacy default stream. */
 typedef struct CUstream_st *sv_stream_t;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 } sv_dtype; /* SV_F16: paged caches only */
+typedef enum {
+  SV_F32 = 0,
+  SV_BF16 = 1,
+  SV_F16 = 2, /* paged caches and their queries, keys and values only */
+  SV_E4M3 = 3 /* paged caches with scales only */
+} sv_dtype;
 
 enum {
   SV_OK = 0,
@@ -96,8 +101,11 @@ enum {
   SV_STATUS_BAD_PROB = 128u,      /* a probability outside [0, 1] or NaN: counted as 0 (above 1:
                                      as 1); or a row that sums to 0, or to 65536 or more */
   SV_STATUS_BAD_PAGE = 256u,      /* a page number outside the pool: not written, read as zeros */
-  SV_STATUS_BAD_LENGTH = 512u     /* kv_len negative, or a step past the request's page table:
+  SV_STATUS_BAD_LENGTH = 512u,    /* kv_len negative, or a step past the request's page table:
                                      that row or request is left out */
+  SV_STATUS_BAD_SCALE = 1024u,    /* a block's scale outside [2^-32, 2^64] or NaN: read as 1 */
+  SV_STATUS_BAD_ROW = 2048u,      /* a parent that is no row: the row continues itself */
+  SV_STATUS_NO_PAGES = 4096u      /* fewer free pages than a step takes: it took none */
 };
 
 #define SV_MAX_GAMMA 31
@@ -359,6 +367,128 @@ int spec_verify_attention(const void *q, const int64_t *q_strides, int q_heads,
                           const int32_t *cu_draft, int total_drafts, int max_drafts, float scale,
                           const uint32_t *draft_mask, void *out, float *lse, void *workspace,
                           size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * A cache in 8 bits.  The pools of sv_kv_cache hold e4m3 codes (dtype SV_E4M3: 1 sign, 4
+ * exponent and 3 mantissa bits, no infinities, largest 448), and a value is its code times
+ * the scale of its block: block tokens of a page (the page's tokens block * i .. block * i +
+ * block - 1) of one key head.  k[(page * (page_size / block) + i) * kv_heads + head] is
+ * the keys' scale, v[..] likewise (device memory, float32).
+ *   block        a power of two, at most SV_MAX_BLOCK and page_size
+ *   head_dim     a multiple of 16; the cache's strides are positive multiples of 16
+ * Scales lie in [2^-32, 2^64].  The append writes powers of two from 2^-32 to 2^56, so
+ * that scaling rounds nothing; the attention reads any scale in the range.
+ * The struct itself is HOST memory, read during the call.
+ */
+#define SV_MAX_BLOCK 128
+typedef struct {
+  float *k, *v; /* [num_pages][page_size / block][kv_heads] */
+  int block;
+} sv_kv_scales;
+
+/*
+ * spec_verify_kv_append for a cache in 8 bits: q, k, v and q_out are dtype (SV_BF16 or
+ * SV_F16), rotated as there, and keys and values are stored as codes.  Of the rows that
+ * a call appends to one block and head (keys and values apart), m is the largest magnitude
+ * of a value, or of a pair that turns (rope_scale sqrt(a^2 + c^2), which no angle changes);
+ * the block's scale becomes the smallest power of two s in [2^-32, 2^56] with 448 s >= m,
+ * and no less than the scale that it had if it holds tokens before kv_len[b].  Their codes
+ * are then rescaled (rounded to nearest), exact but for values below 2^-6 s.  Codes are
+ * rounded to nearest, ties to even; values beyond 448 s, infinities too, become 448 s, NaN stays
+ * NaN (and counts for nothing in m).  A scale stays as large as rejected rows made it while
+ * its block holds older tokens.
+ * A block's older tokens belong to the request that appends (as its page does).  The
+ * other arguments, statuses, errors and ownership: as spec_verify_kv_append; a block
+ * whose older tokens have a scale outside the range keeps their codes, and its scale is
+ * the new rows' (SV_STATUS_BAD_SCALE).
+ */
+int spec_verify_kv_append_e4m3(const void *q, const int64_t *q_strides, int q_heads,
+                               const void *k, const int64_t *k_strides, const void *v,
+                               const int64_t *v_strides, sv_dtype dtype, void *q_out,
+                               const int64_t *q_out_strides, const sv_kv_cache *cache,
+                               const sv_kv_scales *scales, const int32_t *cu_draft,
+                               int total_drafts, int max_drafts, const int64_t *freq, int rot_dim,
+                               int interleaved, float rope_scale, const int32_t *positions,
+                               int position_offset, void *workspace, size_t ws_bytes,
+                               sv_stream_t stream);
+
+/*
+ * Who holds which pages of a pool (all device memory, int32):
+ *   held        [batch]: pages of a request's row of the page table, its first ones
+ *   ref         [num_pages]: rows that hold a page (a prefix that a batch shares counts as
+ *               a row: 1 more); 0: free
+ *   free_pages  [num_pages]: the free pages, in the first *free_count entries
+ *   free_count  [1]
+ * The struct itself is HOST memory, read during the call.
+ */
+typedef struct {
+  int32_t *held, *ref, *free_pages, *free_count;
+} sv_page_pool;
+
+/* Bytes of workspace that the two calls below need; 0 if the sizes are invalid. */
+size_t spec_verify_pages_workspace_size(int num_pages, int batch, int max_pages);
+
+/*
+ * The page table of the next step.  Row b of the page table continues row parents[b]: it
+ * refers to the same tokens (kv_len[b] becomes kv_len[parents[b]], the pages are shared),
+ * a row whose parent is -1 ends (no tokens, no pages).  parents NULL: every row continues
+ * itself.  Then every row gives back the pages behind its tokens, and takes what tokens[b]
+ * more need, so that it holds ceil((kv_len[b] + tokens[b]) / page_size) pages; the entries
+ * behind those that it held before are set to -1.  If tokens[b] > 0 and its last page is
+ * partly filled and held by another row too, it takes a page of its own for it, with
+ * a copy of its tokens' keys, values and scales (what the page holds behind them is left);
+ * where all that hold the page do so, the lowest row keeps it.  After the call an append of tokens[b]
+ * rows writes to pages that no other row holds.
+ *   cache      page_table, kv_len and the pools are written; dtype and scales as in the
+ *              append (scales NULL for 16 bits)
+ *   parents    optional device int32 [batch]
+ *   tokens     device int32 [batch], >= 0 (a verify step: gamma_b + 1)
+ *   workspace  zero-filled once; every call leaves it so, but for the status word.  One call
+ *              at a time, in order on one stream.
+ * Pages that no row holds any more go back to free_pages in the order of the rows and places that
+ * held them; pages are then taken from its end, in the order of the rows, a row's copy
+ * first.  So results repeat, whatever runs beside.  Where the takes need more than there
+ * are, none are taken and nothing is copied: every row holds its tokens' pages
+ * (SV_STATUS_NO_PAGES; the step must not be appended: a later call, after other rows have
+ * ended, takes them).  A kv_len past the pages held counts as what they hold, tokens past
+ * the page table or below 0 as 0 (SV_STATUS_BAD_LENGTH); entries outside the pool are
+ * neither counted nor copied (SV_STATUS_BAD_PAGE).
+ */
+int spec_verify_pages_step(const sv_kv_cache *cache, const sv_kv_scales *scales,
+                           const sv_page_pool *pool, const int32_t *parents,
+                           const int32_t *tokens, void *workspace, size_t ws_bytes,
+                           sv_stream_t stream);
+
+/*
+ * The pages in use (ref > 0; n of them) move to the front of the pool: those at n and behind, in
+ * order, to the free places below n, in order, with all that they hold.  The page table (a
+ * row's first held entries), ref and the list of free pages (n is taken next, then n + 1)
+ * follow.
+ *   remap  device int32 [num_pages]: where each page is now (-1: it was free), for tables
+ *          that the caller keeps (a shared prefix's)
+ * Arguments as above.
+ */
+int spec_verify_pages_compact(const sv_kv_cache *cache, const sv_kv_scales *scales,
+                              const sv_page_pool *pool, int32_t *remap, void *workspace,
+                              size_t ws_bytes, sv_stream_t stream);
+
+/*
+ * spec_verify_attention over a cache in 8 bits: k_j and v_j are codes times their scales.
+ * q and out are dtype (SV_BF16 or SV_F16).  Arguments, masks, prefix, rows that see nothing,
+ * statuses and errors as there, but: the workspace has the size below (zero its first
+ * 4 bytes before the first use); any q_heads that kv_heads divides; a score scale q . k
+ * with its keys' scale stays below 2^27 in magnitude; a query row with an infinity or NaN
+ * gives NaN.  Queries enter the product as sums of 8-bit floats that hold every
+ * value to 2^-21 of its head's largest; weights times their values' scales are rounded as fp16 and
+ * by at most 2^-9 of themselves, or 2^-30 of the row's largest.
+ */
+size_t spec_verify_attention_e4m3_workspace_size(int total_rows, int q_heads, int head_dim);
+int spec_verify_attention_e4m3(const void *q, const int64_t *q_strides, int q_heads,
+                               sv_dtype dtype, const sv_kv_cache *cache,
+                               const sv_kv_scales *scales, const int32_t *prefix_table,
+                               int prefix_len, const int32_t *cu_draft, int total_drafts,
+                               int max_drafts, float scale, const uint32_t *draft_mask, void *out,
+                               float *lse, void *workspace, size_t ws_bytes, sv_stream_t stream);
 
 /*
  * spec_verify_sample_noalloc: spec_verify_sample with no caller workspace.

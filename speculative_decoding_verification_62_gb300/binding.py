@@ -16,13 +16,14 @@ import torch
 
 from . import build as _build
 
-SV_F32, SV_BF16, SV_F16 = 0, 1, 2
+SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
 SV_MAX_GAMMA = 31
 SV_MAX_HEAD_DIM = 128
 SV_MAX_VOCAB = 1 << 24
+SV_MAX_BLOCK = 128
 STATUS_BITS = {1: "BAD_GAMMA", 2: "BAD_TOKEN", 4: "BAD_UNIFORM", 8: "BAD_TEMPERATURE",
                16: "NONFINITE_ROW", 32: "INTERNAL", 64: "TIMEOUT", 128: "BAD_PROB",
-               256: "BAD_PAGE", 512: "BAD_LENGTH"}
+               256: "BAD_PAGE", 512: "BAD_LENGTH", 1024: "BAD_SCALE", 2048: "BAD_ROW", 4096: "NO_PAGES"}
 SV_NOALLOC_SCRATCH_BYTES = 4 << 20
 EXPORTS = ("spec_verify_workspace_size", "spec_verify_sample", "spec_verify_greedy",
            "spec_verify_sample_packed", "spec_verify_greedy_packed", "spec_verify_draw",
@@ -30,7 +31,9 @@ EXPORTS = ("spec_verify_workspace_size", "spec_verify_sample", "spec_verify_gree
            "spec_verify_set_schedule", "spec_verify_route", "spec_verify_cluster_size",
            "spec_verify_set_wait_limit", "spec_verify_set_lazy", "spec_verify_sample_probs",
            "spec_verify_sample_probs_packed", "spec_verify_kv_append", "spec_verify_attention",
-           "spec_verify_attention_workspace_size")
+           "spec_verify_attention_workspace_size", "spec_verify_kv_append_e4m3",
+           "spec_verify_attention_e4m3", "spec_verify_attention_e4m3_workspace_size",
+           "spec_verify_pages_workspace_size", "spec_verify_pages_step", "spec_verify_pages_compact")
 SCHEDULE_AUTO, SCHEDULE_PERSISTENT, SCHEDULE_STREAM = 0, 1, 2
 ROUTE_PERSISTENT, ROUTE_CLUSTER, ROUTE_STREAM, ROUTE_CLAIMS, ROUTE_PIPELINE = 0, 1, 2, 3, 4
 
@@ -45,6 +48,17 @@ class _KvCache(ctypes.Structure):
                 ("head_dim", ctypes.c_int), ("k_strides", ctypes.c_int64 * 3),
                 ("v_strides", ctypes.c_int64 * 3), ("page_table", ctypes.c_void_p),
                 ("max_pages", ctypes.c_int), ("batch", ctypes.c_int), ("kv_len", ctypes.c_void_p)]
+
+
+class _KvScales(ctypes.Structure):
+    """sv_kv_scales of include/spec_verify.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block", ctypes.c_int)]
+
+
+class _PagePool(ctypes.Structure):
+    """sv_page_pool of include/spec_verify.h."""
+    _fields_ = [("held", ctypes.c_void_p), ("ref", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p)]
 
 
 class SpecVerifyError(RuntimeError):
@@ -109,6 +123,21 @@ def load_library():
         lib.spec_verify_attention.restype = ci
         lib.spec_verify_attention.argtypes = [vp, i64p, ci, cache, vp, ci, vp, ci, ci, cf, vp, vp,
                                               vp, vp, sz, vp]
+        scales, pool = ctypes.POINTER(_KvScales), ctypes.POINTER(_PagePool)
+        lib.spec_verify_kv_append_e4m3.restype = ci
+        lib.spec_verify_kv_append_e4m3.argtypes = [vp, i64p, ci, vp, i64p, vp, i64p, ci, vp, i64p, cache,
+                                                   scales, vp, ci, ci, vp, ci, ci, cf, vp, ci, vp, sz, vp]
+        lib.spec_verify_attention_e4m3_workspace_size.restype = sz
+        lib.spec_verify_attention_e4m3_workspace_size.argtypes = [ci, ci, ci]
+        lib.spec_verify_attention_e4m3.restype = ci
+        lib.spec_verify_attention_e4m3.argtypes = [vp, i64p, ci, ci, cache, scales, vp, ci, vp, ci, ci, cf,
+                                                   vp, vp, vp, vp, sz, vp]
+        lib.spec_verify_pages_workspace_size.restype = sz
+        lib.spec_verify_pages_workspace_size.argtypes = [ci, ci, ci]
+        lib.spec_verify_pages_step.restype = ci
+        lib.spec_verify_pages_step.argtypes = [cache, scales, pool, vp, vp, vp, sz, vp]
+        lib.spec_verify_pages_compact.restype = ci
+        lib.spec_verify_pages_compact.argtypes = [cache, scales, pool, vp, vp, sz, vp]
         _lib = lib
         return lib
 
@@ -449,18 +478,29 @@ class PagedCache:
     are used in place (their contents may change between calls, the attributes may not be
     assigned), and kv_len is advanced by commit() alone.  Pages or rows of the pools may
     not overlap one another.
+
+    A cache in 8 bits: pools of float8_e4m3fn (head_dim and strides multiples of 16) with
+    k_scales, v_scales [num_pages, page_size / block, kv_heads] float32, whose shape says
+    how many tokens share a scale.
     """
     k_pages = property(lambda self: self._tensors[0])
     v_pages = property(lambda self: self._tensors[1])
     page_table = property(lambda self: self._tensors[2])
     kv_len = property(lambda self: self._tensors[3])
+    k_scales = property(lambda self: self._tensors[4])
+    v_scales = property(lambda self: self._tensors[5])
 
-    def __init__(self, k_pages, v_pages, page_table, kv_len):
+    def __init__(self, k_pages, v_pages, page_table, kv_len, k_scales=None, v_scales=None):
         self.index = _index(k_pages, "k_pages")
         for name, t in (("v_pages", v_pages), ("page_table", page_table), ("kv_len", kv_len)):
             if _index(t, name) != self.index:
                 raise ValueError(f"{name} is on {t.device}, k_pages on {k_pages.device}")
-        if k_pages.dtype not in (torch.bfloat16, torch.float16):
+        e4m3 = k_scales is not None or v_scales is not None
+        if e4m3 and k_pages.dtype != torch.float8_e4m3fn:
+            raise TypeError(f"k_pages with scales must be float8_e4m3fn, got {k_pages.dtype}")
+        if not e4m3 and k_pages.dtype == torch.float8_e4m3fn:
+            raise ValueError("k_pages of float8_e4m3fn need k_scales and v_scales")
+        if not e4m3 and k_pages.dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"k_pages must be bfloat16 or float16, got {k_pages.dtype}")
         if v_pages.dtype != k_pages.dtype:
             raise TypeError(f"v_pages must be {k_pages.dtype}, got {v_pages.dtype}")
@@ -472,12 +512,13 @@ class PagedCache:
             raise ValueError("a pool needs a page and a head")
         if page < 16 or page > 4096 or page & (page - 1):
             raise ValueError(f"page_size must be a power of two from 16 to 4096, got {page}")
-        if dim < 8 or dim > SV_MAX_HEAD_DIM or dim % 8:
-            raise ValueError(f"head_dim must be a multiple of 8 up to {SV_MAX_HEAD_DIM}, got {dim}")
+        unit = 16 if e4m3 else 8
+        if dim < unit or dim > SV_MAX_HEAD_DIM or dim % unit:
+            raise ValueError(f"head_dim must be a multiple of {unit} up to {SV_MAX_HEAD_DIM}, got {dim}")
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            if t.stride(3) != 1 or any(s <= 0 or s % 8 for s in t.stride()[:3]) or t.data_ptr() % 16:
+            if t.stride(3) != 1 or any(s <= 0 or s % unit for s in t.stride()[:3]) or t.data_ptr() % 16:
                 raise ValueError(f"{name} must be 16-byte aligned with contiguous heads and "
-                                 "strides that are multiples of 8")
+                                 f"strides that are multiples of {unit}")
             order = sorted(range(4), key=lambda i: t.stride(i))
             reach = 0
             for i in order:
@@ -489,14 +530,24 @@ class PagedCache:
             raise ValueError("page_table must be a contiguous int32 [batch, max_pages]")
         B, width = page_table.shape
         _dev(kv_len, "kv_len", torch.int32, (B,))
-        self._tensors = (k_pages, v_pages, page_table, kv_len)
+        self.block, self.scales_ref = 0, None
+        if e4m3:
+            per = k_scales.shape[1] if isinstance(k_scales, torch.Tensor) and k_scales.dim() == 3 else 0
+            self.block = page // per if per and page % per == 0 else 0
+            if not 0 < self.block <= SV_MAX_BLOCK:  # (page and so block are powers of two)
+                raise ValueError("k_scales must be [num_pages, page_size / block, kv_heads] with a block of at "
+                                 f"most {SV_MAX_BLOCK} tokens")
+            self._scales = _KvScales(_arg(k_scales, "k_scales", torch.float32, (n, per, heads), self.index),
+                                     _arg(v_scales, "v_scales", torch.float32, (n, per, heads), self.index), self.block)
+            self.scales_ref = ctypes.byref(self._scales)
+        self._tensors = (k_pages, v_pages, page_table, kv_len, k_scales, v_scales)
         self.cu_shape = (B + 1,)
         self.batch, self.kv_heads, self.head_dim, self.dtype = B, heads, dim, k_pages.dtype
         self.page_size, self.scale = page, dim ** -0.5
         ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
         self.struct = _KvCache(
             k_pages.data_ptr(), v_pages.data_ptr(),
-            SV_BF16 if k_pages.dtype == torch.bfloat16 else SV_F16, n, page, heads, dim,
+            SV_E4M3 if e4m3 else SV_BF16 if k_pages.dtype == torch.bfloat16 else SV_F16, n, page, heads, dim,
             (ctypes.c_int64 * 3)(*k_pages.stride()[:3]), (ctypes.c_int64 * 3)(*v_pages.stride()[:3]),
             ptr(page_table), width, B, ptr(kv_len))
         self.ref = ctypes.byref(self.struct)
@@ -520,17 +571,31 @@ def make_attention_workspace(total_rows: int, q_heads: int, head_dim: int,
     return ws
 
 
-def _heads(t, name, cache, shape):
-    """Address and (row, head) strides of a [rows, heads, head_dim] view of that shape."""
-    if (isinstance(t, torch.Tensor) and t.dtype is cache.dtype and t.get_device() == cache.index
+def make_attention_e4m3_workspace(total_rows: int, q_heads: int, head_dim: int,
+                                  device="cuda") -> torch.Tensor:
+    """Workspace of spec_verify_attention_e4m3 for steps of up to total_rows rows."""
+    n = int(load_library().spec_verify_attention_e4m3_workspace_size(int(total_rows), int(q_heads),
+                                                                     int(head_dim)))
+    if n == 0:
+        raise ValueError(f"invalid sizes rows={total_rows} q_heads={q_heads} head_dim={head_dim}")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _heads(t, name, cache, shape, dtype=None):
+    """Address and (row, head) strides of a [rows, heads, head_dim] view of that shape, of the
+    cache's type or of `dtype`."""
+    dtype = dtype or cache.dtype
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == cache.index
             and t.shape == shape):
         row, head, one = t.stride()
         if one == 1:
             return t.data_ptr(), _two(row, head)
     if _index(t, name) != cache.index:
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{cache.index}")
-    if t.dtype != cache.dtype:
-        raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     raise ValueError(f"{name} must have contiguous heads")
@@ -542,13 +607,31 @@ def _cu_rows(cu_draft, cache, rows):
     return _arg(cu_draft, "cu_draft", torch.int32, cache.cu_shape, cache.index)
 
 
+def _rows16(t, name):
+    """The type of rows beside a cache in 8 bits, and its code."""
+    dtype = getattr(t, "dtype", None)
+    if dtype is torch.bfloat16:
+        return dtype, SV_BF16
+    if dtype is torch.float16:
+        return dtype, SV_F16
+    raise TypeError(f"{name} must be bfloat16 or float16, got {dtype or type(t).__name__}")
+
+
+def _in_8_bits(cache):
+    if cache.scales_ref is None:
+        raise TypeError("the cache must hold float8_e4m3fn with scales")
+
+
 def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, workspace,
                           interleaved=False, rope_scale=1.0, positions=None, position_offset=0,
                           stream=None) -> None:
     """Append a step's keys and values to the paged cache and rotate its queries and keys;
     q and q_out may be None, freq (rope.fixed_point) None for no rotation.  q_out is q
-    itself or overlaps none of q, k and v.  See include/spec_verify.h."""
-    index, dtype, dim = cache.index, cache.dtype, cache.head_dim
+    itself or overlaps none of q, k and v.  To a cache in 8 bits q, k, v and q_out are
+    bfloat16 or float16 (spec_verify_kv_append_e4m3).  See include/spec_verify.h."""
+    index, dtype, dim, scales = cache.index, cache.dtype, cache.head_dim, cache.scales_ref
+    if scales is not None:
+        dtype, code = _rows16(k, "k")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     _index(k, "k")
@@ -558,8 +641,8 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     ks, vs = k.stride(), v.stride()
     if not (k.shape == shape and v.shape == shape and k.dtype is dtype and v.dtype is dtype
             and k.get_device() == index and v.get_device() == index and ks[2] == 1 and vs[2] == 1):
-        _heads(k, "k", cache, shape)
-        _heads(v, "v", cache, shape)
+        _heads(k, "k", cache, shape, dtype)
+        _heads(v, "v", cache, shape, dtype)
     heads, qp, qs, op, os_ = 0, None, None, None, None
     if q is not None:
         heads = q.shape[1]
@@ -568,8 +651,8 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
         if not (q.shape == shape and q_out.shape == shape and q.dtype is dtype and q_out.dtype is dtype
                 and q.get_device() == index and q_out.get_device() == index and qs[2] == 1
                 and os_[2] == 1):
-            _heads(q, "q", cache, shape)
-            _heads(q_out, "q_out", cache, shape)
+            _heads(q, "q", cache, shape, dtype)
+            _heads(q_out, "q_out", cache, shape, dtype)
         row, head = os_[0], os_[1]
         if ((rows > 1 and row < dim) or (heads > 1 and head < dim)
                 or (rows > 1 and heads > 1 and row < (heads - 1) * head + dim
@@ -580,6 +663,13 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
     if freq is not None:
         half = freq.numel()
         rot, fp = 2 * half, _arg(freq, "freq", torch.int64, (half,), index)
+    if scales is not None:
+        _launch((_lib or load_library()).spec_verify_kv_append_e4m3, index, stream,
+                qp, qs, heads, k.data_ptr(), _two(ks[0], ks[1]), v.data_ptr(), _two(vs[0], vs[1]), code, op, os_,
+                cache.ref, scales, cu, rows - cache.batch, max_drafts, fp, rot, 1 if interleaved else 0, rope_scale,
+                None if positions is None else _arg(positions, "positions", torch.int32, (rows,), index),
+                position_offset, _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
+        return
     _launch((_lib or load_library()).spec_verify_kv_append, index, stream,
             qp, qs, heads, k.data_ptr(), _two(ks[0], ks[1]), v.data_ptr(), _two(vs[0], vs[1]), op, os_,
             cache.ref, cu, rows - cache.batch, max_drafts, fp, rot, 1 if interleaved else 0, rope_scale,
@@ -587,16 +677,27 @@ def spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, wor
             position_offset, _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
 
 
+def spec_verify_kv_append_e4m3(q, k, v, cache, cu_draft, max_drafts, freq, q_out, workspace, **more) -> None:
+    """spec_verify_kv_append to a cache in 8 bits, and to no other: keys and values are stored as
+    codes with a scale for each block of tokens and head.  See include/spec_verify.h."""
+    _in_8_bits(cache)
+    spec_verify_kv_append(q, k, v, cache, cu_draft, max_drafts, freq, q_out, workspace, **more)
+
+
 def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix_table=None,
                           prefix_len=0, scale=None, draft_mask=None, lse=None, stream=None) -> None:
     """Attention of a step's rows over the paged cache (and a prefix that the batch shares);
-    scale None: head_dim ** -0.5; out may not lie within q.  See include/spec_verify.h."""
-    index = cache.index
+    scale None: head_dim ** -0.5; out may not lie within q.  Over a cache in 8 bits q and out
+    are bfloat16 or float16, the workspace is make_attention_e4m3_workspace's
+    (spec_verify_attention_e4m3).  See include/spec_verify.h."""
+    index, dtype, scales = cache.index, cache.dtype, cache.scales_ref
     _index(q, "q")
+    if scales is not None:
+        dtype, code = _rows16(q, "q")
     rows, heads = q.shape[0], q.shape[1]
     cu = _cu_rows(cu_draft, cache, rows)
     shape = (rows, heads, cache.head_dim)
-    qp, qs = _heads(q, "q", cache, shape)
+    qp, qs = _heads(q, "q", cache, shape, dtype)
     pt = mask = None
     if prefix_len > 0:
         if not isinstance(prefix_table, torch.Tensor) or prefix_table.numel() * cache.page_size < prefix_len:
@@ -606,12 +707,103 @@ def spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, prefix
         if getattr(draft_mask, "dtype", None) not in (torch.int32, torch.uint32):
             raise TypeError("draft_mask must be int32 or uint32 words")
         mask = _arg(draft_mask, "draft_mask", draft_mask.dtype, (rows,), index)
+    if scales is not None:
+        _launch((_lib or load_library()).spec_verify_attention_e4m3, index, stream,
+                qp, qs, heads, code, cache.ref, scales, pt, prefix_len, cu, rows - cache.batch, max_drafts,
+                cache.scale if scale is None else scale, mask, _arg(out, "out", dtype, shape, index),
+                None if lse is None else _arg(lse, "lse", torch.float32, (rows, heads), index),
+                _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
+        return
     _launch((_lib or load_library()).spec_verify_attention, index, stream,
             qp, qs, heads, cache.ref, pt, prefix_len, cu, rows - cache.batch, max_drafts,
             cache.scale if scale is None else scale, mask,
-            _arg(out, "out", cache.dtype, shape, index),
+            _arg(out, "out", dtype, shape, index),
             None if lse is None else _arg(lse, "lse", torch.float32, (rows, heads), index),
             _arg(workspace, "workspace", torch.uint8, None, index), workspace.numel())
+
+
+def spec_verify_attention_e4m3(q, cache, cu_draft, max_drafts, out, workspace, **more) -> None:
+    """spec_verify_attention over a cache in 8 bits, and over no other.  See
+    include/spec_verify.h."""
+    _in_8_bits(cache)
+    spec_verify_attention(q, cache, cu_draft, max_drafts, out, workspace, **more)
+
+
+class PagePool:
+    """Who holds which pages of a cache's pool, on the device: held [batch] (pages of each row of
+    the page table, its first ones), ref [num_pages] (rows that hold a page), free_pages
+    [num_pages] (the free pages, in its first entries) and free_count [1], all int32.
+
+    PagePool(cache) starts with every page free and rows that hold none;
+    PagePool.of_table(cache, held) takes up a page table that is filled already.  The tensors
+    may also be the caller's own (used in place; the attributes may not be assigned).
+    """
+    held = property(lambda self: self._tensors[0])
+    ref = property(lambda self: self._tensors[1])
+    free_pages = property(lambda self: self._tensors[2])
+    free_count = property(lambda self: self._tensors[3])
+
+    def __init__(self, cache, held=None, ref=None, free_pages=None, free_count=None):
+        n, B, index = cache.struct.num_pages, cache.batch, cache.index
+        dev, i32 = torch.device("cuda", index), torch.int32
+        if held is None:
+            held = torch.zeros((B,), dtype=i32, device=dev)
+        if ref is None:
+            ref = torch.zeros((n,), dtype=i32, device=dev)
+        if free_pages is None:
+            free_pages = torch.arange(n - 1, -1, -1, dtype=i32, device=dev)  # page 0 is taken first
+        if free_count is None:
+            free_count = torch.full((1,), n, dtype=i32, device=dev)
+        ptrs = (_arg(held, "held", i32, (B,), index) or None, _arg(ref, "ref", i32, (n,), index),
+                _arg(free_pages, "free_pages", i32, (n,), index), _arg(free_count, "free_count", i32, (1,), index))
+        self.struct = _PagePool(*ptrs)
+        self.ref_struct = ctypes.byref(self.struct)
+        self._tensors = (held, ref, free_pages, free_count)
+        size = int(load_library().spec_verify_pages_workspace_size(n, B, cache.struct.max_pages))
+        if size == 0:
+            raise ValueError(f"no page pool for {B} rows of {cache.struct.max_pages} pages")
+        self.workspace = torch.zeros(size, dtype=torch.uint8, device=dev)
+
+    @classmethod
+    def of_table(cls, cache, held, prefix_table=None):
+        """The pool of a page table whose rows hold their first held[b] entries already;
+        a prefix that the batch shares counts as a row of its own.  (Synchronises.)"""
+        n = cache.struct.num_pages
+        held = held.to(torch.int32)
+        table = cache.page_table
+        mine = torch.arange(table.shape[1], device=table.device)[None, :] < held[:, None]
+        pages = table[mine].long()
+        if prefix_table is not None:
+            pages = torch.cat([pages, prefix_table.long().flatten()])
+        if pages.numel() and (int(pages.min()) < 0 or int(pages.max()) >= n):
+            raise ValueError("the rows hold pages outside the pool")
+        ref = torch.bincount(pages, minlength=n).int()
+        free = (ref == 0).nonzero()[:, 0].flip(0).int()
+        room = torch.full((n,), -1, dtype=torch.int32, device=table.device)
+        room[:free.numel()] = free
+        count = torch.full((1,), free.numel(), dtype=torch.int32, device=table.device)
+        return cls(cache, held.contiguous(), ref, room, count)
+
+
+def spec_verify_pages_step(cache, pool, tokens, parents=None, stream=None) -> None:
+    """The page table of the next step: row b continues row parents[b] (-1: it ends; None: every
+    row itself), gives back what lies behind its tokens and holds pages for tokens[b] more, with
+    a copy of a partly filled page that others hold.  The status word is in pool.workspace.
+    See include/spec_verify.h."""
+    index, i32, shape = cache.index, torch.int32, (cache.batch,)
+    _launch((_lib or load_library()).spec_verify_pages_step, index, stream, cache.ref,
+            cache.scales_ref, pool.ref_struct,
+            None if parents is None else _arg(parents, "parents", i32, shape, index),
+            _arg(tokens, "tokens", i32, shape, index), pool.workspace.data_ptr(), pool.workspace.numel())
+
+
+def spec_verify_pages_compact(cache, pool, remap, stream=None) -> None:
+    """The pages in use move to the front of the pool; remap [num_pages] int32 receives each
+    page's new place (-1: it was free).  See include/spec_verify.h."""
+    _launch((_lib or load_library()).spec_verify_pages_compact, cache.index, stream, cache.ref,
+            cache.scales_ref, pool.ref_struct,
+            _arg(remap, "remap", torch.int32, (cache.struct.num_pages,), cache.index), pool.workspace.data_ptr(),
+            pool.workspace.numel())
 
 
 def spec_verify_status(workspace, stream=None) -> int:

@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspec_verify.so")
 SOURCES = [os.path.join(PKG, "csrc", n + ".cu")
-           for n in ("spec_verify", "probs", "kv_append", "attention")]
+           for n in ("spec_verify", "probs", "kv_append", "attention", "kv_append_e4m3", "attention_e4m3", "pages")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
