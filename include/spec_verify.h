@@ -479,8 +479,8 @@ int spec_verify_pages_compact(const sv_kv_cache *cache, const sv_kv_scales *scal
  * 4 bytes before the first use); any q_heads that kv_heads divides; a score scale q . k
  * with its keys' scale stays below 2^27 in magnitude; a query row with an infinity or NaN
  * gives NaN.  Queries enter the product as sums of 8-bit floats that hold every
- * value to 2^-21 of its head's largest; weights times their values' scales are rounded as fp16 and
- * by at most 2^-9 of themselves, or 2^-30 of the row's largest.
+ * value to 2^-21 of its head's largest; weights times their values' scales are rounded as fp16:
+ * by at most 2^-11 of themselves, or 2^-30 of the row's largest.
  */
 size_t spec_verify_attention_e4m3_workspace_size(int total_rows, int q_heads, int head_dim);
 int spec_verify_attention_e4m3(const void *q, const int64_t *q_strides, int q_heads,

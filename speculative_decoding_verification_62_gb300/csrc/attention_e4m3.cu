@@ -11,10 +11,11 @@
 // widened.  The other operands are sums of 8-bit floats:
 // - queries: q / f = e4m3 + e5m2 (bf16: exact for values within 2^-13 of the row's largest, and
 //   off by 2^-21 of it at most), fp16 a second e5m2;
-// - weights: rounded to fp16, whose three leading bits are an e5m2, as are the next three, and
-//   what is left is rounded to one: off by 2^-9 of the weight at most.  The maximum of the
-//   weights lies in [2^13, 2^15] at all times after its tile, so that e5m2's smallest
-//   step, 2^-16, is 2^-29 of it.
+// - weights: rounded to fp16, that to the nearest e5m2, what is left to the nearest again, and what is left
+//   then, 2^-7 of the weight's power of two at most and a multiple of 2^-10 of it, is an e5m2: the sum is
+//   the fp16, off by 2^-11 of the weight at most.  (With the first two cut off instead of rounded,
+//   three terms hold nine of its eleven bits.)  The maximum of the weights lies in [2^13, 2^15] at all times
+//   after its tile, so that e5m2's smallest step, 2^-16, is 2^-29 of it.
 // Each product is two or three products of kind::f8f6f4, into one 32-bit accumulator.
 //
 // Work: a unit is (request, up to kN rows of queries, key head) over the request's own keys, or
@@ -328,6 +329,9 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
+// The nearest e5m2 of two halves (ties away from zero), in their upper bytes: half a step of those on
+// top of the bits.  (A NaN turns into -0 here, and stays with what is left.)
+__device__ __forceinline__ uint32_t nearest_e5m2(uint32_t h) { return h + 0x00800080u; }
 __device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -885,16 +889,17 @@ __device__ __forceinline__ void soften(const Params& P, const Piece& p, Control*
         h[y / 2] = half2_of(a, b);
         h[y / 2 + 1] = half2_of(e, g);
       }
-      // an fp16's upper byte is an e5m2
       uint4 code[3];
       uint32_t* first = reinterpret_cast<uint32_t*>(code);
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         uint32_t a = h[2 * y], b = h[2 * y + 1];
-        first[y] = __byte_perm(a, b, 0x7531);
-        a = half2_sub(a, a & 0xff00ff00u), b = half2_sub(b, b & 0xff00ff00u);
-        first[4 + y] = __byte_perm(a, b, 0x7531);
-        a = half2_sub(a, a & 0xff00ff00u), b = half2_sub(b, b & 0xff00ff00u);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t an = nearest_e5m2(a), bn = nearest_e5m2(b);
+          first[4 * k + y] = __byte_perm(an, bn, 0x7531);
+          a = half2_sub(a, an & 0xff00ff00u), b = half2_sub(b, bn & 0xff00ff00u);
+        }
         first[8 + y] = __byte_perm(e5m2x2_half(a), e5m2x2_half(b), 0x5410);
       }
 #pragma unroll
