@@ -542,6 +542,7 @@ class PagedCache:
             self.scales_ref = ctypes.byref(self._scales)
         self._tensors = (k_pages, v_pages, page_table, kv_len, k_scales, v_scales)
         self.cu_shape = (B + 1,)
+        self.sizes = (self.index, n, B, width)  # device, pages, rows, pages of a row
         self.batch, self.kv_heads, self.head_dim, self.dtype = B, heads, dim, k_pages.dtype
         self.page_size, self.scale = page, dim ** -0.5
         ptr = lambda t: t.data_ptr() if t.numel() else None  # noqa: E731
@@ -736,7 +737,8 @@ class PagePool:
 
     PagePool(cache) starts with every page free and rows that hold none;
     PagePool.of_table(cache, held) takes up a page table that is filled already.  The tensors
-    may also be the caller's own (used in place; the attributes may not be assigned).
+    may also be the caller's own, all four (used in place; the attributes may not be assigned).
+    A pool serves caches of the device, pages, rows and table width that it was made for.
     """
     held = property(lambda self: self._tensors[0])
     ref = property(lambda self: self._tensors[1])
@@ -744,24 +746,24 @@ class PagePool:
     free_count = property(lambda self: self._tensors[3])
 
     def __init__(self, cache, held=None, ref=None, free_pages=None, free_count=None):
-        n, B, index = cache.struct.num_pages, cache.batch, cache.index
+        self.sizes = index, n, B, width = cache.sizes
+        given = [t is not None for t in (held, ref, free_pages, free_count)]
+        if any(given) and not all(given):  # (they describe one state)
+            raise ValueError("held, ref, free_pages and free_count go together")
         dev, i32 = torch.device("cuda", index), torch.int32
         if held is None:
             held = torch.zeros((B,), dtype=i32, device=dev)
-        if ref is None:
             ref = torch.zeros((n,), dtype=i32, device=dev)
-        if free_pages is None:
             free_pages = torch.arange(n - 1, -1, -1, dtype=i32, device=dev)  # page 0 is taken first
-        if free_count is None:
             free_count = torch.full((1,), n, dtype=i32, device=dev)
         ptrs = (_arg(held, "held", i32, (B,), index) or None, _arg(ref, "ref", i32, (n,), index),
                 _arg(free_pages, "free_pages", i32, (n,), index), _arg(free_count, "free_count", i32, (1,), index))
         self.struct = _PagePool(*ptrs)
         self.ref_struct = ctypes.byref(self.struct)
         self._tensors = (held, ref, free_pages, free_count)
-        size = int(load_library().spec_verify_pages_workspace_size(n, B, cache.struct.max_pages))
+        size = int(load_library().spec_verify_pages_workspace_size(n, B, width))
         if size == 0:
-            raise ValueError(f"no page pool for {B} rows of {cache.struct.max_pages} pages")
+            raise ValueError(f"no page pool for {B} rows of {width} pages")
         self.workspace = torch.zeros(size, dtype=torch.uint8, device=dev)
 
     @classmethod
@@ -785,11 +787,18 @@ class PagePool:
         return cls(cache, held.contiguous(), ref, room, count)
 
 
+def _of_one_size(cache, pool):
+    if pool.sizes != cache.sizes:
+        raise ValueError("the pool was made for another cache: device, pages, rows and table width are "
+                         f"{pool.sizes}, the cache's {cache.sizes}")
+
+
 def spec_verify_pages_step(cache, pool, tokens, parents=None, stream=None) -> None:
     """The page table of the next step: row b continues row parents[b] (-1: it ends; None: every
     row itself), gives back what lies behind its tokens and holds pages for tokens[b] more, with
     a copy of a partly filled page that others hold.  The status word is in pool.workspace.
     See include/spec_verify.h."""
+    _of_one_size(cache, pool)
     index, i32, shape = cache.index, torch.int32, (cache.batch,)
     _launch((_lib or load_library()).spec_verify_pages_step, index, stream, cache.ref,
             cache.scales_ref, pool.ref_struct,
@@ -800,6 +809,7 @@ def spec_verify_pages_step(cache, pool, tokens, parents=None, stream=None) -> No
 def spec_verify_pages_compact(cache, pool, remap, stream=None) -> None:
     """The pages in use move to the front of the pool; remap [num_pages] int32 receives each
     page's new place (-1: it was free).  See include/spec_verify.h."""
+    _of_one_size(cache, pool)
     _launch((_lib or load_library()).spec_verify_pages_compact, cache.index, stream, cache.ref,
             cache.scales_ref, pool.ref_struct,
             _arg(remap, "remap", torch.int32, (cache.struct.num_pages,), cache.index), pool.workspace.data_ptr(),
