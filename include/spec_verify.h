@@ -443,8 +443,8 @@ size_t spec_verify_pages_workspace_size(int num_pages, int batch, int max_pages)
  *              append (scales NULL for 16 bits)
  *   parents    optional device int32 [batch]
  *   tokens     device int32 [batch], >= 0 (a verify step: gamma_b + 1)
- *   workspace  zero-filled once; every call leaves it so, but for the status word.  One call
- *              at a time, in order on one stream.
+ *   workspace  zero its first 4 bytes before the first use; the rest is scratch, also one that
+ *              served another pool.  One call at a time, in order on one stream.
  * Pages that no row holds any more go back to free_pages in the order of the rows and places that
  * held them; pages are then taken from its end, in the order of the rows, a row's copy
  * first.  So results repeat, whatever runs beside.  Where the takes need more than there

@@ -46,7 +46,8 @@ struct PagesParams {
   float* v_scales;
   int block;
   unsigned int* status;
-  // scratch: zero between the calls
+  // scratch, cleared for the pages that a call looks at (a workspace may have served another
+  // number of pages, whose arrays began elsewhere)
   int32_t* first;       // [num_pages]: INT_MAX less the first place that dropped a page
   int32_t* lowest;      // [num_pages]: INT_MAX less the lowest row that writes to a page
   int32_t* writers;     // [num_pages]: rows that do
@@ -151,7 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1) step_kernel(const __grid_constant
 #pragma unroll 4
     for (int j = (r.stays ? r.live : 0) + lane; j < r.held; j += 32) {
       const int p = mine[j];
-      if (fits(p)) atomicSub(P.ref + p, 1);
+      if (fits(p)) {
+        atomicSub(P.ref + p, 1);
+        P.first[p] = 0;
+      }
     }
     if (!r.stays) {
 #pragma unroll 4
@@ -166,7 +170,15 @@ __global__ void __launch_bounds__(kThreads, 1) step_kernel(const __grid_constant
     }
     if (lane == 0) {
       P.rows[b] = make_int4(r.kv, r.live, r.need, r.held);
-      P.more[b].w = r.n > 0 && r.kv % P.page_size;  // whether it writes behind older tokens
+      int page = -1;  // the page of older tokens that it writes behind
+      if (r.n > 0 && r.kv % P.page_size) {
+        page = (r.stays ? mine : from)[r.kv / P.page_size];
+        if (fits(page))
+          P.writers[page] = P.lowest[page] = 0;
+        else
+          page = -1;
+      }
+      P.more[b].w = page;
     }
   }
   cluster_sync();
@@ -183,17 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1) step_kernel(const __grid_constant
       if (fits(p) && __ldcg(P.ref + p) == 0) atomicMax(P.first + p, INT32_MAX - (b * P.W + j));
     }
     if (lane == 0) {
-      int page = -1;
-      if (__ldcg(&P.more[b].w)) {
-        page = stays ? mine[r.x / P.page_size] : __ldcg(P.entries + (size_t)b * P.W + r.x / P.page_size);
-        if (!fits(page) || __ldcg(P.ref + page) <= 1) {
-          page = -1;
-        } else {
-          atomicAdd(P.writers + page, 1);
-          atomicMax(P.lowest + page, INT32_MAX - b);
-        }
+      const int page = __ldcg(&P.more[b].w);
+      if (page >= 0 && __ldcg(P.ref + page) <= 1) {
+        P.more[b].w = -1;
+      } else if (page >= 0) {
+        atomicAdd(P.writers + page, 1);
+        atomicMax(P.lowest + page, INT32_MAX - b);
       }
-      P.more[b].w = page;
     }
   }
   cluster_sync();
