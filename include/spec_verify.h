@@ -452,7 +452,9 @@ size_t spec_verify_pages_workspace_size(int num_pages, int batch, int max_pages)
  * (SV_STATUS_NO_PAGES; the step must not be appended: a later call, after other rows have
  * ended, takes them).  A kv_len past the pages held counts as what they hold, tokens past
  * the page table or below 0 as 0 (SV_STATUS_BAD_LENGTH); entries outside the pool are
- * neither counted nor copied (SV_STATUS_BAD_PAGE).
+ * neither counted nor copied (SV_STATUS_BAD_PAGE, for entries that are given back, that
+ * another row takes up, and of a page that is written behind older tokens; the call
+ * looks at no others).
  */
 int spec_verify_pages_step(const sv_kv_cache *cache, const sv_kv_scales *scales,
                            const sv_page_pool *pool, const int32_t *parents,

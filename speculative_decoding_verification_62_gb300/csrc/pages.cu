@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_kernel(const __grid_constant
       if (fits(p)) {
         atomicSub(P.ref + p, 1);
         P.first[p] = 0;
+      } else {
+        flags |= SV_STATUS_BAD_PAGE;
       }
     }
     if (!r.stays) {
@@ -173,10 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1) step_kernel(const __grid_constant
       int page = -1;  // the page of older tokens that it writes behind
       if (r.n > 0 && r.kv % P.page_size) {
         page = (r.stays ? mine : from)[r.kv / P.page_size];
-        if (fits(page))
+        if (fits(page)) {
           P.writers[page] = P.lowest[page] = 0;
-        else
+        } else {
+          flags |= SV_STATUS_BAD_PAGE;
           page = -1;
+        }
       }
       P.more[b].w = page;
     }

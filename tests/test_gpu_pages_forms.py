@@ -62,3 +62,52 @@ def test_one_workspace_for_pools_of_other_sizes():
                 w.set_len([k + rng.randint(0, t) if p >= 0 else 0 for k, t, p in zip(w.model.kv, tokens, parents)])
             if turn % 3 == 2:
                 w.compact()
+
+
+@pytest.mark.parametrize("bad", [1000, 20, -1, -2 ** 31])
+@pytest.mark.parametrize("own_parents", [False, True])
+def test_bad_entries_of_rows_that_continue_themselves(own_parents, bad):
+    w = Pool(3, 4, 20)
+    parents = ints([0, 1, 2]) if own_parents else None
+    w.step([20, 20, 20])
+    w.set_len([20, 20, 20])
+    w.cache.page_table[1, 1] = w.model.table[1][1] = bad
+    bytes_ = [x.clone() for x in w.everything()]
+    # the page that row 1 writes to behind 4 tokens
+    binding.spec_verify_pages_step(w.cache, w.pool, ints([1, 13, 1]), parents)
+    assert binding.spec_verify_status(w.pool.workspace) == S["BAD_PAGE"]
+    w.model.table[1][2] = w.model.free.pop()  # (its third page is taken all the same)
+    w.model.ref[w.model.table[1][2]] = 1
+    w.model.held = [2, 3, 2]
+    w.same()
+    # given back: it counts for no page
+    w.set_len([20, 7, 20])
+    binding.spec_verify_pages_step(w.cache, w.pool, ints([1, 1, 1]), parents)
+    assert binding.spec_verify_status(w.pool.workspace) == S["BAD_PAGE"]
+    w.model.free.append(w.model.table[1][2])
+    w.model.ref[w.model.table[1][2]] = 0
+    w.model.table[1][1:3] = [-1, -1]
+    w.model.held = [2, 1, 2]
+    w.same()
+    w.step([1, 1, 1])
+    for x, y in zip(w.everything(), bytes_):
+        assert torch.equal(x, y)
+
+
+def test_bad_entries_that_forks_take_up():
+    """A parent's entry outside the pool: status, and tables and counts as without that page."""
+    w = Pool(3, 4, 20)
+    w.step([20, 20, 20])
+    w.set_len([20, 20, 20])
+    table, ref, free = [list(r) for r in w.model.table], list(w.model.ref), list(w.model.free)
+    w.cache.page_table[1, 0] = 1000
+    binding.spec_verify_pages_step(w.cache, w.pool, ints([0, 0, 0]), ints([1, 1, 1]))
+    assert binding.spec_verify_status(w.pool.workspace) == S["BAD_PAGE"]
+    shared = table[1][1]
+    gone = [table[0][0], table[0][1], table[2][0], table[2][1]]
+    for p in gone:
+        ref[p] = 0
+    ref[shared] = 3
+    w.model.table = [[1000, shared, -1, -1] for _ in range(3)]
+    w.model.ref, w.model.free = ref, free + gone
+    w.same()
