@@ -468,7 +468,7 @@ int spec_verify_pages_step(const sv_kv_cache *cache, const sv_kv_scales *scales,
  * follow.
  *   remap  device int32 [num_pages]: where each page is now (-1: it was free), for tables
  *          that the caller keeps (a shared prefix's)
- * Arguments as above.
+ * Arguments as above; with batch 0 what a prefix holds moves all the same.
  */
 int spec_verify_pages_compact(const sv_kv_cache *cache, const sv_kv_scales *scales,
                               const sv_page_pool *pool, int32_t *remap, void *workspace,

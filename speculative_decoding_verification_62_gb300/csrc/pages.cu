@@ -483,8 +483,9 @@ PagesLayout pages_layout(size_t pages, size_t B, size_t W) {
   return L;
 }
 
+// (A call about rows alone has nothing to do for none of them.)
 int make_params(PagesParams& P, const sv_kv_cache* cache, const sv_kv_scales* scales, const sv_page_pool* pool,
-                void* workspace, size_t ws_bytes) {
+                void* workspace, size_t ws_bytes, bool rows_alone) {
   if (!cache || !pool) return SV_ERR_NULL;
   const sv_kv_cache& c = *cache;
   if (c.dtype == SV_E4M3 && !scales) return SV_ERR_NULL;
@@ -494,8 +495,15 @@ int make_params(PagesParams& P, const sv_kv_cache* cache, const sv_kv_scales* sc
       (long long)c.max_pages * c.page_size > INT32_MAX ||
       (long long)c.page_size * c.kv_heads * c.head_dim > INT32_MAX / 2)
     return SV_ERR_SCALAR;
-  if (c.batch == 0) return SV_OK;
-  if (!pool->held || !pool->ref || !pool->free_pages || !pool->free_count || !workspace) return SV_ERR_NULL;
+  if (c.batch == 0) {
+    if (rows_alone) return SV_OK;
+    // (the pools' addresses are checked with the rows')
+    if (!c.k_pages || !c.v_pages || (c.dtype == SV_E4M3 && (!scales->k || !scales->v))) return SV_ERR_NULL;
+    if (!sv::aligned(c.k_pages, 16) || !sv::aligned(c.v_pages, 16) ||
+        (c.dtype == SV_E4M3 && (!sv::aligned(scales->k, 4) || !sv::aligned(scales->v, 4))))
+      return SV_ERR_ALIGN;
+  }
+  if ((c.batch > 0 && !pool->held) || !pool->ref || !pool->free_pages || !pool->free_count || !workspace) return SV_ERR_NULL;
   for (const void* p : {pool->held, pool->ref, pool->free_pages, pool->free_count})
     if (!sv::aligned(p, 4)) return SV_ERR_ALIGN;
   if (!sv::aligned(workspace, 256)) return SV_ERR_ALIGN;
@@ -571,7 +579,7 @@ int spec_verify_pages_step(const sv_kv_cache* cache, const sv_kv_scales* scales,
                            const int32_t* parents, const int32_t* tokens, void* workspace, size_t ws_bytes,
                            sv_stream_t stream) {
   PagesParams P = {};
-  int rc = make_params(P, cache, scales, pool, workspace, ws_bytes);
+  int rc = make_params(P, cache, scales, pool, workspace, ws_bytes, true);
   if (rc || P.B == 0) return rc;
   if (!tokens) return SV_ERR_NULL;
   if (!sv::aligned(tokens, 4) || !sv::aligned(parents, 4)) return SV_ERR_ALIGN;
@@ -587,8 +595,8 @@ int spec_verify_pages_step(const sv_kv_cache* cache, const sv_kv_scales* scales,
 int spec_verify_pages_compact(const sv_kv_cache* cache, const sv_kv_scales* scales, const sv_page_pool* pool,
                               int32_t* remap, void* workspace, size_t ws_bytes, sv_stream_t stream) {
   PagesParams P = {};
-  int rc = make_params(P, cache, scales, pool, workspace, ws_bytes);
-  if (rc || P.B == 0) return rc;
+  int rc = make_params(P, cache, scales, pool, workspace, ws_bytes, false);
+  if (rc) return rc;
   if (!remap) return SV_ERR_NULL;
   if (!sv::aligned(remap, 4)) return SV_ERR_ALIGN;
   P.remap = remap;

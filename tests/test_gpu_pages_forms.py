@@ -111,3 +111,25 @@ def test_bad_entries_that_forks_take_up():
     w.model.table = [[1000, shared, -1, -1] for _ in range(3)]
     w.model.ref, w.model.free = ref, free + gone
     w.same()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_prefix_moves_without_rows(kind):
+    w = Pool(2, 3, 30, kind=kind)
+    c = w.cache
+    more = dict(k_scales=w.scales[0], v_scales=w.scales[1]) if w.scales else {}
+    empty = binding.PagedCache(c.k_pages, c.v_pages, c.page_table[:0], c.kv_len[:0], **more)
+    prefix = ints([20, 3, 29, 0, 11])
+    pool = binding.PagePool.of_table(empty, ints([]), prefix)
+    before = [x.clone() for x in w.everything()]
+    remap = torch.full((30,), -7, dtype=torch.int32, device="cuda")
+    binding.spec_verify_pages_compact(empty, pool, remap)
+    assert binding.spec_verify_status(pool.workspace) == 0
+    assert remap.tolist() == [{0: 0, 3: 3, 11: 1, 20: 2, 29: 4}.get(p, -1) for p in range(30)]
+    assert pool.ref.tolist() == [1] * 5 + [0] * 25 and int(pool.free_count) == 25
+    assert pool.free_pages[:25].tolist() == list(range(29, 4, -1))
+    for now, was in zip(w.everything(), before):
+        assert torch.equal(now[remap[prefix.long()].long()], was[prefix.long()])
+    # a step of no rows does nothing
+    binding.spec_verify_pages_step(empty, pool, ints([]))
+    assert int(pool.free_count) == 25
