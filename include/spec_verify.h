@@ -482,7 +482,8 @@ int spec_verify_pages_compact(const sv_kv_cache *cache, const sv_kv_scales *scal
  * with its keys' scale stays below 2^27 in magnitude; a query row with an infinity or NaN
  * gives NaN.  Queries enter the product as sums of 8-bit floats that hold every
  * value to 2^-21 of its head's largest; weights times their values' scales are rounded as fp16:
- * by at most 2^-11 of themselves, or 2^-30 of the row's largest.
+ * by at most 2^-11 of themselves, or 2^-30 of the row's largest (from scores of 2^20 in magnitude
+ * on less good than that, 2^-14 of it near 2^27).
  */
 size_t spec_verify_attention_e4m3_workspace_size(int total_rows, int q_heads, int head_dim);
 int spec_verify_attention_e4m3(const void *q, const int64_t *q_strides, int q_heads,

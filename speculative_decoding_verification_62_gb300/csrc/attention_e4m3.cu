@@ -53,6 +53,7 @@ constexpr int kMaxList = 1 << 30;
 constexpr float kNone = -3.0e38f;  // a maximum of nothing
 constexpr float kTop = 13.f;       // log2 of the largest weight where the maximum just moved
 constexpr float kLimit = 15.f;     // and where it moves
+constexpr float kFar = 0x1p20f;    // logarithms from here on are rounded by 2^-4 and more
 constexpr unsigned long long kDrainNs = 2000000000ull;  // limit of the waits that end an aborted CTA
 
 template <typename T>
@@ -507,7 +508,7 @@ struct Control {
   uint64_t kv_full[2][kStages], kv_empty[2][kStages];  // keys, values
   uint64_t q_full, s_full[2], p_ready, pv_done, drain;
   uint32_t tmem;
-  int abort;
+  int abort, far;  // far: of the last moves of the maxima, one was by kFar or more
   unsigned int copied[2];
   int scan[kThreads / 32];
   Walk start;
@@ -803,12 +804,16 @@ __device__ __forceinline__ void soften(const Params& P, const Piece& p, Control*
         }
       }
     };
+    int moves = 0;       // of the maxima, in this tile
+    bool moved = false;  // this thread's column
+  formed:
     form();
     float over = -INFINITY;
 #pragma unroll
     for (int x = 0; x < 16 * CH; x += 2) over = max3(over, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-    if (any_of(over > kLimit || forced || !st.ok)) {
-      // the maxima move
+    if (any_of((over > kLimit && moves < 4) || (moves == 0 ? forced : moves == 1 && c->far) || !st.ok)) {
+      // The maxima move, and the logarithms are formed again.  Far from zero the first were rounded, by as
+      // much as 16 each way, and so was what moved: it moves once more, by what is small and good now.
       if (any_of(!st.ok)) {
         st.ok = false;
         return;
@@ -823,25 +828,27 @@ __device__ __forceinline__ void soften(const Params& P, const Piece& p, Control*
         }
         if (lane < 16) c->most[warp][x + lane] = mine;
       }
+      if (tid == 0) c->far = 0;
       (void)any_of(false);
       if (tid < 16 * CH) {
         // over the old maximum (NaN left out)
         const float top = fmaxf(fmaxf(c->most[0][tid], c->most[1][tid]), fmaxf(c->most[2][tid], c->most[3][tid]));
         const float was = c->top[tid];
         float f = 1.f;
-        if (was == kNone ? top > -INFINITY : top > kLimit) {
-          // (rounded up: no weight passes 2^kTop now)
+        if (was == kNone ? top > -INFINITY : top > kLimit || (moved && top > -INFINITY)) {
+          // (rounded up: no weight passes 2^kTop, but for the rounding of a far `top`)
           const float now = was == kNone ? __fadd_ru(top, -kTop) : __fadd_ru(was, __fadd_ru(top, -kTop));
           f = exp2_fast(was - now);
+          moved = true;
+          if (fabsf(top) >= kFar) c->far = 1;
           c->top[tid] = now;
           c->neg[tid] = -now;
         }
         c->scale[tid] = f;
       }
       forced = any_of(tid < p.cols && c->top[tid] == kNone);
-      form();
       if (i > 0) {
-        st.ok = warp_wait(&c->pv_done, (tile - 1) & 1, P, c);
+        st.ok = warp_wait(&c->pv_done, (tile - 1) & 1, P, c) && st.ok;
         fence_after();
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
@@ -861,6 +868,8 @@ __device__ __forceinline__ void soften(const Params& P, const Piece& p, Control*
         tmem_wait_store();
         fence_before();
       }
+      ++moves;
+      goto formed;
     }
     if (i > 0) st.ok = warp_wait(&c->pv_done, (tile - 1) & 1, P, c) && st.ok;  // the weights' place is free
     // The value rows behind the last key of its 32 hold what memory held there, and weights of 0
