@@ -481,7 +481,7 @@ int spec_verify_pages_compact(const sv_kv_cache *cache, const sv_kv_scales *scal
  * 4 bytes before the first use); any q_heads that kv_heads divides; a score scale q . k
  * with its keys' scale stays below 2^27 in magnitude; a query row with an infinity or NaN
  * gives NaN.  Queries enter the product as sums of 8-bit floats that hold every
- * value to 2^-21 of its head's largest; weights times their values' scales are rounded as fp16:
+ * value to 2^-21 of its head's largest, or of 2^-93; weights times their values' scales are rounded as fp16:
  * by at most 2^-11 of themselves, or 2^-30 of the row's largest (from scores of 2^20 in magnitude
  * on less good than that, 2^-14 of it near 2^27).
  */

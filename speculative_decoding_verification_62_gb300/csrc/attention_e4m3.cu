@@ -694,9 +694,9 @@ __device__ __forceinline__ void queries(const Params& P, const Piece& p, Control
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // q 2^e has its largest in [2^7, 2^8)
+      // q 2^e has its largest in [2^7, 2^8) (from 2^-93 on)
       int e = 134 - (int)(top >> 23);
-      e = top == 0 ? 0 : e > 100 ? 100 : e < -100 ? -100 : e;
+      e = top == 0 ? 0 : e > 100 ? 100 : e < -120 ? -120 : e;
       const float up = __uint_as_float((uint32_t)(e + 127) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
       uint32_t code[kTerms][4];
 #pragma unroll
@@ -718,7 +718,7 @@ __device__ __forceinline__ void queries(const Params& P, const Piece& p, Control
         *reinterpret_cast<uint2*>(at + x * Smem<T>::q_term) =
             finite ? make_uint2(code[x][0] | (code[x][1] << 16), code[x][2] | (code[x][3] << 16))
                    : make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      if (in == 0) c->factor[n] = P.sl2 * down;
+      if (in == 0) c->factor[n] = fminf(P.sl2 * down, 0x1p127f);  // (finite: keys of zeros score 0)
     }
   }
 }

@@ -8,6 +8,7 @@ import torch
 from cache8_refs import values
 from operator_refs import attend
 from speculative_decoding_verification_62_gb300 import binding
+import test_gpu_attention_e4m3
 from test_gpu_attention_e4m3 import DT, S, Batch, ints, tolerance
 
 pytestmark = pytest.mark.gpu
@@ -19,6 +20,13 @@ def tight(q, k, o, lse, spread, size, weight, scale, lv, dtype):
     after them has three bits)."""
     tol, tl = tolerance(q, k, o, lse, spread, size, weight, scale, lv, dtype)
     return tol - (2.0 ** -9 * 1.13 - 2.0 ** -11) * 1.01 * spread, tl
+
+
+def check(w, out, lse, mask=None, scale=None, only=None):
+    """Batch.check with tight()."""
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(test_gpu_attention_e4m3, "tolerance", tight)
+        return w.check(out, lse, mask, scale, only)
 
 
 @pytest.mark.parametrize("seed", [1, 2, 3])
@@ -88,3 +96,22 @@ def test_scores_far_from_zero(scale, total, dtype):
         u = torch.finfo(w.dtype).eps / 2
         err = (out[rows].double() - o).abs()
         assert not ((err > (u + 2.0 ** -11 + 2.0 ** -14) * 1.01 * o.abs() + 2.0 ** -25) & alone[..., None]).any()
+
+
+@pytest.mark.parametrize("power, scale_power", [(115, -116), (122, -122), (100, -102), (-90, 92), (-93, 95)])
+def test_queries_of_any_size(power, scale_power):
+    """bf16 queries of 2^power whose scores are ordinary by the scale."""
+    w = Batch([300, 77, 5], [3, 1, 0], 4, 2, 64, 16, 16, "bf16", seed=9)
+    w.q.mul_(2.0 ** power)
+    out, lse = w.run(scale=2.0 ** scale_power)
+    check(w, out, lse, scale=2.0 ** scale_power)
+
+
+def test_keys_of_zeros_under_huge_queries():
+    """Whatever the queries and the scale, keys of zeros score 0: the values' mean."""
+    w = Batch([40], [0], 2, 1, 64, 16, 16, "bf16", spread=0)
+    w.bytes[0].zero_()
+    w.k[0].zero_()
+    w.q.fill_(2.0 ** 127)
+    out, lse = w.run(scale=2.0 ** 20)
+    check(w, out, lse, scale=2.0 ** 20)
