@@ -7,6 +7,8 @@
 //   s  = smallest 2^e, -32 <= e <= 56, with m2 <= (448 2^e)^2; at least the old scale
 //        where the block holds older tokens
 //   code = rn_e4m3(x / s);  older codes: rn_e4m3(code s_old / s)
+// (The rotation's factor counts: its power of two before the squares, which so overflow or vanish only
+// where s ends, what is left of it behind them.)
 // A turn leaves a^2 + c^2, so that the scale is known before any angle, and no rounding of
 // an angle can move it: products of 16-bit values are exact in 32 bits and their sum is
 // rounded once.  (Of a power of two too much a code of 3 mantissa bits loses nothing
@@ -19,7 +21,7 @@
 #include "append.h"
 #include "internal.h"
 
-#include <atomic>
+#include <cmath>
 
 namespace {
 
@@ -48,7 +50,7 @@ struct Append8Params {
   const long long* freq;
   const int32_t* positions;
   int offset;
-  float scale;
+  float scale, power, rest2;  // the rotation's factor; its square is power^2 rest2, power a power of two
   unsigned int* status;
 };
 
@@ -183,10 +185,12 @@ __device__ __forceinline__ void turned(const Words<VW>& w, const Place& p, const
 }
 // The largest square of a value or of a turning pair's length (NaN left out)
 template <typename T, int VW, bool INTER>
-__device__ __forceinline__ float squares(const Words<VW>& w, const Place& p, float scale2) {
+__device__ __forceinline__ float squares(const Words<VW>& w, const Place& p, float power, float rest2) {
   float pairs = 0.f, single = 0.f;
+  const float by = p.turns ? power : 1.f;
   if constexpr (VW == 1) {
-    const float2 a = Conv<T>::up((unsigned int)w.x | ((unsigned int)w.y << 16));
+    float2 a = Conv<T>::up((unsigned int)w.x | ((unsigned int)w.y << 16));
+    a.x *= by, a.y *= by;
     if (p.turns)
       pairs = fmaf(a.x, a.x, a.y * a.y);
     else
@@ -194,7 +198,8 @@ __device__ __forceinline__ float squares(const Words<VW>& w, const Place& p, flo
   } else {
 #pragma unroll
     for (int i = 0; i < VW / 2; ++i) {
-      const float2 a = Conv<T>::up(w.x.w[i]), b = Conv<T>::up(w.y.w[i]);
+      float2 a = Conv<T>::up(w.x.w[i]), b = Conv<T>::up(w.y.w[i]);
+      a.x *= by, a.y *= by, b.x *= by, b.y *= by;
       const float ax = a.x * a.x, bx = b.x * b.x;
       if (p.turns)
         pairs = fmaxf(pairs, INTER ? fmaxf(fmaf(a.y, a.y, ax), fmaf(b.y, b.y, bx))
@@ -203,7 +208,7 @@ __device__ __forceinline__ float squares(const Words<VW>& w, const Place& p, flo
         single = fmaxf(single, fmaxf(fmaxf(ax, a.y * a.y), fmaxf(bx, b.y * b.y)));
     }
   }
-  return fmaxf(pairs * scale2, single);
+  return fmaxf(pairs * rest2, single);
 }
 
 template <typename T, int VW, bool INTER, int THREADS>
@@ -247,7 +252,6 @@ __device__ __forceinline__ void kv_part(const Append8Params& P, float2* s_turn) 
     if (lane == 0 && any) atomicOr(P.status, any);
   }
   __syncthreads();
-  const float scale2 = P.scale * P.scale;
 #pragma unroll 1
   for (int x = 0; x < s_runs; ++x) {
     const Run run = s_run[x];
@@ -284,13 +288,13 @@ __device__ __forceinline__ void kv_part(const Append8Params& P, float2* s_turn) 
 #pragma unroll
       for (int k = 0; k < kHold; ++k) {
         const int e = lane + 32 * k;
-        if (e < tasks) m2 = fmaxf(m2, squares<T, VW, INTER>(held[k], place_of<VW, INTER>(e % per, keys, P.rot), scale2));
+        if (e < tasks) m2 = fmaxf(m2, squares<T, VW, INTER>(held[k], place_of<VW, INTER>(e % per, keys, P.rot), P.power, P.rest2));
       }
 #pragma unroll 1
       for (int e = lane + 32 * kHold; e < tasks; e += 32) {
         const int r = e / per;
         const Place p = place_of<VW, INTER>(e - r * per, keys, P.rot);
-        m2 = fmaxf(m2, squares<T, VW, INTER>(fetch<VW>(src + r * row_bytes, p), p, scale2));
+        m2 = fmaxf(m2, squares<T, VW, INTER>(fetch<VW>(src + r * row_bytes, p), p, P.power, P.rest2));
       }
       m2 = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m2)));
       float s = __uint_as_float((unsigned int)(exponent_of(m2) + 127) << 23);
@@ -544,6 +548,9 @@ extern "C" int spec_verify_kv_append_e4m3(
   P.positions = positions;
   P.offset = position_offset;
   P.scale = rope_scale;
+  int e = std::ilogb(rope_scale);
+  P.power = std::ldexp(1.f, e < -126 ? -126 : e);
+  P.rest2 = (rope_scale / P.power) * (rope_scale / P.power);
   P.status = static_cast<unsigned int*>(workspace);
   // vectors of 8 values where every head's start and both halves of a rotation allow it
   bool wide = rot_dim % 16 == 0;
