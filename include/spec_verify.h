@@ -396,7 +396,10 @@ typedef struct {
  * are then rescaled (rounded to nearest), exact but for values below 2^-6 s.  Codes are
  * rounded to nearest, ties to even; values beyond 448 s, infinities too, become 448 s, NaN stays
  * NaN (and counts for nothing in m).  A scale stays as large as rejected rows made it while
- * its block holds older tokens.
+ * its block holds older tokens, and their codes have lost for good what it cost: an infinity
+ * (m counts it, s is 2^56) or a huge value takes all their bits, also in a row that is
+ * rejected.  A program whose model can produce one looks at its rows before the append,
+ * or has blocks of 1 token, where no row touches another's.
  * A block's older tokens belong to the request that appends (as its page does).  The
  * other arguments, statuses, errors and ownership: as spec_verify_kv_append; a block
  * whose older tokens have a scale outside the range keeps their codes, and its scale is
