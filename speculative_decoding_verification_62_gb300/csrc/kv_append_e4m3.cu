@@ -470,13 +470,21 @@ int launch_threads(Append8Params P, cudaStream_t stream) {
   return sv::code_of(cudaLaunchKernelEx(&cfg, append8_kernel<T, VW, INTER, THREADS>, P));
 }
 
+// us a call (32 / 8 heads of 128, bf16; the calls of a graph):
+// - a CTA looks for runs among one row while CTAs are few, and up to 16: 17.9 with one, 26.2 with 4 (1200
+//   rows); 115 with one, 106 with 4 and with 16 (20000); 4 / 1 heads of 64: 34.8, 23.2, 20.6 (20000)
+// - 256 threads while CTAs are few, and longer where a run has heads for 8 warps: 5.5 against 8.3 with 128
+//   (1 row), 12.9 / 16.6 (800), 19.6 / 27.2 (2048), 30.9 / 40.4 (5000), 111 / 106 (20000); 16 / 4 heads 18.8 / 20.8
+//   (5000), 28.7 / 25.8 (8000); 4 / 1 heads of 64: 4.9 / 5.0 (256), 6.3 / 5.4 (800)
+// - two rows of q a CTA from 2048 on: 20.5 against 32.1 with one (4 / 1 heads of 64, 20000), 22.2 / 25.7 (24 / 6
+//   of 96, 5000), no difference with 32 / 8 heads; below, 6.9 / 6.8 (64 rows), 6.4 / 7.1 for one (8 / 1 heads, 800)
 template <typename T, int VW, bool INTER>
 int launch(Append8Params& P, cudaStream_t stream) {
   const int rows = (P.T + kSlots - 1) / kSlots;
   P.run_rows = rows < kMaxRuns ? rows : kMaxRuns;
   P.kv_ctas = (P.T + P.run_rows - 1) / P.run_rows;
   P.q_rows = P.T < 2048 ? 1 : 2;
-  if (P.T < 608) return launch_threads<T, VW, INTER, 256>(P, stream);
+  if (P.T < 608 || (P.Hk >= 4 && P.T < 6144)) return launch_threads<T, VW, INTER, 256>(P, stream);
   return launch_threads<T, VW, INTER, 128>(P, stream);
 }
 

@@ -586,7 +586,10 @@ int spec_verify_pages_step(const sv_kv_cache* cache, const sv_kv_scales* scales,
   P.parents = parents;
   P.tokens = tokens;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int cluster = (long long)P.B * P.W > 4096 ? kCluster : 1;
+  // Rows for more warps than a CTA has: us a call with one CTA and with eight, no forks and forks of four: 36
+  // rows of 16 pages 11.6 / 10.5, 17.4 / 15.1; 64 of 64 13.5 / 12.4, 23.2 / 19.0; 256 of 64 35 / 14, 71 / 22.  Up to
+  // 32 rows a CTA has a warp for each: 8 of 64 8.3 / 10.8, 12.7 / 16.0; 32 of 1000 9.2 / 10.9, 72 / 79.
+  const int cluster = P.B > kWarps ? kCluster : 1;
   rc = launch(step_kernel, P, dim3(cluster), kThreads, cluster, s);
   if (rc) return rc;
   return launch(copy_kernel, P, dim3(P.B < 4096 ? P.B : 4096, 8), kCopyThreads, 1, s);
@@ -601,9 +604,12 @@ int spec_verify_pages_compact(const sv_kv_cache* cache, const sv_kv_scales* scal
   if (!sv::aligned(remap, 4)) return SV_ERR_ALIGN;
   P.remap = remap;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int cluster = P.num_pages > 4096 ? kCluster : 1;
+  // us with one CTA and with eight: 6.0 / 8.0 (388 pages), 9.2 / 10.3 (1988), 11.4 / 10.9 (2521), 13.9 / 11.6
+  // (3992), 23 / 14.5 (8000), 96 / 46 (40000)
+  const int cluster = P.num_pages > 2 * kThreads ? kCluster : 1;
   rc = launch(plan_kernel, P, dim3(cluster), kThreads, cluster, s);
   if (rc) return rc;
+  // (eight CTAs an SM fill it; moves of 700 pages of 256 KB take 73 us with one, 60 with two, 60 with eight)
   P.parts = (int)(((long long)P.page_size * P.Hk * P.row_bytes + kPart - 1) / kPart);
   const long long tasks = 2ll * P.num_pages * P.parts > P.B / 8 ? 2ll * P.num_pages * P.parts : P.B / 8 + 1;
   return launch(compact_kernel, P, dim3((unsigned int)(tasks < 152 * 8 ? tasks : 152 * 8)), kCopyThreads, 1, s);

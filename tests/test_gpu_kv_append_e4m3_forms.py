@@ -18,3 +18,12 @@ def test_a_rotations_factor_against_the_values(size, rope_scale, rot, interleave
     w = Step([9, 40, 0], [5, 20, 3], 4, 2, 64, 32, 16, "bf16", size=size)
     freq = rope.frequencies(rot)
     w.check(w.run(freq, rope_scale=rope_scale, interleaved=interleaved), freq, interleaved, rope_scale=rope_scale)
+
+
+@pytest.mark.parametrize("rows", [607, 608, 2047, 2048, 6143, 6144])
+@pytest.mark.parametrize("D, rot, inter, Hk", [(128, 128, False, 4), (64, 32, True, 9), (48, 20, False, 5)])
+def test_around_the_borders_of_the_forms_with_many_heads(rows, D, rot, inter, Hk):
+    lens, gam = [5] * 25 + [70] + [31] * 25, [3] * 25 + [rows - 201] + [3] * 25
+    w = Step(lens, gam, 2 * Hk, Hk, D, 32, 16, "bf16", seed=9)
+    freq = rope.frequencies(rot, 10000.0)
+    w.check(w.run(freq, interleaved=inter), freq, inter)

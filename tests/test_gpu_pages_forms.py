@@ -133,3 +133,17 @@ def test_a_prefix_moves_without_rows(kind):
     # a step of no rows does nothing
     binding.spec_verify_pages_step(empty, pool, ints([]))
     assert int(pool.free_count) == 25
+
+
+@pytest.mark.parametrize("B, pages", [(31, 2048), (32, 2049), (33, 2500), (64, 600)])
+def test_around_the_borders_of_the_forms(B, pages):
+    """One CTA or a cluster: 32 rows and one more, 2048 pages and one more."""
+    rng = random.Random(B)
+    w = Pool(B, 8, pages, heads=1, D=8)
+    w.step([rng.randint(0, 100) for _ in range(B)])
+    w.set_len([rng.randint(0, h * 16) for h in w.model.held])
+    for turn in range(3):
+        parents = [rng.choice([b, b, rng.randrange(B), -1]) for b in range(B)]
+        tokens = [0 if p < 0 else rng.randint(0, 128 - w.model.kv[p]) for p in parents]
+        w.step(tokens, parents)
+        w.compact()
