@@ -400,7 +400,8 @@ typedef struct {
  * (m counts it, s is 2^56) or a huge value takes all their bits, also in a row that is
  * rejected.  A program whose model can produce one looks at its rows before the append,
  * or has blocks of 1 token, where no row touches another's.
- * A block's older tokens belong to the request that appends (as its page does).  The
+ * A block's older tokens belong to the request that appends (as its page does).  A call has
+ * at most 2^31 - 4097 rows.  The
  * other arguments, statuses, errors and ownership: as spec_verify_kv_append; a block
  * whose older tokens have a scale outside the range keeps their codes, and its scale is
  * the new rows' (SV_STATUS_BAD_SCALE).

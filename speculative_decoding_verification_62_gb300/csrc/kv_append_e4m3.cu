@@ -30,6 +30,7 @@ using namespace sv::append;
 constexpr int kHold = 4;      // tasks of a lane that stay in registers: 16 rows of 128 values
 constexpr int kMaxRuns = 16;  // rows a CTA looks for runs among
 constexpr int kSlots = 1216;  // CTAs of a wave: eight an SM
+constexpr int kMaxRows = INT32_MAX - 4096;  // so that sums of a row and a CTA's or a wave's fit 32 bits
 
 struct Append8Params {
   const char* q;
@@ -502,7 +503,7 @@ extern "C" int spec_verify_kv_append_e4m3(
   if (rc) return rc;
   if ((dtype != SV_BF16 && dtype != SV_F16) || total_drafts < 0 || max_drafts < 0 || q_heads < 0 || rot_dim < 0 ||
       rot_dim % 2 || rot_dim > c.head_dim || (interleaved != 0 && interleaved != 1) || !(rope_scale > 0.f) ||
-      rope_scale > 3.0e38f || (long long)total_drafts + c.batch > INT32_MAX)
+      rope_scale > 3.0e38f || (long long)total_drafts + c.batch > kMaxRows)
     return SV_ERR_SCALAR;
   if (!k || !v || !cu_draft || !workspace || (rot_dim > 0 && !freq)) return SV_ERR_NULL;
   if (q_heads > 0 && (!q || !q_out || !q_strides || !q_out_strides)) return SV_ERR_NULL;

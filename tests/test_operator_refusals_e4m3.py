@@ -99,8 +99,9 @@ def test_bad_caches_and_scales(call):
 def test_append_refusals():
     for bad in (dict(dtype=0), dict(dtype=3), dict(total=-1), dict(G=-1), dict(heads=-1), dict(rot=63), dict(rot=66),
                 dict(rot=-2), dict(inter=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf),
-                dict(total=2 ** 31 - 2)):
+                dict(total=2 ** 31 - 2), dict(total=2 ** 31 - 1000), dict(total=2 ** 31 - 4099)):
         assert append(**bad) == -1, bad
+    assert append(total=2 ** 31 - 4100, ws_bytes=2) == -4  # (the most goes on to the next check)
     for name in ("q", "qs", "k", "ks", "v", "vs", "o", "os", "cu", "freq", "ws"):
         assert append(**{name: None}) == -2, name
     lib = binding.load_library()
