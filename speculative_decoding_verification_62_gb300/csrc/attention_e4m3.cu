@@ -15,7 +15,8 @@
 //   then, 2^-7 of the weight's power of two at most and a multiple of 2^-10 of it, is an e5m2: the sum is
 //   the fp16, off by 2^-11 of the weight at most.  (With the first two cut off instead of rounded,
 //   three terms hold nine of its eleven bits.)  The maximum of the weights lies in [2^13, 2^15] at all times
-//   after its tile, so that e5m2's smallest step, 2^-16, is 2^-29 of it.
+//   after its tile, so that e5m2's smallest step, 2^-16, is 2^-29 of it.  (Of scores near 2^27 it lies in
+//   [2^-3, 2^15]: the maximum itself is a multiple of 16 there.)
 // Each product is two or three products of kind::f8f6f4, into one 32-bit accumulator.
 //
 // Work: a unit is (request, up to kN rows of queries, key head) over the request's own keys, or
@@ -30,11 +31,12 @@
 // swizzle).  The next tile's scores are formed beside this one's softmax; a CTA's
 // waits are filled by the other of its SM.
 //
-// Bound: the codes, read once (one request of 131000 tokens, 8 key heads of 128: 270 MB).  Measured far from it:
-// that request takes 137 us (39.5 at the copy rate), 256 requests of up to 5000 tokens 598 (197), at 36 % and (64 of
-// them) 25 % of the issue slots and 15 % and 6 % of the tensor pipe: a tile's steps, scores, weights, moves of the maximum, wait
-// for one another.  The list counts a tile as one whatever its columns: behind a prefix (64 columns a tile
-// beside 16) the busiest SM works 1.6 times as long as the average.
+// Bound: the codes, read once (one request of 131000 tokens, 8 key heads of 128: 268 MB).
+// Measured far from it: that request takes 137 us (39.5 at the copy rate), 256 requests of up to
+// 5000 tokens 598 (197), at 36 % and (64 of them) 25 % of the issue slots and 15 % and 6 % of the
+// tensor pipe: a tile's steps, scores, weights, moves of the maximum, wait for one another.
+// The list counts a tile as one whatever its columns: behind a prefix (64 columns a tile beside
+// 16) the busiest SM works 1.6 times as long as the average.
 #include "../../include/spec_verify.h"
 #include "internal.h"
 

@@ -16,10 +16,11 @@
 //
 // Bound: q, k and v are read once and written once, k and v in half the bytes.  A warp
 // takes one head's keys or values of a run: its first 16 rows stay in registers between
-// the maximum and the codes (a longer run's others are read twice).  Rows of q are turned by CTAs of their own
-// beside them.  Measured (24 / 6 heads of 96, 23000 prompt rows in fp16, 43 us at the copy rate): 73 us in blocks of 16
-// tokens, 147 in blocks of 128.  A verify step of 1150 rows (32 / 8 heads of 128) takes 13.8 us (3.9), its look-ups one
-// after another; rotations of other widths than a multiple of 16, or rows that are not 16-byte aligned, go value by value: 40 of 80
+// the maximum and the codes (a longer run's others are read twice).  Rows of q are turned by CTAs
+// of their own beside them.  Measured (24 / 6 heads of 96, 23000 prompt rows in fp16, 43 us at
+// the copy rate): 73 us in blocks of 16 tokens, 147 in blocks of 128.  A verify step of 1150 rows
+// (32 / 8 heads of 128) takes 13.8 us (3.9), its look-ups one after another.  A rotation of a
+// width that is no multiple of 16, or rows that are not 16-byte aligned, go value by value: 40 of 80
 // values 21 us for such a step.
 #include "../../include/spec_verify.h"
 #include "append.h"

@@ -10,8 +10,9 @@
 // the rows in order.
 //
 // Bound: the table's entries of the rows that change, two dependent reads each; then the copied tokens
-// (read and written once).  Measured: 256 rows, forks of four, contexts of up to 20000 tokens in pages of 64, 48 us, nearly all
-// of it the cluster's (its CTAs read every entry of a changed row up to five times; 8 SMs work); without forks 16.
+// (read and written once).  Measured: 256 rows, forks of four, contexts of up to 20000 tokens in
+// pages of 64, 48 us, nearly all of it the cluster's (its CTAs read every entry of a changed
+// row up to five times; 8 SMs work); without forks 16.
 // A compaction that moves 1440 pages of 256 KB takes 125 us, 89 % of the copy rate.
 #include "../../include/spec_verify.h"
 #include "internal.h"
